@@ -28,7 +28,8 @@ EXPORTED = ("moe_experts_create", "moe_experts_set_hash_table", "moe_workspace_s
             "moe_testing_stall_loads", "moe_set_stage_events", "moe_route_noalloc", "moe_measure_mxf8f6f4_peak",
             "moe_stack_create", "moe_stack_forward", "moe_stack_destroy", "moe_mx_blocks_unpack",
             "moe_experts_set_activation_format", "moe_measure_mxf4_peak", "moe_testing_read_h",
-            "moe_experts_set_router", "moe_testing_read_y32", "moe_testing_set_pair_gemm")
+            "moe_experts_set_router", "moe_testing_read_y32", "moe_testing_set_pair_gemm", "moe_add_rms_norm",
+            "moe_kv_append", "moe_paged_attention", "moe_paged_attention_workspace")
 
 MOE_MX_NIBBLES_PAIRED, MOE_MX_NIBBLES_SPLIT = 0, 1
 MOE_ACT_MXFP8, MOE_ACT_MXFP4 = 0, 1
@@ -52,6 +53,26 @@ class moe_config_t(ctypes.Structure):
 class moe_stack_layer_t(ctypes.Structure):
     _fields_ = [("experts", ctypes.c_void_p), ("shared", ctypes.c_void_p), ("router_w", ctypes.c_void_p),
                 ("router_bias", ctypes.c_void_p)]
+
+
+class moe_norm_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("x", "residual", "weight", "sum", "y", "y_q", "y_s")] +
+                [(n, ctypes.c_int64) for n in ("x_stride", "residual_stride", "sum_stride", "y_stride")] +
+                [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("weight_f32", ctypes.c_int32), ("eps", ctypes.c_float)])
+
+
+class moe_kv_cache_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v", "k_s", "v_s", "block_table", "seq_lens", "status")] +
+                [(n, ctypes.c_int64) for n in ("page_stride", "row_stride", "head_stride")] +
+                [(n, ctypes.c_int32) for n in ("format", "n_pages", "page_size", "n_kv_heads", "head_dim", "n_seqs",
+                                               "max_pages")])
+
+
+class moe_attention_t(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("q_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("n_q_heads", ctypes.c_int32), ("L", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 class moe_input_t(ctypes.Structure):
@@ -93,6 +114,12 @@ def lib() -> ctypes.CDLL:
         L.moe_stack_forward.argtypes = [vp, inp, vp, vp, vp]
         L.moe_stack_destroy.argtypes = [vp]
         L.moe_mx_blocks_unpack.argtypes = [vp, ctypes.c_int64, i32, vp, vp, vp]
+        L.moe_add_rms_norm.argtypes = [ctypes.POINTER(moe_norm_t), vp]
+        cachep = ctypes.POINTER(moe_kv_cache_t)
+        L.moe_kv_append.argtypes = [cachep, vp, ctypes.c_int64, vp, ctypes.c_int64, i32, vp]
+        L.moe_paged_attention.argtypes = [cachep, ctypes.POINTER(moe_attention_t), vp]
+        L.moe_paged_attention_workspace.argtypes = [cachep, i32, i32]
+        L.moe_paged_attention_workspace.restype = ctypes.c_size_t
         L.moe_stack_destroy.restype = None
         L.moe_experts_destroy.argtypes = [vp]
         L.moe_experts_destroy.restype = None
@@ -101,7 +128,7 @@ def lib() -> ctypes.CDLL:
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = ctypes.c_char_p
         for name in EXPORTED:
-            if name not in ("moe_workspace_size", "moe_experts_destroy", "moe_status_string", "moe_last_error",
+            if name not in ("moe_workspace_size", "moe_paged_attention_workspace", "moe_experts_destroy", "moe_status_string", "moe_last_error",
                             "moe_stack_destroy"):
                 getattr(L, name).restype = st
         _LIB = L
@@ -506,3 +533,6 @@ class MoEStack:
             self.close()
         except Exception:
             pass
+
+
+from .decode import PagedKVCache, moe_add_rms_norm  # noqa: E402  (needs the names above)

@@ -1,0 +1,180 @@
+"""The decode-step operators around the MoE layer (``include/moe_decode.h``): the residual addition with its
+root-mean-square norm, and the paged key-value cache with the attention that reads it.
+
+Like the rest of the binding these only check and marshal arguments; every step runs in the library's
+kernels, asynchronously on the given stream (default: the current one).
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from . import (MOE_OK, MoEError, _ok, _stream, lib, moe_attention_t, moe_kv_cache_t, moe_norm_t)
+
+MOE_KV_BF16, MOE_KV_MXFP8 = 0, 1
+KV_STATUS = {1: "a sequence length outside the block table", 2: "a page index outside the cache"}
+
+
+def _rows(t: torch.Tensor | None, name: str, shape, dtype=torch.bfloat16) -> int | None:
+    """Address of a row-strided 2-D tensor with contiguous columns."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the columns of {name} must be contiguous")
+    return t.data_ptr()
+
+
+def moe_add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None, weight: torch.Tensor, eps: float = 1e-6,
+                     sum_out: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                     y_q: torch.Tensor | None = None, y_s: torch.Tensor | None = None, stream=None) -> None:
+    """sum_out = bf16(x + residual); y = bf16((x + residual) * weight / rms); (y_q, y_s) = MXFP8(y).
+
+    x, residual, sum_out, y: bf16 [T, d] (row-strided views allowed); weight: bf16 or fp32 [d]; y_q: uint8
+    [T, d] E4M3 codes and y_s: uint8 [T, d / 32] E8M0 bytes, contiguous, as ``moe_permute`` writes them.
+    residual and each output may be None; sum_out may be x or residual, y may be x."""
+    T, d = x.shape
+    if weight.dtype not in (torch.bfloat16, torch.float32) or weight.shape != (d,) or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous bf16 or fp32 tensor of {d} columns")
+    a = moe_norm_t(_rows(x, "x", (T, d)), _rows(residual, "residual", (T, d)), weight.data_ptr(),
+                   _rows(sum_out, "sum_out", (T, d)), _rows(y, "y", (T, d)),
+                   _rows(y_q, "y_q", (T, d), torch.uint8), _rows(y_s, "y_s", (T, d // 32), torch.uint8))
+    for t, name in ((y_q, "y_q"), (y_s, "y_s")):
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if T > 1:  # the stride of a lone row means nothing
+        a.x_stride = x.stride(0)
+        a.residual_stride = 0 if residual is None else residual.stride(0)
+        a.sum_stride = 0 if sum_out is None else sum_out.stride(0)
+        a.y_stride = 0 if y is None else y.stride(0)
+    a.T, a.d, a.weight_f32, a.eps = T, d, weight.dtype == torch.float32, eps
+    _ok("moe_add_rms_norm", lib().moe_add_rms_norm(ctypes.byref(a), _stream(stream)))
+
+
+class PagedKVCache:
+    """One layer's paged key-value cache over the caller's tensors.
+
+    k, v: [n_pages, page_size, n_kv_heads, head_dim], bf16, or uint8 E4M3 codes (MXFP8) with k_scales,
+    v_scales uint8 [..., head_dim / 32]; any strides with contiguous columns, the same for k and v.
+    block_table: int32 [n_seqs, max_pages], contiguous; seq_lens: int32 [n_seqs], the tokens of every request
+    including the ones of the current step.  Their contents may change between calls (in place).
+
+    ``append`` writes a step's new keys and values; ``attend`` is the attention of the step's new tokens."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                 k_scales: torch.Tensor | None = None, v_scales: torch.Tensor | None = None):
+        mx = k_scales is not None
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must be alike: [n_pages, page_size, n_kv_heads, head_dim], columns contiguous")
+        if k.dtype != (torch.uint8 if mx else torch.bfloat16) or v.dtype != k.dtype:
+            raise ValueError("k and v must be bf16, or uint8 E4M3 codes with k_scales and v_scales")
+        if mx != (v_scales is not None):
+            raise ValueError("k_scales and v_scales go together")
+        n_pages, page, heads, d = k.shape
+        if mx:
+            for s in (k_scales, v_scales):
+                if s.dtype != torch.uint8 or s.shape != (n_pages, page, heads, d // 32) or s.stride(3) != 1:
+                    raise ValueError("scales must be uint8 [n_pages, page_size, n_kv_heads, head_dim / 32]")
+                if any(n > 1 and 32 * a != b for n, a, b in zip(s.shape[:3], s.stride(), k.stride())):
+                    raise ValueError("the scales' strides must be those of k and v divided by 32")
+        if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
+            raise ValueError("block_table must be a contiguous int32 [n_seqs, max_pages]")
+        if seq_lens.dtype != torch.int32 or seq_lens.shape != block_table.shape[:1] or not seq_lens.is_contiguous():
+            raise ValueError("seq_lens must be a contiguous int32 [n_seqs]")
+        tensors = [t for t in (k, v, block_table, seq_lens, k_scales, v_scales) if t is not None]
+        if len({t.device for t in tensors}) != 1 or not k.is_cuda:
+            raise ValueError("the cache's tensors must be on one CUDA device")
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.block_table, self.seq_lens = block_table, seq_lens
+        self.device, self.n_seqs, self.n_kv_heads, self.head_dim = k.device, seq_lens.shape[0], heads, d
+        self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        st = [s if n > 1 else 0 for n, s in zip(k.shape[:3], k.stride())]  # strides of lone entries mean nothing
+        self._c = moe_kv_cache_t(k.data_ptr(), v.data_ptr(), k_scales.data_ptr() if mx else None,
+                                 v_scales.data_ptr() if mx else None, block_table.data_ptr(), seq_lens.data_ptr(),
+                                 self.status.data_ptr(), *st, MOE_KV_MXFP8 if mx else MOE_KV_BF16, n_pages, page,
+                                 heads, d, self.n_seqs, block_table.shape[1])
+        self._ref = ctypes.byref(self._c)
+        self._workspaces = {}
+
+    @classmethod
+    def allocate(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, block_table: torch.Tensor,
+                 seq_lens: torch.Tensor, fmt: str = "bf16") -> "PagedKVCache":
+        """A cache with zeroed pages of its own on the block table's device; fmt: "bf16" or "mxfp8"."""
+        if fmt not in ("bf16", "mxfp8"):
+            raise ValueError(f"unknown cache format {fmt!r}")
+        shape, dev = (n_pages, page_size, n_kv_heads, head_dim), block_table.device
+        if fmt == "bf16":
+            return cls(*(torch.zeros(shape, dtype=torch.bfloat16, device=dev) for _ in "kv"), block_table, seq_lens)
+        k, v = (torch.zeros(shape, dtype=torch.uint8, device=dev) for _ in "kv")
+        ks, vs = (torch.zeros((*shape[:3], head_dim // 32), dtype=torch.uint8, device=dev) for _ in "kv")
+        return cls(k, v, block_table, seq_lens, ks, vs)
+
+    def _step_rows(self, t: torch.Tensor, name: str, heads: int | None = None, dtype=torch.bfloat16):
+        """(L, heads, row stride) of [n_seqs, L, heads, head_dim] whose rows (b, l) lie at one stride."""
+        if t.dim() != 4 or t.dtype != dtype or t.device != self.device or t.shape[0] != self.n_seqs or \
+                t.shape[3] != self.head_dim or (heads is not None and t.shape[2] != heads):
+            raise ValueError(f"{name} must be {dtype} [{self.n_seqs}, L, {heads or 'heads'}, {self.head_dim}] on "
+                             f"{self.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+        B, L, h, d = t.shape
+        sb, sl, sh, sd = t.stride()
+        if sd != 1 or (h > 1 and sh != d) or (B > 1 and L > 1 and sb != L * sl):
+            raise ValueError(f"{name}: heads must be contiguous and the rows (request, token) at one stride")
+        return L, h, 0 if B * L <= 1 else (sl if L > 1 else sb)
+
+    def append(self, k_new: torch.Tensor, v_new: torch.Tensor, stream=None) -> None:
+        """Write the step's L new tokens: bf16 [n_seqs, L, n_kv_heads, head_dim], token l of request b at
+        position seq_lens[b] - L + l (negative positions are skipped)."""
+        L, _, ks = self._step_rows(k_new, "k_new", self.n_kv_heads)
+        Lv, _, vs = self._step_rows(v_new, "v_new", self.n_kv_heads)
+        if L != Lv:
+            raise ValueError("k_new and v_new hold different numbers of tokens")
+        _ok("moe_kv_append", lib().moe_kv_append(self._ref, k_new.data_ptr(), ks, v_new.data_ptr(), vs, L,
+                                                 _stream(stream)))
+
+    def workspace(self, n_q_heads: int, L: int, stream) -> torch.Tensor:
+        """The attention's workspace for calls on this stream, made (zeroed, on that stream) at first use."""
+        key = (n_q_heads, L, stream.cuda_stream)
+        ws = self._workspaces.get(key)
+        if ws is None:
+            n = int(lib().moe_paged_attention_workspace(self._ref, n_q_heads, L))
+            if n == 0:
+                raise MoEError("moe_paged_attention_workspace", 1, lib().moe_last_error().decode())
+            with torch.cuda.stream(stream):
+                ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
+            self._workspaces[key] = ws
+        return ws
+
+    def attend(self, q: torch.Tensor, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+               scale: float | None = None, stream=None) -> torch.Tensor:
+        """Attention of the L newest tokens of every request: q, out bf16 [n_seqs, L, n_q_heads, head_dim]; lse
+        fp32 [n_seqs, L, n_q_heads] or None; scale defaults to head_dim ** -0.5.  Row l sees the positions below
+        seq_lens[b] - L + 1 + l; a row that sees nothing gives 0 (lse -inf)."""
+        L, heads, qs = self._step_rows(q, "q")
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        Lo, _, os_ = self._step_rows(out, "out", heads)
+        if Lo != L:
+            raise ValueError("q and out hold different numbers of tokens")
+        if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:3] or not lse.is_contiguous() or
+                                lse.device != self.device):
+            raise ValueError(f"lse must be a contiguous fp32 tensor of shape {tuple(q.shape[:3])}")
+        if q.numel() == 0:
+            return out
+        stream = torch.cuda.current_stream(self.device) if stream is None else stream
+        ws = self.workspace(heads, L, stream)
+        a = moe_attention_t(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(),
+                            ws.numel(), qs, os_, heads, L,
+                            1.0 / math.sqrt(self.head_dim) if scale is None else scale)
+        _ok("moe_paged_attention", lib().moe_paged_attention(self._ref, ctypes.byref(a), _stream(stream)))
+        return out
+
+    def check(self) -> None:
+        """Wait for the device, then raise if a call met a bad length or page since the last check."""
+        bits = int(self.status.item())
+        if bits != MOE_OK:
+            self.status.zero_()
+            raise MoEError("PagedKVCache", 5, "; ".join(t for b, t in KV_STATUS.items() if bits & b))
