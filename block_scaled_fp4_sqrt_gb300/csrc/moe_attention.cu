@@ -5,30 +5,34 @@
 // The cache is read once, so a step's few rows a key-value head (heads of the group x L) leave it memory-bound.
 // Layout of the work:
 //  * A unit is (request, kv head, row tile): the rows r = l * group + j of the query heads that share the kv head,
-//    16 MT WM of them at a time.  Every unit is cut into tiles of 64 tokens; the tiles of all units, in order, are
+//    16 MT of them at a time.  Every unit is cut into tiles of 64 tokens; the tiles of all units, in order, are
 //    dealt to the grid in equal contiguous runs, computed by every block from the lengths alone.  A long request is
 //    thus spread over the GPU and short ones share a block, whatever the mix of lengths.
-//  * A block is 4 WM warps: each warp owns 16 of a tile's 64 tokens and (WM = 2) half of the rows.  With WM = 1 a
-//    warp loads its own tokens (cp.async, a ring of stages) and no barrier of the block is in the loop.
-//  * A warp keeps the running maximum and sum of its rows over its own tokens; the four token groups are joined
-//    in shared memory at a unit's end, and a unit that several blocks share is joined, in block order, by the last
-//    of them to arrive (a counter per unit, zero between calls).
+//  * A block is four warps.  For a tile each warp fetches 16 tokens (cp.async, a ring of stages), computes the
+//    scores of these 16 tokens for all rows, and leaves p in shared memory; after a barrier each warp accumulates
+//    a quarter of the columns over all 64 tokens.  The accumulators then take 16 MT D / 128 / 4 registers a thread
+//    instead of four times that, quantised values are unpacked once a block, and a unit's end needs no exchange.
+//  * The running maximum of a row moves only when a score exceeds it by more than 2^8 (a vote in the barrier that
+//    publishes p): p stays below 256, which costs no precision, and accumulators are rescaled rarely.
+//  * A unit that several blocks share is joined, in block order, by the last of them to arrive (a counter per unit,
+//    zero between calls); more than 16 parts in two steps, of which the first runs in many blocks at once.
 //
 // Products run on mma.sync: with at most 64 rows to a kv head a 128-row tcgen05 tile would be mostly padding, its
 // accumulator would have to cross tensor memory for every softmax step, and quantised operands could not be
-// unpacked in registers.  Measured rates: bf16 m16n8k16 605 TFLOP/s, E4M3 m16n8k32 2.28 PFLOP/s.
+// unpacked in registers.  Measured rate of the 16-bit forms (m16n8k16): 605 TFLOP/s.
 //  * bf16 cache: both products in bf16 with fp32 accumulation.  p is rounded to bf16 (8 bits, as the output is);
 //    its sum is taken before that rounding.
-//  * MXFP8 cache, scores: the E4M3 codes of K enter the tensor cores as they are.  q (8 significant bits) is split
-//    exactly into two E4M3 terms of 4 bits each after scaling its row by a power of two (elements below 2^-9 of
-//    the row's maximum lose bits: an error under 2^-17 of that maximum); a block's E8M0 scale multiplies the fp32
-//    product of its 32 columns.  Two E4M3 instructions replace the unpacking of K and two bf16 ones.
+//  * MXFP8 cache, scores: E4M3 codes become fp16 (exact, one conversion a pair) and meet q in fp16, its row scaled by
+//    a power of two to a maximum in [2^14, 2^15): bf16's 8 bits are kept down to 2^-28 of the maximum.  A block's
+//    E8M0 scale multiplies the fp32 product of its 32 columns.  (mma.sync on E4M3 operands runs the same fp16
+//    instructions here, after conversions of both operands: 690 instead of 200 instructions a tile and warp.)
 //  * MXFP8 cache, values: E4M3 codes become bf16 by moving bits (value times 2^-120) and one packed multiplication
 //    by the block's scale times 2^120; every product of a code and a power of two is exact in bf16.
 #include <float.h>
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "moe_decode_device.cuh"
 
@@ -37,8 +41,12 @@ namespace moe {
 namespace {
 
 constexpr int kTile = 64;      // tokens of a tile
-constexpr int kWarpTok = 16;   // tokens of a tile that a warp owns
-constexpr int kTokWarps = 4;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kWarpTok = kTile / kWarps;  // tokens of a tile that a warp fetches and scores
+constexpr int kPPitch = kTile * 2 + 16;   // bytes of a row of p: eight rows fall on distinct banks
+constexpr int kJoin = 16;                 // parts that are joined in one step
+constexpr float kGrow = 8.f;              // log2 units by which a score may exceed the running maximum
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -53,6 +61,8 @@ struct AttnParams {
   PageDiv pd;
   int* counters;    // [n_seqs * kv heads * row_tiles], zero between calls
   float* partial;   // [grid][2][rows of a tile][head_dim + 2]
+  int* group_counters;   // [grid / kJoin + 1][2], zero between calls
+  float* group_partial;  // [grid / kJoin + 1][2][rows of a tile][head_dim + 2]
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
@@ -87,10 +97,31 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// d = a b (no accumulator to clear first)
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Two E4M3 codes (the low or high half of r) as an fp16 pair, exact.
+__device__ __forceinline__ uint32_t e4m3_f16(uint32_t r, bool high) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(high ? r >> 16 : r)));
+  return h;
+}
+
+// (c0, c1) += (a0, a1) * (b0, b1)
+__device__ __forceinline__ void fma2(float& c0, float& c1, float a0, float a1, float b0, float b1) {
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%0, %1};\n"
+      " fma.rn.f32x2 c, a, b, c;\n mov.b64 {%0, %1}, c;\n}"
+      : "+f"(c0), "+f"(c1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -124,76 +155,78 @@ __device__ __forceinline__ float e8m0_float(uint32_t w, int j) {
   return __uint_as_float(j == 3 ? (w >> 1) & 0x7F800000u : (w << (23 - 8 * j)) & 0x7F800000u);
 }
 
-// Position in the sequence of all tiles: request b (length len, nt tiles), unit w = head * row_tiles + row tile of
-// the request, tile t of the unit.
+// Position in the sequence of all tiles: request b (length len, nt tiles a unit), kv head, row tile rt, tile t.
 struct Cursor {
-  int b, w, t, nt, len;
+  int b, head, rt, t, nt, len;
 };
 
-template <int D, bool MX, int MT, int WM>
+template <int D, bool MX, int MT>
 struct Cfg {
-  static constexpr int kWarps = kTokWarps * WM;
-  static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kRows = 16 * MT * WM;                 // rows of a row tile
+  static constexpr int kRows = 16 * MT;                      // rows of a row tile
   static constexpr int kRowBytes = MX ? D : 2 * D;           // one token of one head
   static constexpr int kScale = MX ? D / 32 : 0;             // scale bytes of a token
   static constexpr int kHalf = kTile * kRowBytes;            // K (or V) of a stage
   static constexpr int kStageBytes = 2 * kHalf + 2 * kTile * kScale;
-  static constexpr int kJoinStride = D + 8;                  // floats; 8 rows of a fragment fall on distinct banks
-  static constexpr int kJoinBytes = kRows * kJoinStride * 4; // the join's accumulator
-  static constexpr int kStatBytes = 2 * kTokWarps * kRows * 4 + 2 * kRows * 4;
-  // Blocks an SM holds: two where 16 or 32 rows leave registers for it, one with eight warps.
-  static constexpr int kBlocks = WM == 1 ? 2 : 1;
-  static constexpr int kBudget = (kBlocks == 2 ? 113 : 226) * 1024 - kJoinBytes - kStatBytes - 256;
+  static constexpr int kQPitch = 2 * D + 16;
+  static constexpr int kQBytes = kRows * kQPitch;
+  static constexpr int kPBytes = kRows * kPPitch;
+  static constexpr bool kQRegs = MT <= 2;                    // q fragments stay in registers
+  // p may take q's place once the fragments are in registers
+  static constexpr int kQPBytes = kQRegs ? (kQBytes > kPBytes ? kQBytes : kPBytes) : kQBytes + kPBytes;
+  static constexpr int kStatBytes = (2 * kWarps + 2) * kRows * 4;
+  // Blocks an SM holds: three, or two where a stage (32 KB) or the registers (64 rows) leave no room for more.
+  static constexpr int kBlocks = kStageBytes > 20 * 1024 || MT == 4 ? 2 : 3;
+  static constexpr int kBudget = (kBlocks == 2 ? 113 : 75) * 1024 - kQPBytes - kStatBytes - 256;
   static constexpr int kFit = kBudget / kStageBytes;
   static constexpr int kStages = kFit < 2 ? 2 : kFit > 6 ? 6 : kFit;
-  static constexpr int kSmem = kStages * kStageBytes + kJoinBytes + kStatBytes + 128;
+  static constexpr int kSmem = kStages * kStageBytes + kQPBytes + kStatBytes + 128;
 };
 
-template <int D, bool MX, int MT, int WM>
-__global__ void __launch_bounds__(Cfg<D, MX, MT, WM>::kThreads, Cfg<D, MX, MT, WM>::kBlocks)
-    paged_attention_kernel(const AttnParams p) {
-  using C = Cfg<D, MX, MT, WM>;
-  constexpr int kChunks = C::kRowBytes / 16;  // 16-byte pieces of a token row: 16, 8 or 4
-  constexpr int kNT = D / 8;                  // output column tiles
+template <int D, bool MX, int MT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_attention_kernel(const AttnParams p) {
+  using C = Cfg<D, MX, MT>;
+  constexpr int kChunks = C::kRowBytes / 16;   // 16-byte pieces of a token row: 16, 8 or 4
+  constexpr int kQ = D / 16;                   // steps of the scores' contraction
+  constexpr int kCols = D / kWarps;            // output columns of a warp: 32 or 16
+  constexpr int kNT = kCols / 8;               // 8-column tiles of a warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-  float* join = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);  // [kRows][kJoinStride]
-  float* s_m = join + C::kRows * C::kJoinStride;           // [token warp][row]
-  float* s_l = s_m + kTokWarps * C::kRows;    // [token warp][row]
-  float* s_M = s_l + kTokWarps * C::kRows;    // [row]
-  float* s_Z = s_M + C::kRows;                // [row]
+  uint8_t* s_q = smem + C::kStages * C::kStageBytes;          // q, bf16 or (MXFP8) fp16
+  uint8_t* s_p = C::kQRegs ? s_q : s_q + C::kQBytes;          // p of the current tile
+  float* s_mx = reinterpret_cast<float*>(s_q + C::kQPBytes);  // [warp][row]
+  float* s_l = s_mx + kWarps * C::kRows;                      // [warp][row]
+  float* s_f = s_l + kWarps * C::kRows;                       // [row] score factor
+  int* s_lim = reinterpret_cast<int*>(s_f + C::kRows);        // [row] first position the row does not see
   __shared__ int s_b, s_last;
-  __shared__ int64_t s_part[32];
+  __shared__ int64_t s_part[kWarps], s_first;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int wt = warp % kTokWarps, wm = warp / kTokWarps;  // token group, row half
   const int li = lane >> 2, lc = lane & 3;
+  const int mrow = lane & 7, mi = lane >> 3;  // this lane's row address in an ldmatrix of four 8 x 16-byte tiles
   pdl_trigger();
   pdl_wait();
 
   // ---- this block's run of tiles
-  const int B = p.c.n_seqs, HR = p.c.n_kv_heads * p.row_tiles;
+  const int B = p.c.n_seqs, H = p.c.n_kv_heads, HR = H * p.row_tiles;
   auto tiles_of = [](int len) { return len > 0 ? (len + kTile - 1) / kTile : 1; };
   int64_t sum = 0;
-  for (int b = tid; b < B; b += C::kThreads) sum += tiles_of(seq_len_of(p.c, b));
+  for (int b = tid; b < B; b += kThreads) sum += tiles_of(seq_len_of(p.c, b));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
   if (lane == 0) s_part[warp] = sum;
   __syncthreads();
   int64_t total = 0;
 #pragma unroll
-  for (int i = 0; i < C::kWarps; ++i) total += s_part[i];
+  for (int i = 0; i < kWarps; ++i) total += s_part[i];
   total *= HR;
   const int64_t per = (total + gridDim.x - 1) / gridDim.x;
   const int64_t t0 = per * blockIdx.x, t1 = t0 + per < total ? t0 + per : total;
   if (t0 >= t1) return;
   Cursor cur;
-  int64_t base;  // first tile of request cur.b
   {
     const int64_t want = t0 / HR;  // in tiles of one unit per request
     int64_t carry = 0;
-    for (int b0 = 0; b0 < B; b0 += C::kThreads) {
+    for (int b0 = 0; b0 < B; b0 += kThreads) {
       const int b = b0 + tid;
       const int n = b < B ? tiles_of(seq_len_of(p.c, b)) : 0;
       int64_t incl = n;
@@ -207,54 +240,54 @@ __global__ void __launch_bounds__(Cfg<D, MX, MT, WM>::kThreads, Cfg<D, MX, MT, W
       __syncthreads();
       int64_t before = carry;
 #pragma unroll
-      for (int i = 0; i < C::kWarps; ++i) {
+      for (int i = 0; i < kWarps; ++i) {
         if (i < warp) before += s_part[i];
         carry += s_part[i];
       }
       if (n > 0 && before + incl - n <= want && want < before + incl) {
         s_b = b;
-        s_part[31] = before + incl - n;
+        s_first = before + incl - n;
       }
       __syncthreads();
       if (want < carry) break;
     }
     cur.b = s_b;
-    base = s_part[31] * HR;
     cur.len = seq_len_of(p.c, cur.b);
     cur.nt = tiles_of(cur.len);
-    const int64_t off = t0 - base;
-    cur.w = (int)(off / cur.nt);
-    cur.t = (int)(off - (int64_t)cur.w * cur.nt);
+    const int64_t off = t0 - s_first * HR;
+    const int w = (int)(off / cur.nt);
+    cur.t = (int)(off - (int64_t)w * cur.nt);
+    cur.head = w / p.row_tiles;
+    cur.rt = w - cur.head * p.row_tiles;
   }
   auto advance = [&](Cursor& c) {
     if (++c.t < c.nt) return;
     c.t = 0;
-    if (++c.w < HR) return;
-    c.w = 0;
+    if (++c.rt < p.row_tiles) return;
+    c.rt = 0;
+    if (++c.head < H) return;
+    c.head = 0;
     if (++c.b < B) {
       c.len = seq_len_of(p.c, c.b);
       c.nt = tiles_of(c.len);
     }
   };
 
-  // ---- loading: with WM = 1 a warp fetches the 16 tokens it will read; with WM = 2 all warps share the 64
-  constexpr int kLoadWarps = WM == 1 ? 1 : C::kWarps;           // warps that share a set of tokens
-  constexpr int kLoadTok = WM == 1 ? kWarpTok : kTile;          // tokens in the set
-  constexpr int kTokPerWarp = kLoadTok / kLoadWarps;            // tokens one warp fetches: 16 or 8
-  const int tok_first = WM == 1 ? wt * kWarpTok : warp * kTokPerWarp;
+  // ---- loading: a warp fetches 16 tokens of a tile
   const uint32_t smem_base = smem_addr(smem);
+  const int tok_first = warp * kWarpTok;
   auto swz = [](int row, int chunk) {
     return (kChunks >= 8 ? (chunk ^ (row & 7)) : (chunk ^ ((row >> 1) & 3))) * 16;
   };
-  // page of this lane's token of the tile that will be loaded next (lanes 0..kTokPerWarp-1), or -1; looked up one
-  // tile ahead, so that the table's latency is not in front of the loads
+  // page of this lane's token (lanes 0..15) of the tile that will be loaded next, or -1; looked up one tile ahead,
+  // so that the table's latency is not in front of the loads
   Cursor ld = cur;
   int64_t ld_left = t1 - t0;
   int nxt_page = -1, nxt_row = 0;
   auto lookup = [&]() {
     nxt_page = -1;
     const int t = ld.t * kTile + tok_first + lane;
-    if (ld_left > 0 && lane < kTokPerWarp && t < ld.len) {
+    if (ld_left > 0 && lane < kWarpTok && t < ld.len) {
       const int j = page_of(t, p.pd, p.c.page_size, &nxt_row);
       nxt_page = __ldg(p.c.block_table + (int64_t)ld.b * p.c.max_pages + j);
       if ((unsigned)nxt_page >= (unsigned)p.c.n_pages) {
@@ -265,19 +298,20 @@ __global__ void __launch_bounds__(Cfg<D, MX, MT, WM>::kThreads, Cfg<D, MX, MT, W
   };
   uint32_t late_dst = 0;
   uint16_t late_val = 0;
-  static_assert(!(MX && D == 64) || C::kStages >= 3, "a late scale must be stored, and a barrier passed, before its tile is read");
+  static_assert(!(MX && D == 64) || C::kStages >= 3,
+                "a late scale must be stored, and a barrier passed, before its tile is read");
   auto load_stage = [&](int stage) {
     if constexpr (MX && D == 64) {
       if (late_dst) asm volatile("st.shared.u16 [%0], %1;" ::"r"(late_dst), "h"(late_val) : "memory");
       late_dst = 0;
     }
     if (ld_left > 0) {
-      const int head = ld.w / p.row_tiles;
-      const int64_t off = nxt_page >= 0 ? nxt_page * p.c.page_stride + nxt_row * p.c.row_stride + head * p.c.head_stride : -1;
+      const int64_t off =
+          nxt_page >= 0 ? nxt_page * p.c.page_stride + nxt_row * p.c.row_stride + ld.head * p.c.head_stride : -1;
       const uint32_t kbase = smem_base + stage * C::kStageBytes;
       constexpr int kPerIter = 32 / kChunks;  // tokens a warp instruction covers
 #pragma unroll
-      for (int i = 0; i < kTokPerWarp; i += kPerIter) {
+      for (int i = 0; i < kWarpTok; i += kPerIter) {
         const int tk = i + lane / kChunks, ch = lane % kChunks;
         const int64_t o = __shfl_sync(0xFFFFFFFFu, off, tk);
         const bool ok = o >= 0;
@@ -286,19 +320,17 @@ __global__ void __launch_bounds__(Cfg<D, MX, MT, WM>::kThreads, Cfg<D, MX, MT, W
         cp_async16(dst, static_cast<const uint8_t*>(p.c.k) + byte, ok);
         cp_async16(dst + C::kHalf, static_cast<const uint8_t*>(p.c.v) + byte, ok);
       }
-      if constexpr (MX) {  // lane t: K scales, lane 16 + t: V scales (WM = 2: 8 + t)
-        const int tk = lane % kTokPerWarp;
+      if constexpr (MX) {  // lane t: K scales, lane 16 + t: V scales
+        const int tk = lane % kWarpTok;
         const int64_t o = __shfl_sync(0xFFFFFFFFu, off, tk);
-        if (lane < 2 * kTokPerWarp) {
-          const bool v = lane >= kTokPerWarp;
-          const uint32_t dst = kbase + 2 * C::kHalf + (v ? kTile * C::kScale : 0) + (tok_first + tk) * C::kScale;
-          const uint8_t* src = (v ? p.c.v_s : p.c.k_s) + ((o >= 0 ? o : 0) >> 5);
-          if constexpr (D == 128) {
-            cp_async4(dst, src, o >= 0);
-          } else {  // two bytes, less than cp.async copies: through a register, stored one tile later
-            late_val = o >= 0 ? __ldg(reinterpret_cast<const uint16_t*>(src)) : (uint16_t)0;
-            late_dst = dst;
-          }
+        const bool v = lane >= kWarpTok;
+        const uint32_t dst = kbase + 2 * C::kHalf + (v ? kTile * C::kScale : 0) + (tok_first + tk) * C::kScale;
+        const uint8_t* src = (v ? p.c.v_s : p.c.k_s) + ((o >= 0 ? o : 0) >> 5);
+        if constexpr (D == 128) {
+          cp_async4(dst, src, o >= 0);
+        } else {  // two bytes, less than cp.async copies: through a register, stored one tile later
+          late_val = o >= 0 ? __ldg(reinterpret_cast<const uint16_t*>(src)) : (uint16_t)0;
+          late_dst = dst;
         }
       }
       --ld_left;
@@ -312,218 +344,594 @@ __global__ void __launch_bounds__(Cfg<D, MX, MT, WM>::kThreads, Cfg<D, MX, MT, W
   for (int s = 0; s < C::kStages - 1; ++s) load_stage(s);
 
   // ---- per-unit state
-  constexpr int kQ = MX ? D / 32 : D / 16;  // K steps of the scores
-  uint32_t qa[MT][kQ][4];
-  uint32_t qb[MX ? MT : 1][MX ? kQ : 1][4];  // the second E4M3 term
+  uint32_t qa[C::kQRegs ? MT : 1][C::kQRegs ? kQ : 1][4];
   float o[MT][kNT][4];
-  float m[MT][2], l[MT][2], f[MT][2];        // running maximum (log2 units), this thread's sum, score factor
-  int limit[MT][2];
+  float m[MT][2], l[MT][2], f[MT][2];  // running maximum (log2 units), this thread's sum, score factor
+
+  const uint32_t q_base = smem_addr(s_q), p_base = smem_addr(s_p);
+  // A fragment of rows 16 a.., step k of the contraction
+  auto q_frag = [&](int a, int k, uint32_t (&r)[4]) {
+    ldsm4(q_base + (a * 16 + (mi & 1) * 8 + mrow) * C::kQPitch + 32 * k + (mi >> 1) * 16, r);
+  };
 
   auto begin_unit = [&]() {
-    const int head = cur.w / p.row_tiles, rt = cur.w - head * p.row_tiles;
+    const int row0 = cur.rt * C::kRows;
+    constexpr int kVec = D / 8;  // threads a row, neighbours in a warp: 16 or 8
+    constexpr int kIter = C::kRows * kVec / kThreads;
+    uint4 raw[kIter];
+    int lim[kIter];
 #pragma unroll
-    for (int a = 0; a < MT; ++a)
+    for (int it = 0; it < kIter; ++it) {  // all loads first
+      const int i = it * kThreads + tid, r = row0 + i / kVec;
+      const int ql = r < p.rows ? r / p.group : 0, j = r - ql * p.group;
+      raw[it] = make_uint4(0u, 0u, 0u, 0u);
+      lim[it] = 0;
+      if (r < p.rows) {
+        raw[it] = __ldg(reinterpret_cast<const uint4*>(p.q + ((int64_t)cur.b * p.L + ql) * p.q_stride +
+                                                       ((int64_t)cur.head * p.group + j) * D + (i % kVec) * 8));
+        lim[it] = cur.len - p.L + 1 + ql;
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      const int i = it * kThreads + tid, rr = i / kVec, col = (i % kVec) * 8;
+      float factor = p.scale_log2;
+      if constexpr (!MX) {
+        *reinterpret_cast<uint4*>(s_q + rr * C::kQPitch + col * 2) = raw[it];
+      } else {
+        uint32_t top = __vmaxu2(__vmaxu2(raw[it].x & 0x7FFF7FFFu, raw[it].y & 0x7FFF7FFFu),
+                                __vmaxu2(raw[it].z & 0x7FFF7FFFu, raw[it].w & 0x7FFF7FFFu));
+        top = max(top & 0xFFFFu, top >> 16);  // largest magnitude, as bf16 bits
+#pragma unroll
+        for (int x = 1; x < kVec; x <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+        // 2^up brings the row's maximum to [2^14, 2^15); rows below 2^-112 stay below it (their scores vanish in fp32)
+        const int be = (int)(top >> 7);
+        const int up = be ? min(141 - be, 126) : 126;
+        const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
+        factor = be == 255 ? __uint_as_float(0x7FC00000u) : p.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
+        float v[8];
+        bf16x8_to_f32(raw[it], v);
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __half2 h2 = __floats2half2_rn(v[2 * e] * mul, v[2 * e + 1] * mul);
+          h[e] = *reinterpret_cast<const uint32_t*>(&h2);
+        }
+        // A lane of the scores' B fragment holds columns 4 c .. 4 c + 3 of a 16-column chunk of K, one word.  So
+        // columns 4 c, 4 c + 1 take the places 2 c, 2 c + 1 of the contraction and 4 c + 2, 4 c + 3 the places 8 later.
+        uint8_t* dst = s_q + rr * C::kQPitch + (col & ~15) * 2 + (col & 8);
+        *reinterpret_cast<uint2*>(dst) = make_uint2(h[0], h[2]);
+        *reinterpret_cast<uint2*>(dst + 16) = make_uint2(h[1], h[3]);
+      }
+      if (col == 0) {
+        s_f[rr] = factor;
+        s_lim[rr] = lim[it];
+      }
+    }
+    __syncthreads();
+    if constexpr (C::kQRegs) {
+#pragma unroll
+      for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int k = 0; k < kQ; ++k) q_frag(a, k, qa[a][k]);
+    }
+#pragma unroll
+    for (int a = 0; a < MT; ++a) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int r = rt * C::kRows + (wm * MT + a) * 16 + li + 8 * h;
-        const bool in = r < p.rows;
-        const int ql = in ? r / p.group : 0, j = in ? r - ql * p.group : 0;
-        limit[a][h] = in ? cur.len - p.L + 1 + ql : 0;
+        f[a][h] = s_f[a * 16 + li + 8 * h];
         m[a][h] = -INFINITY;
         l[a][h] = 0.f;
-        const __nv_bfloat16* src =
-            p.q + ((int64_t)cur.b * p.L + ql) * p.q_stride + ((int64_t)head * p.group + j) * D;
-        if constexpr (!MX) {
-          f[a][h] = p.scale_log2;
-#pragma unroll
-          for (int k = 0; k < kQ; ++k) {
-            qa[a][k][h] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * lc)) : 0u;
-            qa[a][k][h + 2] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + 16 * k + 8 + 2 * lc)) : 0u;
-          }
-        } else {
-          uint2 raw[kQ][2];
-          uint32_t top = 0;  // largest magnitude of the row, as bf16 bits
-#pragma unroll
-          for (int k = 0; k < kQ; ++k)
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              raw[k][z] = in ? __ldg(reinterpret_cast<const uint2*>(src + 32 * k + 16 * z + 4 * lc)) : make_uint2(0u, 0u);
-              top = __vmaxu2(top, __vmaxu2(raw[k][z].x & 0x7FFF7FFFu, raw[k][z].y & 0x7FFF7FFFu));
-            }
-          top = max(top & 0xFFFFu, top >> 16);
-          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-          top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-          // 2^up brings the maximum to [2^7, 2^8); rows below 2^-118 stay below it (their scores are 0 in fp32)
-          const int be = (int)(top >> 7);
-          const int up = be ? min(134 - be, 126) : 126;
-          const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
-          f[a][h] = be == 255 ? __uint_as_float(0x7FC00000u)
-                              : p.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
-#pragma unroll
-          for (int k = 0; k < kQ; ++k)
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              float v[4] = {__uint_as_float(raw[k][z].x << 16), __uint_as_float(raw[k][z].x & 0xFFFF0000u),
-                            __uint_as_float(raw[k][z].y << 16), __uint_as_float(raw[k][z].y & 0xFFFF0000u)};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] *= mul;
-              const uint32_t c0 = e4m3x2(v[0], v[1]), c1 = e4m3x2(v[2], v[3]);
-              uint32_t h0, h1;  // the codes back as fp16 pairs (exact)
-              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h0) : "h"((uint16_t)c0));
-              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h1) : "h"((uint16_t)c1));
-              const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-              const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-              qa[a][k][h + 2 * z] = c0 | (c1 << 16);
-              qb[a][k][h + 2 * z] = (uint32_t)e4m3x2(v[0] - f0.x, v[1] - f0.y) |
-                                    ((uint32_t)e4m3x2(v[2] - f1.x, v[3] - f1.y) << 16);
-            }
-        }
       }
-#pragma unroll
-    for (int a = 0; a < MT; ++a)
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[a][n][e] = 0.f;
+    }
   };
 
-  // o += p v, token by token, leaving out the tokens with p = 0
-  auto add_values_one_by_one = [&](const float (&s)[MT][2][4], uint32_t vb, uint32_t sb) {
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        for (int c = 0; c < 4; ++c) {
-          const int tk = n * 8 + 2 * c + e;
-          float pr[MT][2];
-#pragma unroll
-          for (int a = 0; a < MT; ++a)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) pr[a][h] = __shfl_sync(0xFFFFFFFFu, s[a][n][2 * h + e], (lane & ~3) + c);
-#pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int col = MX ? (nt / 2) * 16 + 4 * lc + (nt & 1) + 2 * y : nt * 8 + 2 * lc + y;
-              const uint32_t at = vb + tk * C::kRowBytes + swz(tk, (MX ? col : 2 * col) / 16) + (MX ? col : 2 * col) % 16;
-              float v;
-              if constexpr (MX) {
-                uint16_t code;
-                uint32_t h2, byte;
-                asm volatile("ld.shared.u8 %0, [%1];" : "=h"(code) : "r"(at));
-                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(sb + (kTile + tk) * C::kScale + col / 32));
-                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(code));
-                v = __low2float(*reinterpret_cast<const __half2*>(&h2)) * __uint_as_float(byte << 23);
-              } else {
-                uint16_t bits;
-                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(bits) : "r"(at));
-                v = __uint_as_float((uint32_t)bits << 16);
-              }
-#pragma unroll
-              for (int a = 0; a < MT; ++a)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  if (pr[a][h] != 0.f) o[a][nt][2 * h + y] = fmaf(pr[a][h], v, o[a][nt][2 * h + y]);
-            }
-        }
-  };
-
-  // ---- one tile: this warp's 16 tokens
-  auto tile = [&](int stage) {
-    const uint32_t kb = smem_base + stage * C::kStageBytes + wt * kWarpTok * C::kRowBytes;
-    const uint32_t vb = kb + C::kHalf;
-    const uint32_t sb = smem_base + stage * C::kStageBytes + 2 * C::kHalf + wt * kWarpTok * C::kScale;
-    float s[MT][2][4];
+  // ---- the scores of this warp's 16 tokens, in log2 units, and their masks
+  float s[MT][2][4];
+  auto scores = [&](int stage) {
+    const uint32_t kb = smem_base + stage * C::kStageBytes + tok_first * C::kRowBytes;
 #pragma unroll
     for (int a = 0; a < MT; ++a)
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[a][n][e] = 0.f;
-    const int mrow = lane & 7, mi = lane >> 3;  // this lane's row address in an ldmatrix of four 8 x 16-byte tiles
+    const int row = (mi >> 1) * 8 + mrow;
+    uint32_t kw[2][2];  // MXFP8: scale words of this thread's score columns
+    if constexpr (MX) {
+      const uint32_t sb = smem_base + stage * C::kStageBytes + 2 * C::kHalf + tok_first * C::kScale;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const uint32_t at = sb + (n * 8 + 2 * lc) * C::kScale;
+        if constexpr (D == 128) {
+          asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(kw[n][0]), "=r"(kw[n][1]) : "r"(at));
+        } else {
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kw[n][0]) : "r"(at));
+          kw[n][1] = kw[n][0] >> 16;
+        }
+      }
+    }
+    auto q_step = [&](int a, int k, uint32_t (&r)[4]) {
+      if constexpr (C::kQRegs) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = qa[a][k][i];
+      } else {
+        q_frag(a, k, r);
+      }
+    };
     if constexpr (!MX) {
 #pragma unroll
       for (int k = 0; k < kQ; ++k) {
-        const int row = (mi >> 1) * 8 + mrow;
         uint32_t kf[4];
         ldsm4(kb + row * C::kRowBytes + swz(row, 2 * k + (mi & 1)), kf);
 #pragma unroll
         for (int a = 0; a < MT; ++a) {
-          mma_bf16(s[a][0], qa[a][k], kf[0], kf[1]);
-          mma_bf16(s[a][1], qa[a][k], kf[2], kf[3]);
+          uint32_t q[4];
+          q_step(a, k, q);
+          mma_bf16(s[a][0], q, kf[0], kf[1]);
+          mma_bf16(s[a][1], q, kf[2], kf[3]);
         }
       }
     } else {
-      uint32_t kw[2][2];  // scale words of this thread's score columns
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int k = 0; k < kQ; k += 2) {  // one MX block
+        uint32_t kf[4];  // tokens 0..7: chunks k, k + 1; tokens 8..15: chunks k, k + 1
+        ldsm4(kb + row * C::kRowBytes + swz(row, k + (mi & 1)), kf);
+        uint32_t b[4][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t at = sb + (n * 8 + 2 * lc + e) * C::kScale;
-          if constexpr (D == 128) {
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(kw[n][e]) : "r"(at));
-          } else {
-            uint16_t h;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at));
-            kw[n][e] = h;
-          }
+        for (int i = 0; i < 4; ++i) {
+          b[i][0] = e4m3_f16(kf[i], false);
+          b[i][1] = e4m3_f16(kf[i], true);
         }
-#pragma unroll
-      for (int k = 0; k < kQ; ++k) {
-        const int row = (mi >> 1) * 8 + mrow;
-        uint32_t kf[4];
-        ldsm4(kb + row * C::kRowBytes + swz(row, 2 * k + (mi & 1)), kf);
+        float k0[2], k1[2];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const float k0 = e8m0_float(kw[n][0], k), k1 = e8m0_float(kw[n][1], k);
+          k0[n] = e8m0_float(kw[n][0], k / 2);
+          k1[n] = e8m0_float(kw[n][1], k / 2);
+        }
 #pragma unroll
-          for (int a = 0; a < MT; ++a) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_e4m3(d, qa[a][k], kf[2 * n], kf[2 * n + 1]);
-            mma_e4m3(d, qb[a][k], kf[2 * n], kf[2 * n + 1]);
-            s[a][n][0] = fmaf(d[0], k0, s[a][n][0]);
-            s[a][n][1] = fmaf(d[1], k1, s[a][n][1]);
-            s[a][n][2] = fmaf(d[2], k0, s[a][n][2]);
-            s[a][n][3] = fmaf(d[3], k1, s[a][n][3]);
+        for (int a = 0; a < MT; ++a) {
+          uint32_t q0[4], q1[4];
+          q_step(a, k, q0);
+          q_step(a, k + 1, q1);
+          float d[2][4];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) mma_f16_zero(d[n], q0, b[2 * n][0], b[2 * n][1]);
+#pragma unroll
+          for (int n = 0; n < 2; ++n) mma_f16(d[n], q1, b[2 * n + 1][0], b[2 * n + 1][1]);
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            fma2(s[a][n][0], s[a][n][1], d[n][0], d[n][1], k0[n], k1[n]);
+            fma2(s[a][n][2], s[a][n][3], d[n][2], d[n][3], k0[n], k1[n]);
           }
         }
       }
     }
-    // scale, mask, running maximum
-    const int tok0 = cur.t * kTile + wt * kWarpTok;
-    const bool edge = tok0 + kWarpTok > cur.len - p.L + 1;  // some row does not see all 16 tokens
-    float mx[MT][2];
 #pragma unroll
     for (int a = 0; a < MT; ++a)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float v = s[a][n][2 * h + e] * f[a][h];
-            if (edge && tok0 + n * 8 + 2 * lc + e >= limit[a][h]) v = -INFINITY;
-            s[a][n][2 * h + e] = v;
-          }
-        mx[a][h] = fmaxf(fmaxf(s[a][0][2 * h], s[a][0][2 * h + 1]), fmaxf(s[a][1][2 * h], s[a][1][2 * h + 1]));
-      }
-    bool grow = false;
-#pragma unroll
-    for (int a = 0; a < MT; ++a)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        mx[a][h] = fmaxf(mx[a][h], __shfl_xor_sync(0xFFFFFFFFu, mx[a][h], 1));
-        mx[a][h] = fmaxf(mx[a][h], __shfl_xor_sync(0xFFFFFFFFu, mx[a][h], 2));
-        // the maximum moves only when it is exceeded by more than 2^8: p stays below 256, which costs no
-        // precision, and the accumulators are rescaled rarely
-        grow |= mx[a][h] > m[a][h] + 8.f;
-      }
-    if (__any_sync(0xFFFFFFFFu, grow)) {
+        for (int e = 0; e < 4; ++e) s[a][n][e] *= f[a][e >> 1];
+    const int tok0 = cur.t * kTile + tok_first;
+    if (tok0 + kWarpTok > cur.len - p.L + 1) {  // some row does not see all of them
 #pragma unroll
       for (int a = 0; a < MT; ++a)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float nm = fmaxf(m[a][h], mx[a][h]);
+          const int lim = s_lim[a * 16 + li + 8 * h] - tok0 - 2 * lc;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (n * 8 + e >= lim) s[a][n][2 * h + e] = -INFINITY;
+        }
+    }
+  };
+
+  // p of this warp's tokens to shared memory; returns this thread's sums
+  auto put_p = [&](float (&sum)[MT][2]) {
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float ref = m[a][h] == -INFINITY ? 0.f : m[a][h];
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = ex2(s[a][i >> 1][2 * h + (i & 1)] - ref);
+        sum[a][h] = (e[0] + e[1]) + (e[2] + e[3]);
+        const uint32_t at = p_base + (a * 16 + li + 8 * h) * kPPitch + (tok_first + 2 * lc) * 2;
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(pack_bf16(e[0], e[1])) : "memory");
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 16), "r"(pack_bf16(e[2], e[3])) : "memory");
+      }
+  };
+
+  // ---- o += p v over the tile's 64 tokens, this warp's columns
+  auto p_frag = [&](int a, int ks, uint32_t (&r)[4]) {
+    ldsm4(p_base + (a * 16 + (mi & 1) * 8 + mrow) * kPPitch + ks * 32 + (mi >> 1) * 16, r);
+  };
+  auto values_bf16 = [&](uint32_t vb) {
+#pragma unroll
+    for (int ks = 0; ks < kTile / 16; ++ks) {
+      uint32_t vf[kNT / 2][4];
+      const int row = ks * 16 + (mi & 1) * 8 + mrow;
+#pragma unroll
+      for (int n = 0; n < kNT; n += 2)
+        ldsm4_trans(vb + row * C::kRowBytes + swz(row, warp * kNT + n + (mi >> 1)), vf[n / 2]);
+#pragma unroll
+      for (int a = 0; a < MT; ++a) {
+        uint32_t pa[4];
+        p_frag(a, ks, pa);
+#pragma unroll
+        for (int n = 0; n < kNT; n += 2) {
+          mma_bf16(o[a][n], pa, vf[n / 2][0], vf[n / 2][1]);
+          mma_bf16(o[a][n + 1], pa, vf[n / 2][2], vf[n / 2][3]);
+        }
+      }
+    }
+  };
+  // MXFP8.  A warp's columns lie in one block of 32, so a token has one scale here.  pair[ks][i]: scale bytes of
+  // tokens 16 ks + 8 i + 2 lc and the next, in 16-bit halves: what a B fragment register holds.
+  // A scale above 2^7 does not fit the one multiplier 2^(byte - 127 + 120): LARGE adds a second one.
+  auto values_mx = [&](uint32_t vb, const uint32_t (&pair)[kTile / 16][2], auto large) {
+    constexpr bool LARGE = decltype(large)::value;
+    constexpr int kZ = kCols / 16;  // 16-byte chunks of a warp's columns
+#pragma unroll
+    for (int ks = 0; ks < kTile / 16; ++ks) {
+      uint32_t vf[4];
+      if constexpr (kZ == 2) {
+        const int row = ks * 16 + (mi & 1) * 8 + mrow;
+        ldsm4_trans(vb + row * C::kRowBytes + swz(row, warp * 2 + (mi >> 1)), vf);
+      } else {  // one chunk: the four 8-row tiles are the tokens of two steps; the step picks its half
+        const int row = (ks & ~1) * 16 + mi * 8 + mrow;
+        uint32_t both[4];
+        ldsm4_trans(vb + row * C::kRowBytes + swz(row, warp), both);
+        vf[0] = both[2 * (ks & 1)];
+        vf[1] = both[2 * (ks & 1) + 1];
+      }
+      uint32_t mul[2], rest[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t b = pair[ks][i];
+        if constexpr (LARGE) {
+          const uint32_t cut = __vminu2(b, 0x00860086u);
+          rest[i] = 0x3F803F80u + ((b - cut) << 7);
+          b = cut;
+        }
+        mul[i] = b * 128u + 0x3C003C00u;
+      }
+      uint32_t bf[kZ][2][2];
+#pragma unroll
+      for (int z = 0; z < kZ; ++z)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          bf[z][0][i] = mul_bf16x2(e4m3_even_bf16(vf[2 * z + i]), mul[i]);
+          bf[z][1][i] = mul_bf16x2(e4m3_odd_bf16(vf[2 * z + i]), mul[i]);
+          if constexpr (LARGE) {
+            bf[z][0][i] = mul_bf16x2(bf[z][0][i], rest[i]);
+            bf[z][1][i] = mul_bf16x2(bf[z][1][i], rest[i]);
+          }
+        }
+#pragma unroll
+      for (int a = 0; a < MT; ++a) {
+        uint32_t pa[4];
+        p_frag(a, ks, pa);
+#pragma unroll
+        for (int z = 0; z < kZ; ++z) {
+          mma_bf16(o[a][2 * z], pa, bf[z][0][0], bf[z][0][1]);      // columns 16 z + 0, 2, 4 ..
+          mma_bf16(o[a][2 * z + 1], pa, bf[z][1][0], bf[z][1][1]);  // .. and 1, 3, 5 ..
+        }
+      }
+    }
+  };
+  // column of o[.][n][2 h + y] inside the warp's columns
+  auto col_of = [&](int n, int y) { return MX ? (n / 2) * 16 + 4 * lc + (n & 1) + 2 * y : n * 8 + 2 * lc + y; };
+
+  // Token by token, leaving out the tokens with p = 0.
+  auto values_one_by_one = [&](uint32_t vb, uint32_t sb) {
+    for (int tk = 0; tk < kTile; ++tk) {
+      float v[kNT][2];
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int col = warp * kCols + col_of(n, y);
+          const int byte = MX ? col : 2 * col;
+          const uint32_t at = vb + tk * C::kRowBytes + swz(tk, byte / 16) + byte % 16;
+          if constexpr (MX) {
+            uint16_t code;
+            uint32_t h2, e;
+            asm volatile("ld.shared.u8 %0, [%1];" : "=h"(code) : "r"(at));
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(sb + tk * C::kScale + col / 32));
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(code));
+            v[n][y] = __low2float(*reinterpret_cast<const __half2*>(&h2)) * __uint_as_float(e << 23);
+          } else {
+            uint16_t bits;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(bits) : "r"(at));
+            v[n][y] = __uint_as_float((uint32_t)bits << 16);
+          }
+        }
+#pragma unroll
+      for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint16_t bits;
+          asm volatile("ld.shared.u16 %0, [%1];" : "=h"(bits) : "r"(p_base + (a * 16 + li + 8 * h) * kPPitch + tk * 2));
+          const float pr = __uint_as_float((uint32_t)bits << 16);
+          if (pr == 0.f) continue;
+#pragma unroll
+          for (int n = 0; n < kNT; ++n)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) o[a][n][2 * h + y] = fmaf(pr, v[n][y], o[a][n][2 * h + y]);
+        }
+    }
+  };
+
+  auto values = [&](int stage) {
+    const uint32_t vb = smem_base + stage * C::kStageBytes + C::kHalf;
+    const uint32_t sb = vb + C::kHalf + kTile * C::kScale;
+    // Tokens that some rows see and others do not (the step's own new tokens): p = 0 must keep a NaN or an
+    // infinity out, which a matrix product would let through.  Rare, so it is looked for only in such tiles.
+    if (p.L > 1 && (cur.t + 1) * kTile > cur.len - p.L + 1) {
+      bool odd = false;
+      for (int i = lane; i < kTile * kCols * (MX ? 1 : 2) / 16; i += 32) {
+        constexpr int kPer = kCols * (MX ? 1 : 2) / 16;
+        const int row = i / kPer;
+        uint32_t w[4];
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(vb + row * C::kRowBytes + swz(row, warp * kPer + i % kPer)));
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          odd |= MX ? __vcmpeq4(w[z] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u : __vcmpeq2(w[z] & 0x7F807F80u, 0x7F807F80u) != 0u;
+      }
+      if (__any_sync(0xFFFFFFFFu, odd)) {
+        values_one_by_one(vb, sb);
+        return;
+      }
+    }
+    if constexpr (!MX) {
+      values_bf16(vb);
+    } else {
+      uint32_t pair[kTile / 16][2], top = 0;
+      const int blk = warp * kCols / 32;
+#pragma unroll
+      for (int ks = 0; ks < kTile / 16; ++ks)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t at = sb + (ks * 16 + 8 * i + 2 * lc) * C::kScale;
+          uint32_t w0, w1;
+          if constexpr (D == 128) {
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(at));
+            w0 = __byte_perm(w0, w1, 0x0400u + 0x0101u * (uint32_t)blk) & 0x00FF00FFu;
+          } else {
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0) : "r"(at));
+            w0 = (w0 >> (8 * blk)) & 0x00FF00FFu;
+          }
+          pair[ks][i] = w0;
+          top = __vmaxu2(top, w0);
+        }
+      if (__any_sync(0xFFFFFFFFu, __vmaxu2(top, 0x00860086u) != 0x00860086u))
+        values_mx(vb, pair, std::true_type{});
+      else
+        values_mx(vb, pair, std::false_type{});
+    }
+  };
+
+  // ---- a unit's end: write the rows, or this block's part of them
+  constexpr size_t kSlot = (size_t)C::kRows * (D + 2);
+  auto end_unit = [&](int64_t unit_first) {
+    const int row0 = cur.rt * C::kRows;
+    const int nrows = min(C::kRows, p.rows - row0);
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[a][h] += __shfl_xor_sync(0xFFFFFFFFu, l[a][h], 1);
+        l[a][h] += __shfl_xor_sync(0xFFFFFFFFu, l[a][h], 2);
+        if (lc == 0) s_l[warp * C::kRows + a * 16 + li + 8 * h] = l[a][h];
+      }
+    __syncthreads();
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = a * 16 + li + 8 * h;
+        l[a][h] = (s_l[r] + s_l[C::kRows + r]) + (s_l[2 * C::kRows + r] + s_l[3 * C::kRows + r]);
+      }
+    const int64_t unit_end = unit_first + cur.nt;
+    // this thread's rows of the final result: o / l and the logarithm of the sum
+    auto write_rows = [&]() {
+#pragma unroll
+      for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = a * 16 + li + 8 * h;
+          if (r >= nrows) continue;
+          const int ql = (row0 + r) / p.group, j = row0 + r - ql * p.group;
+          const float z = l[a][h];
+          const float inv = z == 0.f ? 0.f : 1.f / z;  // a row that sees nothing is 0; a NaN sum stays NaN
+          const int64_t token = (int64_t)cur.b * p.L + ql;
+          const int head = cur.head * p.group + j;
+          __nv_bfloat16* dst = p.out + token * p.out_stride + (int64_t)head * D + warp * kCols;
+          if constexpr (MX) {
+#pragma unroll
+            for (int n = 0; n < kNT; n += 2)
+              *reinterpret_cast<uint2*>(dst + n * 8 + 4 * lc) =
+                  make_uint2(pack_bf16(o[a][n][2 * h] * inv, o[a][n + 1][2 * h] * inv),
+                             pack_bf16(o[a][n][2 * h + 1] * inv, o[a][n + 1][2 * h + 1] * inv));
+          } else {
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+              *reinterpret_cast<uint32_t*>(dst + n * 8 + 2 * lc) =
+                  pack_bf16(o[a][n][2 * h] * inv, o[a][n][2 * h + 1] * inv);
+          }
+          if (p.lse && warp == 0 && lc == 0)
+            p.lse[token * p.Hq + head] = m[a][h] == -INFINITY ? -INFINITY : (m[a][h] + log2f(z)) * kLn2;
+        }
+    };
+    if (unit_first >= t0 && unit_end <= t1) {  // the whole unit was this block's
+      write_rows();
+      return;
+    }
+    auto put_part = [&](float* slot) {
+#pragma unroll
+      for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = a * 16 + li + 8 * h;
+          if (r >= nrows) continue;
+          float* dst = slot + r * D + warp * kCols;
+          if constexpr (MX) {
+#pragma unroll
+            for (int n = 0; n < kNT; n += 2)
+              __stcg(reinterpret_cast<float4*>(dst + n * 8 + 4 * lc),
+                     make_float4(o[a][n][2 * h], o[a][n + 1][2 * h], o[a][n][2 * h + 1], o[a][n + 1][2 * h + 1]));
+          } else {
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+              __stcg(reinterpret_cast<float2*>(dst + n * 8 + 2 * lc), make_float2(o[a][n][2 * h], o[a][n][2 * h + 1]));
+          }
+          if (warp == 0 && lc == 0) {
+            __stcg(slot + C::kRows * D + r, m[a][h]);
+            __stcg(slot + C::kRows * (D + 1) + r, l[a][h]);
+          }
+        }
+    };
+    // o, m, l = the parts 0 .. n_parts - 1 joined in this order; each step loads one part of all rows
+    auto join = [&](int n_parts, auto slot_of) {
+#pragma unroll
+      for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          m[a][h] = -INFINITY;
+          l[a][h] = 0.f;
+#pragma unroll
+          for (int n = 0; n < kNT; ++n) o[a][n][2 * h] = o[a][n][2 * h + 1] = 0.f;
+        }
+#pragma unroll 2
+      for (int i = 0; i < n_parts; ++i) {
+        const float* src = slot_of(i);
+        float pm[MT][2], pl[MT][2], po[MT][2][2 * kNT];
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = min(a * 16 + li + 8 * h, nrows - 1);  // idle rows repeat the last one's loads
+            pm[a][h] = __ldcg(src + C::kRows * D + r);
+            pl[a][h] = __ldcg(src + C::kRows * (D + 1) + r);
+            const float* row = src + r * D + warp * kCols;
+            if constexpr (MX) {
+#pragma unroll
+              for (int n = 0; n < kNT; n += 2) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(row + n * 8 + 4 * lc));
+                po[a][h][2 * n] = x.x, po[a][h][2 * n + 2] = x.y, po[a][h][2 * n + 1] = x.z, po[a][h][2 * n + 3] = x.w;
+              }
+            } else {
+#pragma unroll
+              for (int n = 0; n < kNT; ++n) {
+                const float2 x = __ldcg(reinterpret_cast<const float2*>(row + n * 8 + 2 * lc));
+                po[a][h][2 * n] = x.x, po[a][h][2 * n + 1] = x.y;
+              }
+            }
+          }
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float nm = fmaxf(m[a][h], pm[a][h]);
+            const float c0 = m[a][h] == nm ? 1.f : ex2(m[a][h] - nm), c1 = pm[a][h] == nm ? 1.f : ex2(pm[a][h] - nm);
+            m[a][h] = nm;
+            l[a][h] = fmaf(pl[a][h], c1, l[a][h] * c0);
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                o[a][n][2 * h + y] = fmaf(po[a][h][2 * n + y], c1, o[a][n][2 * h + y] * c0);
+          }
+      }
+    };
+    // counts this block in; true for the last of n
+    auto last_of = [&](int* counter, int n) {
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        s_last = atomicAdd(counter, 1) == n - 1;
+        if (s_last) *counter = 0;
+      }
+      __syncthreads();
+      if (!s_last) return false;
+      __threadfence();
+      return true;
+    };
+    // slot 0 of a block is the unit its run begins in, slot 1 the one that it ends in
+    const int b0 = (int)(unit_first / per), b1 = (int)((unit_end - 1) / per), parts = b1 - b0 + 1;
+    auto block_slot = [&](int b) {
+      return p.partial + ((size_t)b * 2 + (unit_first > b * per ? 1 : 0)) * kSlot;
+    };
+    put_part(block_slot(blockIdx.x));
+    int* counter = p.counters + ((int64_t)cur.b * H + cur.head) * p.row_tiles + cur.rt;
+    if (parts <= kJoin) {
+      if (!last_of(counter, parts)) return;
+      join(parts, [&](int i) { return block_slot(b0 + i); });
+    } else {
+      // many parts: blocks 16 g .. 16 g + 15 are joined first, then these groups.  A group can hold the end of one
+      // such unit and the beginning of the next, told apart as slots are.
+      auto group_at = [&](int g) { return (size_t)g * 2 + (unit_first > (int64_t)g * kJoin * per ? 1 : 0); };
+      const int g0 = b0 / kJoin, g1 = b1 / kJoin, g = blockIdx.x / kJoin;
+      const int first = max(b0, g * kJoin), n = min(b1, g * kJoin + kJoin - 1) - first + 1;
+      if (!last_of(p.group_counters + group_at(g), n)) return;
+      join(n, [&](int i) { return block_slot(first + i); });
+      put_part(p.group_partial + group_at(g) * kSlot);
+      if (!last_of(counter, g1 - g0 + 1)) return;
+      join(g1 - g0 + 1, [&](int i) { return p.group_partial + group_at(g0 + i) * kSlot; });
+    }
+    write_rows();
+  };
+
+  // ---- the run
+  int stage = 0;
+  bool fresh = true;
+  for (int64_t pos = t0; pos < t1;) {
+    if (fresh) {
+      begin_unit();
+      fresh = false;
+    }
+    cp_async_wait<C::kStages - 2>();
+    __syncthreads();  // the tile has landed for all warps, and all are done with the previous one
+    load_stage(stage == 0 ? C::kStages - 1 : stage - 1);
+    scores(stage);
+    bool grow = false;
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        grow |= fmaxf(fmaxf(s[a][0][2 * h], s[a][0][2 * h + 1]), fmaxf(s[a][1][2 * h], s[a][1][2 * h + 1])) >
+                m[a][h] + kGrow;
+    float add[MT][2];
+    put_p(add);
+    if (__syncthreads_or(grow)) {
+#pragma unroll
+      for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float mx = fmaxf(fmaxf(s[a][0][2 * h], s[a][0][2 * h + 1]), fmaxf(s[a][1][2 * h], s[a][1][2 * h + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+          if (lc == 0) s_mx[warp * C::kRows + a * 16 + li + 8 * h] = mx;
+        }
+      __syncthreads();
+#pragma unroll
+      for (int a = 0; a < MT; ++a)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = a * 16 + li + 8 * h;
+          const float nm = fmaxf(fmaxf(fmaxf(s_mx[r], s_mx[C::kRows + r]),
+                                       fmaxf(s_mx[2 * C::kRows + r], s_mx[3 * C::kRows + r])), m[a][h]);
           const float c = m[a][h] == nm ? 1.f : ex2(m[a][h] - nm);
           m[a][h] = nm;
           l[a][h] *= c;
@@ -533,288 +941,19 @@ __global__ void __launch_bounds__(Cfg<D, MX, MT, WM>::kThreads, Cfg<D, MX, MT, W
             o[a][n][2 * h + 1] *= c;
           }
         }
+      put_p(add);
+      __syncthreads();
     }
-    uint32_t pa[MT][4];
-#pragma unroll
-    for (int a = 0; a < MT; ++a) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float ref = m[a][h] == -INFINITY ? 0.f : m[a][h];
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) s[a][n][2 * h + e] = ex2(s[a][n][2 * h + e] - ref);
-        l[a][h] += (s[a][0][2 * h] + s[a][0][2 * h + 1]) + (s[a][1][2 * h] + s[a][1][2 * h + 1]);
-      }
-      pa[a][0] = pack_bf16(s[a][0][0], s[a][0][1]);
-      pa[a][1] = pack_bf16(s[a][0][2], s[a][0][3]);
-      pa[a][2] = pack_bf16(s[a][1][0], s[a][1][1]);
-      pa[a][3] = pack_bf16(s[a][1][2], s[a][1][3]);
-    }
-    // Tokens that some rows see and others do not (the step's own new tokens): p = 0 must keep a NaN or an
-    // infinity out, which a matrix product would let through.  Rare, so it is looked for only in such tiles.
-    if (edge && p.L > 1) {
-      bool odd = false;
-      for (int i = lane; i < kWarpTok * C::kRowBytes / 16; i += 32) {
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(vb + i * 16));
-#pragma unroll
-        for (int z = 0; z < 4; ++z)
-          odd |= MX ? __vcmpeq4(w[z] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u : __vcmpeq2(w[z] & 0x7F807F80u, 0x7F807F80u) != 0u;
-      }
-      if (__any_sync(0xFFFFFFFFu, odd)) {
-        add_values_one_by_one(s, vb, sb);
-        return;
-      }
-    }
-    const int vrow = (mi & 1) * 8 + mrow;
-    if constexpr (!MX) {
-#pragma unroll
-      for (int n = 0; n < kNT; n += 2) {
-        uint32_t vf[4];
-        ldsm4_trans(vb + vrow * C::kRowBytes + swz(vrow, n + (mi >> 1)), vf);
-#pragma unroll
-        for (int a = 0; a < MT; ++a) {
-          mma_bf16(o[a][n], pa[a], vf[0], vf[1]);
-          mma_bf16(o[a][n + 1], pa[a], vf[2], vf[3]);
-        }
-      }
-    } else {
-      // scale words of tokens 2c, 2c + 1 and 2c + 8, 2c + 9: the pairs that a B fragment register holds
-      uint32_t vw[2][2];
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t at = sb + (kTile + n * 8 + 2 * lc + e) * C::kScale;
-          if constexpr (D == 128) {
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(vw[n][e]) : "r"(at));
-          } else {
-            uint16_t h;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at));
-            vw[n][e] = h;
-          }
-        }
-      // a scale above 2^7 does not fit the one multiplier 2^(byte - 127 + 120): its rest is a second one
-      const bool large = __any_sync(0xFFFFFFFFu, (__vcmpgtu4(vw[0][0], 0x86868686u) | __vcmpgtu4(vw[0][1], 0x86868686u) |
-                                                  __vcmpgtu4(vw[1][0], 0x86868686u) | __vcmpgtu4(vw[1][1], 0x86868686u)) != 0u);
-#pragma unroll
-      for (int cc = 0; cc < D / 16; cc += 2) {  // chunks of 16 columns; a pair of chunks is one MX block
-        uint32_t vf[4];
-        ldsm4_trans(vb + vrow * C::kRowBytes + swz(vrow, cc + (mi >> 1)), vf);
-        uint32_t mul[2], rest[2];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          uint32_t pair = ((vw[n][0] >> (4 * cc)) & 0xFFu) | (((vw[n][1] >> (4 * cc)) & 0xFFu) << 16);
-          rest[n] = 0x3F803F80u;
-          if (large) {
-            const uint32_t cut = __vminu2(pair, 0x00860086u);
-            rest[n] += (pair - cut) << 7;
-            pair = cut;
-          }
-          mul[n] = pair * 128u + 0x3C003C00u;
-        }
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {  // chunk cc + z
-          uint32_t e0 = mul_bf16x2(e4m3_even_bf16(vf[2 * z]), mul[0]), e1 = mul_bf16x2(e4m3_even_bf16(vf[2 * z + 1]), mul[1]);
-          uint32_t d0 = mul_bf16x2(e4m3_odd_bf16(vf[2 * z]), mul[0]), d1 = mul_bf16x2(e4m3_odd_bf16(vf[2 * z + 1]), mul[1]);
-          if (large) {
-            e0 = mul_bf16x2(e0, rest[0]), e1 = mul_bf16x2(e1, rest[1]);
-            d0 = mul_bf16x2(d0, rest[0]), d1 = mul_bf16x2(d1, rest[1]);
-          }
-#pragma unroll
-          for (int a = 0; a < MT; ++a) {
-            mma_bf16(o[a][2 * (cc + z)], pa[a], e0, e1);      // columns 16 (cc + z) + 0, 2, 4 ..
-            mma_bf16(o[a][2 * (cc + z) + 1], pa[a], d0, d1);  // .. and 1, 3, 5 ..
-          }
-        }
-      }
-    }
-  };
-
-  // ---- a unit's end: join the token groups, then write the rows, or this block's part of them
-  const int64_t cta0 = t0;  // first tile of this block
-  auto end_unit = [&](int64_t unit_first, int first_tile) {
-    const int head = cur.w / p.row_tiles, rt = cur.w - head * p.row_tiles;
-    const int row0 = rt * C::kRows;
-    const int nrows = min(C::kRows, p.rows - row0);
 #pragma unroll
     for (int a = 0; a < MT; ++a)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        l[a][h] += __shfl_xor_sync(0xFFFFFFFFu, l[a][h], 1);
-        l[a][h] += __shfl_xor_sync(0xFFFFFFFFu, l[a][h], 2);
-        if (lc == 0) s_m[wt * C::kRows + (wm * MT + a) * 16 + li + 8 * h] = m[a][h];
-      }
-    __syncthreads();  // also: the previous unit's readers of join are done
-#pragma unroll
-    for (int a = 0; a < MT; ++a)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = (wm * MT + a) * 16 + li + 8 * h;
-        float M = s_m[r];
-#pragma unroll
-        for (int w = 1; w < kTokWarps; ++w) M = fmaxf(M, s_m[w * C::kRows + r]);
-        const float c = m[a][h] == -INFINITY ? 0.f : ex2(m[a][h] - M);
-        if (lc == 0) {
-          s_l[wt * C::kRows + r] = l[a][h] * c;
-          if (wt == 0) s_M[r] = M;
-        }
-#pragma unroll
-        for (int n = 0; n < kNT; ++n) {
-          o[a][n][2 * h] *= c;
-          o[a][n][2 * h + 1] *= c;
-        }
-      }
-    // four rounds: in round i token group w adds columns quarter (w + i) % 4, so that all warps work in every
-    // round and each quarter receives the groups in a fixed order
-    constexpr int kQuarter = kNT / 4;
-#pragma unroll
-    for (int i = 0; i < kTokWarps; ++i) {
-      const int quarter = (wt + i) % kTokWarps;
-#pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        if (n / kQuarter != quarter) continue;
-#pragma unroll
-        for (int a = 0; a < MT; ++a)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float* row = join + ((wm * MT + a) * 16 + li + 8 * h) * C::kJoinStride;
-            // MXFP8: tile 2 cc holds the even columns of chunk cc, tile 2 cc + 1 the odd ones
-            const int c0 = MX ? (n / 2) * 16 + 4 * lc + (n & 1) : n * 8 + 2 * lc;
-            const int c1 = MX ? c0 + 2 : c0 + 1;
-            if (i == 0) {
-              row[c0] = o[a][n][2 * h];
-              row[c1] = o[a][n][2 * h + 1];
-            } else {
-              row[c0] += o[a][n][2 * h];
-              row[c1] += o[a][n][2 * h + 1];
-            }
-          }
-      }
-      __syncthreads();
-    }
-    if (tid < C::kRows) {
-      float z = 0.f;
-#pragma unroll
-      for (int w = 0; w < kTokWarps; ++w) z += s_l[w * C::kRows + tid];
-      s_Z[tid] = z;
-    }
-    __syncthreads();
-    const int64_t unit_end = unit_first + cur.nt;
-    auto write_row8 = [&](int r, int c8, const float (&v)[8], float inv) {
-      const int ql = (row0 + r) / p.group, j = row0 + r - ql * p.group;
-      float y[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = v[i] * inv;
-      *reinterpret_cast<uint4*>(p.out + ((int64_t)cur.b * p.L + ql) * p.out_stride +
-                                ((int64_t)head * p.group + j) * D + c8) = f32_to_bf16x8(y);
-    };
-    auto write_lse = [&](int r, float M, float z) {
-      const int ql = (row0 + r) / p.group, j = row0 + r - ql * p.group;
-      p.lse[((int64_t)cur.b * p.L + ql) * p.Hq + head * p.group + j] = M == -INFINITY ? -INFINITY : (M + log2f(z)) * kLn2;
-    };
-    // rows that see nothing: z = 0, result 0; a NaN sum stays NaN
-    auto inverse = [](float z) { return z == 0.f ? 0.f : 1.f / z; };
-    if (first_tile == 0 && unit_end <= t1) {  // the whole unit was this block's
-      for (int i = tid; i < nrows * (D / 8); i += C::kThreads) {
-        const int r = i / (D / 8), c8 = (i % (D / 8)) * 8;
-        float v[8];
-        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(join + r * C::kJoinStride + c8);
-        *reinterpret_cast<float4*>(v + 4) = *reinterpret_cast<const float4*>(join + r * C::kJoinStride + c8 + 4);
-        write_row8(r, c8, v, inverse(s_Z[r]));
-      }
-      if (p.lse && tid < nrows) write_lse(tid, s_M[tid], s_Z[tid]);
-      return;
-    }
-    // part of a unit: slot 0 of a block is the unit its run begins in, slot 1 the one that it ends in
-    constexpr size_t kSlot = (size_t)C::kRows * (D + 2);
-    float* mine = p.partial + ((size_t)blockIdx.x * 2 + (unit_first > cta0 ? 1 : 0)) * kSlot;
-    for (int i = tid; i < nrows * (D / 4); i += C::kThreads) {
-      const int r = i / (D / 4), c4 = (i % (D / 4)) * 4;
-      __stcg(reinterpret_cast<float4*>(mine + r * D + c4), *reinterpret_cast<const float4*>(join + r * C::kJoinStride + c4));
-    }
-    if (tid < nrows) {
-      __stcg(mine + C::kRows * D + tid, s_M[tid]);
-      __stcg(mine + C::kRows * (D + 1) + tid, s_Z[tid]);
-    }
-    __threadfence();
-    __syncthreads();
-    const int64_t b0 = unit_first / per, b1 = (unit_end - 1) / per;
-    const int parts = (int)(b1 - b0) + 1;
-    if (tid == 0) {
-      int* counter = p.counters + (int64_t)cur.b * HR + cur.w;
-      const int n = atomicAdd(counter, 1);
-      s_last = n == parts - 1;
-      if (s_last) *counter = 0;
-    }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    // the last block joins the parts in block order
-    auto part = [&](int i) {
-      return p.partial + ((size_t)(b0 + i) * 2 + (i == 0 && unit_first > b0 * per ? 1 : 0)) * kSlot;
-    };
-    for (int r = warp; r < nrows; r += C::kWarps) {
-      float M = -INFINITY;
-      for (int i = lane; i < parts; i += 32) M = fmaxf(M, __ldcg(part(i) + C::kRows * D + r));
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
-      const float ref = M == -INFINITY ? 0.f : M;
-      float z = 0.f;
-      for (int i = lane; i < parts; i += 32)
-        z += __ldcg(part(i) + C::kRows * (D + 1) + r) * ex2(__ldcg(part(i) + C::kRows * D + r) - ref);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, off);
-      if (lane == 0) {
-        s_M[r] = M;
-        s_Z[r] = z;
-      }
-    }
-    __syncthreads();
-    for (int i = tid; i < nrows * (D / 8); i += C::kThreads) {
-      const int r = i / (D / 8), c8 = (i % (D / 8)) * 8;
-      const float ref = s_M[r] == -INFINITY ? 0.f : s_M[r];
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-      for (int k = 0; k < parts; ++k) {
-        const float* src = part(k);
-        const float c = ex2(__ldcg(src + C::kRows * D + r) - ref);
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(src + r * D + c8));
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(src + r * D + c8 + 4));
-        v[0] = fmaf(x.x, c, v[0]), v[1] = fmaf(x.y, c, v[1]), v[2] = fmaf(x.z, c, v[2]), v[3] = fmaf(x.w, c, v[3]);
-        v[4] = fmaf(y.x, c, v[4]), v[5] = fmaf(y.y, c, v[5]), v[6] = fmaf(y.z, c, v[6]), v[7] = fmaf(y.w, c, v[7]);
-      }
-      write_row8(r, c8, v, inverse(s_Z[r]));
-    }
-    if (p.lse && tid < nrows) write_lse(tid, s_M[tid], s_Z[tid]);
-  };
-
-  // ---- the run
-  int stage = 0;
-  int64_t pos = t0;
-  int first_tile = cur.t;
-  bool fresh = true;
-  while (pos < t1) {
-    if (fresh) {
-      begin_unit();
-      fresh = false;
-    }
-    cp_async_wait<C::kStages - 2>();
-    if constexpr (WM == 1)
-      __syncwarp();
-    else
-      __syncthreads();
-    // the slot of the previous tile is free (its readers passed the barrier above)
-    load_stage(stage == 0 ? C::kStages - 1 : stage - 1);
-    tile(stage);
+      for (int h = 0; h < 2; ++h) l[a][h] += add[a][h];
+    values(stage);
     stage = stage == C::kStages - 1 ? 0 : stage + 1;
     ++pos;
     if (cur.t + 1 == cur.nt || pos == t1) {
-      end_unit(pos - 1 - cur.t, first_tile);
-      first_tile = 0;
+      __syncthreads();  // p is no longer read: its place may take the next unit's q
+      end_unit(pos - 1 - cur.t);
       fresh = true;
     }
     advance(cur);
@@ -822,15 +961,15 @@ __global__ void __launch_bounds__(Cfg<D, MX, MT, WM>::kThreads, Cfg<D, MX, MT, W
   cp_async_wait<0>();
 }
 
-template <int D, bool MX, int MT, int WM>
+template <int D, bool MX, int MT>
 cudaError_t launch_one(const AttnParams& p, int num_sms, cudaStream_t s) {
-  using C = Cfg<D, MX, MT, WM>;
-  auto* kernel = paged_attention_kernel<D, MX, MT, WM>;
+  using C = Cfg<D, MX, MT>;
+  auto* kernel = paged_attention_kernel<D, MX, MT>;
   static PerDeviceOnce once;
   cudaError_t e =
       once.run([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(num_sms * C::kBlocks), dim3(C::kThreads), C::kSmem, s, p);
+  return launch_pdl(kernel, dim3(num_sms * C::kBlocks), dim3(kThreads), C::kSmem, s, p);
 }
 
 // Rows of a row tile: the smallest of 16, 32 and 64 that holds the rows of a kv head, 64 above that.
@@ -839,16 +978,16 @@ int tile_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
 template <int D, bool MX>
 cudaError_t launch_rows(const AttnParams& p, int num_sms, cudaStream_t s) {
   switch (tile_rows(p.rows)) {
-    case 16: return launch_one<D, MX, 1, 1>(p, num_sms, s);
-    case 32: return launch_one<D, MX, 2, 1>(p, num_sms, s);
-    default: return launch_one<D, MX, 2, 2>(p, num_sms, s);
+    case 16: return launch_one<D, MX, 1>(p, num_sms, s);
+    case 32: return launch_one<D, MX, 2>(p, num_sms, s);
+    default: return launch_one<D, MX, 4>(p, num_sms, s);
   }
 }
 
 struct Sizes {
   int64_t rows;
   int row_tiles;
-  size_t counters, bytes;
+  size_t blocks, groups, units, counters, slot, bytes;
 };
 
 moe_status_t plan(const moe_kv_cache_t& c, int n_q_heads, int L, int num_sms, const char* call, Sizes* z) {
@@ -863,9 +1002,12 @@ moe_status_t plan(const moe_kv_cache_t& c, int n_q_heads, int L, int num_sms, co
   z->row_tiles = (int)((z->rows + tr - 1) / tr);
   const int64_t units = (int64_t)c.n_seqs * c.n_kv_heads * z->row_tiles;
   if (units > (1ll << 30)) return decode_fail(MOE_ERR_UNSUPPORTED, "%s: too many row tiles", call);
-  z->counters = ((size_t)units * 4 + 255) / 256 * 256;
-  const int blocks = num_sms * (tr == 64 ? 1 : 2);
-  z->bytes = z->counters + (size_t)blocks * 2 * tr * (c.head_dim + 2) * 4;
+  z->blocks = num_sms * 3;  // the most blocks an SM holds
+  z->groups = z->blocks / kJoin + 1;
+  z->units = (size_t)units;
+  z->counters = ((z->units + 2 * z->groups) * 4 + 255) / 256 * 256;
+  z->slot = (size_t)tr * (c.head_dim + 2) * 4;
+  z->bytes = z->counters + 2 * (z->blocks + z->groups) * z->slot;
   return MOE_OK;
 }
 
@@ -929,7 +1071,9 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   p.scale_log2 = a->scale * kLog2e;
   p.pd = page_div((uint32_t)c.page_size);
   p.counters = static_cast<int*>(a->workspace);
+  p.group_counters = p.counters + z.units;
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + z.counters);
+  p.group_partial = p.partial + 2 * z.blocks * (z.slot / 4);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool mx = c.format == MOE_KV_MXFP8;
   cudaError_t e = c.head_dim == 128 ? (mx ? launch_rows<128, true>(p, sms, s) : launch_rows<128, false>(p, sms, s))
