@@ -29,13 +29,14 @@ EXPORTED = ("moe_experts_create", "moe_experts_set_hash_table", "moe_workspace_s
             "moe_stack_create", "moe_stack_forward", "moe_stack_destroy", "moe_mx_blocks_unpack",
             "moe_experts_set_activation_format", "moe_measure_mxf4_peak", "moe_testing_read_h",
             "moe_experts_set_router", "moe_testing_read_y32", "moe_testing_set_pair_gemm", "moe_add_rms_norm",
-            "moe_kv_append", "moe_paged_attention", "moe_paged_attention_workspace")
+            "moe_kv_append", "moe_paged_attention", "moe_paged_attention_workspace", "moe_forward_few")
 
 MOE_MX_NIBBLES_PAIRED, MOE_MX_NIBBLES_SPLIT = 0, 1
 MOE_ACT_MXFP8, MOE_ACT_MXFP4 = 0, 1
 ACT_FORMATS = {"mxfp8": MOE_ACT_MXFP8, "mxfp4": MOE_ACT_MXFP4}
 
 MOE_N_STAGES = 5
+MOE_FEW_MAX_T = 8
 STAGE_NAMES = ("route", "dispatch", "gemm_gate_up", "gemm_down", "combine")
 
 
@@ -120,6 +121,7 @@ def lib() -> ctypes.CDLL:
         L.moe_paged_attention.argtypes = [cachep, ctypes.POINTER(moe_attention_t), vp]
         L.moe_paged_attention_workspace.argtypes = [cachep, i32, i32]
         L.moe_paged_attention_workspace.restype = ctypes.c_size_t
+        L.moe_forward_few.argtypes = [inp, vp, vp, vp, vp, vp, vp, vp, vp]
         L.moe_stack_destroy.restype = None
         L.moe_experts_destroy.argtypes = [vp]
         L.moe_experts_destroy.restype = None
@@ -204,6 +206,14 @@ def moe_expert_ffn(h, n_rows: int, offsets, a_q, a_s, row_w, y, stream=None) -> 
 def moe_forward(x, router_w, router_bias, experts, shared, out, token_ids=None, stream=None) -> None:
     _ok("moe_forward", lib().moe_forward(ctypes.byref(_input(x, token_ids)), _p(router_w), _p(router_bias),
                                          experts, shared, _p(out), _stream(stream)))
+
+
+def moe_forward_few(x, router_w, router_bias, experts, shared, out, topk_ids=None, topk_w=None, token_ids=None,
+                    stream=None) -> None:
+    """moe_forward for at most MOE_FEW_MAX_T rows in one kernel; topk_ids int32 and topk_w fp32 [T, top_k]
+    receive the routing."""
+    _ok("moe_forward_few", lib().moe_forward_few(ctypes.byref(_input(x, token_ids)), _p(router_w), _p(router_bias),
+                                                 experts, shared, _p(out), _p(topk_ids), _p(topk_w), _stream(stream)))
 
 
 def moe_get_routing(h):
@@ -413,6 +423,18 @@ class MoELayer:
             out = torch.empty((x.shape[0], self.d), dtype=torch.bfloat16, device=self.device)
         rw, rb = (None, None) if self.resident_router else (self.router_w, self.router_bias)
         moe_forward(x, rw, rb, self.h, self.h_shared, out, token_ids, stream)
+        return out
+
+    def forward_few(self, x: torch.Tensor, token_ids: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                    topk_ids: torch.Tensor | None = None, topk_w: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+        """``forward`` for at most MOE_FEW_MAX_T rows, in one kernel (MXFP8 activations)."""
+        if token_ids is None and self.hash_table is not None:
+            token_ids = self.token_ids
+        if out is None:
+            out = torch.empty((x.shape[0], self.d), dtype=torch.bfloat16, device=self.device)
+        rw, rb = (None, None) if self.resident_router else (self.router_w, self.router_bias)
+        moe_forward_few(x, rw, rb, self.h, self.h_shared, out, topk_ids, topk_w, token_ids, stream)
         return out
 
     def route(self, x: torch.Tensor, token_ids: torch.Tensor | None = None):

@@ -11,7 +11,9 @@
 #include <string>
 
 #include "moe.h"
+#include "moe_decode.h"
 #include "moe_dispatch_state.cuh"
+#include "moe_few.h"
 #include "moe_internal.h"
 #include "moe_testing.h"
 
@@ -32,6 +34,8 @@ struct moe_experts_s {
   CUtensorMap tm2h;
   CUtensorMap tm_sf13;  // the scale atoms as rows of 256 B, 4-row boxes (both atoms of a slab)
   CUtensorMap tm_sf2;
+  CUtensorMap tm13f;  // packed codes in 32-row boxes (W13) and 64-row boxes (W2): the one-kernel layer's tiles
+  CUtensorMap tm2f;
   int act_fp4 = 0;    // activation format: 0 = MXFP8, 1 = MXFP4 (moe_experts_set_activation_format)
   __nv_bfloat16* router_split = nullptr;  // owned: resident router weight planes (moe_experts_set_router)
   float* router_w32 = nullptr;            // owned: the resident router weights in fp32 (small batches)
@@ -248,6 +252,11 @@ size_t workspace_layout(int max_T, int d, int f, int E, int k, Workspace* ws, vo
   w.y_rows.val = (__half*)take((size_t)dm.rows * d * 2);
   w.y_rows.exp = (uint8_t*)take((size_t)dm.rows * (d / 32));
   w.route_done = (int32_t*)take(4);
+  const size_t few_T = std::min(max_T, kFewMaxT);
+  w.few_counters = (int32_t*)take((size_t)few_counters(d) * 4);
+  w.few_h = (__half*)take(few_T * (k + 1) * f * 2);
+  w.few_h_s = (uint8_t*)take(few_T * (k + 1) * (f / 32));
+  w.few_rows = (float*)take(few_T * (k + 1) * d * 4);
   if (ws) *ws = w;
   return align_up(off, 256);
 }
@@ -331,6 +340,8 @@ moe_status_t moe_experts_create(const moe_config_t* cfg, int32_t n, const uint8_
   if (st == MOE_OK) st = make_map(&h->tm2h, h->w2, true, 128, (uint64_t)n * d * (f / 128), 128);
   if (st == MOE_OK) st = make_map_atoms(&h->tm_sf13, h->sf13, sf13_bytes / 256, 4);
   if (st == MOE_OK) st = make_map_atoms(&h->tm_sf2, h->sf2, sf2_bytes / 256, 4);
+  if (st == MOE_OK) st = make_map_packed(&h->tm13f, h->w13, 64, (uint64_t)n * 2 * f * (d / 128), 32);
+  if (st == MOE_OK) st = make_map_packed(&h->tm2f, h->w2, 64, (uint64_t)n * d * (f / 128), 64);
   if (st != MOE_OK) {
     moe_experts_destroy(h);
     return st;
@@ -422,6 +433,8 @@ moe_status_t moe_set_workspace(moe_experts_t h, void* ws, size_t bytes, int32_t 
   workspace_layout(max_T, h->cfg.d_model, h->cfg.d_ff, h->cfg.n_experts, h->cfg.top_k, &h->ws, ws);
   // the small-batch router's CTA count starts at zero (and every call leaves it there)
   MOE_CUDA(cudaMemset(h->ws.route_done, 0, sizeof(int32_t)), "router counter");
+  // as do those of the one-kernel layer
+  MOE_CUDA(cudaMemset(h->ws.few_counters, 0, (size_t)few_counters(h->cfg.d_model) * 4), "few-token counters");
   h->ws_base = ws;
   h->ws_bytes = bytes;
   h->ws_max_T = max_T;
@@ -747,6 +760,89 @@ uint64_t experts_generation(moe_experts_t h) { return h ? h->generation : 0; }
 }  // namespace moe
 
 extern "C" {
+
+moe_status_t moe_forward_few(const moe_input_t* x, const float* router_w, const float* router_bias, moe_experts_t h,
+                             moe_experts_t sh, void* out_bf16, int32_t* topk_ids, float* topk_w,
+                             moe_stream_t stream) {
+  moe_status_t st = check_input(h, x);
+  if (st != MOE_OK) return st;
+  const int T = x->T, E = h->cfg.n_experts, k = h->cfg.top_k, d = h->cfg.d_model, f = h->cfg.d_ff;
+  if (T > MOE_FEW_MAX_T) return fail(MOE_ERR_UNSUPPORTED, "moe_forward_few takes up to %d rows, got %d", MOE_FEW_MAX_T, T);
+  if (h->n != E) return fail(MOE_ERR_INVALID_ARG, "routed set must hold cfg.n_experts experts");
+  if (sh) {
+    if (sh->n != 1) return fail(MOE_ERR_INVALID_ARG, "shared set must hold exactly one expert");
+    if (sh->cfg.d_model != d || sh->cfg.d_ff != f)
+      return fail(MOE_ERR_INVALID_ARG, "shared expert shape differs from the routed experts");
+  }
+  if (h->act_fp4 || (sh && sh->act_fp4))
+    return fail(MOE_ERR_UNSUPPORTED, "moe_forward_few runs MXFP8 activations only");
+  if (T > 0 && !out_bf16) return fail(MOE_ERR_INVALID_ARG, "out is NULL");
+  if (out_bf16 && !aligned(out_bf16, 16)) return fail(MOE_ERR_INVALID_ARG, "out must be 16-byte aligned");
+  if (!aligned(topk_ids, 4) || !aligned(topk_w, 4))
+    return fail(MOE_ERR_INVALID_ARG, "topk_ids and topk_w must be 4-byte aligned");
+  const bool resident = !router_w && !router_bias && h->router_split;
+  if (h->hash_table) {
+    if (router_w || router_bias) return fail(MOE_ERR_INVALID_ARG, "hash layer: router_w and router_bias must be NULL");
+    if (!x->token_ids) return fail(MOE_ERR_INVALID_ARG, "hash layer: token_ids is NULL");
+  } else {
+    if (!resident && (!router_w || !router_bias))
+      return fail(MOE_ERR_INVALID_ARG, "router_w / router_bias is NULL and the handle has no resident router");
+    if (x->token_ids) return fail(MOE_ERR_INVALID_ARG, "token_ids given but no hash table is set");
+    if (E > 512) return fail(MOE_ERR_UNSUPPORTED, "the learned router supports up to 512 experts");
+    if (!resident && !aligned(router_w, 16)) return fail(MOE_ERR_INVALID_ARG, "router_w must be 16-byte aligned");
+  }
+  // tile coordinates are 32-bit row numbers of the packed codes
+  if ((uint64_t)h->n * 2 * f * (d / 128) > 0x7fffffffull || (uint64_t)h->n * d * (f / 128) > 0x7fffffffull)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_forward_few: expert set too large");
+  if (T > 0 && !few_stages(T, d))
+    return fail(MOE_ERR_UNSUPPORTED, "moe_forward_few: %d rows of %d columns leave no shared memory for the weights", T, d);
+  if (T == 0) {
+    h->last_T = 0;
+    return MOE_OK;
+  }
+  FewArgs a{};
+  a.x = static_cast<const __nv_bfloat16*>(x->x_bf16);
+  if (h->hash_table) {
+    a.tok = x->token_ids;
+    a.table = h->hash_table;
+    a.V = h->hash_V;
+  } else {
+    a.router_w = resident ? h->router_w32 : router_w;
+    a.bias = resident ? h->router_bias : router_bias;
+  }
+  a.sf13 = h->sf13;
+  a.sf2 = h->sf2;
+  a.sf13s = sh ? sh->sf13 : h->sf13;
+  a.sf2s = sh ? sh->sf2 : h->sf2;
+  a.logits = h->ws.logits;
+  a.h = h->ws.few_h;
+  a.h_s = h->ws.few_h_s;
+  a.rows = h->ws.few_rows;
+  a.counters = h->ws.few_counters;
+  a.ws_ids = h->ws.topk_ids;
+  a.ws_w = h->ws.topk_w;
+  a.out_ids = topk_ids;
+  a.out_w = topk_w;
+  a.out = static_cast<__nv_bfloat16*>(out_bf16);
+  a.status = h->status;
+  a.budget_ns = h->budget_ns;
+  a.T = T;
+  a.d = d;
+  a.f = f;
+  a.E = E;
+  a.k = k;
+  a.has_shared = sh ? 1 : 0;
+  a.route_scale = h->cfg.route_scale;
+  a.limit = h->cfg.swiglu_limit;
+  a.stall = h->stall_loads;
+  MOE_CUDA(launch_few_tokens(h->tm13f, h->tm2f, sh ? sh->tm13f : h->tm13f, sh ? sh->tm2f : h->tm2f, a, h->num_sms,
+                             reinterpret_cast<cudaStream_t>(stream)),
+           "few-token layer");
+  h->last_T = T;
+  h->last_fwd_T = -1;  // its rows are not moe_forward's: nothing to read back
+  h->last_rows = 0;
+  return MOE_OK;
+}
 
 moe_status_t moe_get_routing(moe_experts_t h, const int32_t** ids, const float** w, int32_t* T) {
   if (!h || !ids || !w || !T) return fail(MOE_ERR_INVALID_ARG, "NULL argument");

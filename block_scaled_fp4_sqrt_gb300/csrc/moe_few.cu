@@ -1,0 +1,698 @@
+// The whole MoE layer for a few tokens (T <= 8) in one kernel (moe_forward_few): routing, MXFP8 activations,
+// both expert products, SwiGLU and the weighted combine, with the arithmetic of moe_forward.
+//
+// Bound: the touched experts' MXFP4 weights are read once, 13.4 MB an expert at d = 4096, f = 2048 (94 MB for one
+// token, about 0.6 GB for eight), so a step should take their time at HBM rate.  What moe_forward loses against that at
+// these sizes are the gaps between its five kernels; here one persistent block per SM keeps a ring of weight
+// tiles in flight from the routing to the end.
+//
+//  1. Router.  Block b computes the fp32 logits of experts b, b + grid, .. for all tokens (its warps split d);
+//     the same pass loads x and quantises it to MXFP8.  A grid-wide count, then every block selects the top-k of
+//     every token for itself and lists the touched experts (slots) with their tokens.
+//  2. Work items, dealt to the blocks in turn: for every slot f/32 gate-up items (32 gate and 32 up rows of W13, one
+//     MX block of h), then for every slot d/64 down items (64 rows of W2).  The blocks never meet in between: a
+//     down item waits for its own slot's gate-up items (a counter a slot), which came earlier in the list, and
+//     its weights are already in the ring by then.
+//  3. A down item's rows, times their routing weight, go to fp32 rows [token][choice][d]; the last item of a
+//     (64 columns, token) pair sums the token's rows in order (choices, then the shared expert) and rounds once.
+//
+// A block: 1 producer warp (TMA: 64-row, 128-deep weight tiles of 4 KB and their scale atoms, 64-byte swizzle), 16
+// product warps (4 row tiles x 4 ways of splitting the K groups), 3 epilogue warps.
+//
+// Products run on mma.sync m16n8k16 with the weight rows as M and up to 8 tokens as N: E2M1 weights become fp16 by
+// one conversion a pair (exact), x and h are held as fp16 (their E4M3 codes, x with its block scales folded in:
+// exact down to 2^-22 of the token's maximum, far below the fp32 sums' rounding), and the product of each block of
+// 32 is scaled in fp32.  tcgen05 would spend its 128-row operand on at most 8 tokens, and its issue chain and
+// accumulator hand-over are what bounds moe_forward's items here; mma.sync needs 16 of the 47 cycles that a
+// sub-partition has per 16 x 32 weights at full HBM rate.
+#include <float.h>
+
+#include <algorithm>
+
+#include "moe_decode_device.cuh"
+#include "moe_few.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kMaxT = kFewMaxT;
+constexpr int kMmaWarps = 16, kEpiWarps = 3;          // 20 warps with the producer: five a sub-partition
+constexpr int kEpiTok = (kFewMaxT + kEpiWarps - 1) / kEpiWarps;
+constexpr int kThreads = 32 * (kMmaWarps + kEpiWarps + 1);
+constexpr int kTileBytes = 64 * 64;                     // 64 weight rows x 128 E2M1
+constexpr int kStageBytes = kTileBytes + 2 * kSfAtomBytes;
+constexpr int kMaxK = 16;
+constexpr int kMaxSlots = kFewMaxSlots;
+constexpr int kRedStride = 9;                           // floats a row of the partial products (8 tokens)
+constexpr int kRedFloats = 4 * 64 * kRedStride;
+constexpr int kMaxStages = 32;
+
+struct Shared {  // fixed-size part of the block's shared memory
+  uint64_t full[kMaxStages], empty[kMaxStages], red_full[2], red_empty[2];
+  float red[2][kRedFloats];      // [buffer][K split][row][token]
+  float part[kMmaWarps][2][kMaxT];
+  float fx[kMaxT];               // x = fp16 value * fx
+  float w[kMaxT][kMaxK];
+  int ids[kMaxT][kMaxK];
+  int e_max[kMaxT];
+  int rows_of[kMaxT];            // expert rows the token's sum consists of
+  uint32_t taken[kMaxT];         // choices j that are rows of their own (a repeated id joins its first choice)
+  uint32_t touched[32];
+  int n_slots;
+  int abort;
+  int slot_expert[kMaxSlots];    // -1: the shared expert
+  int slot_cnt[kMaxSlots];
+  int slot_ready[kMaxSlots];
+  uint8_t slot_tok[kMaxSlots][kMaxT];
+  uint8_t slot_j[kMaxSlots][kMaxT];
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// Four bytes of E2M1 pairs as fp16 pairs (exact): element 2 i of a byte in the low half.
+__device__ __forceinline__ void e2m1_f16(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// E8M0 byte j of w as a float (byte 0, 2^-127, reads as 0).
+__device__ __forceinline__ float e8m0_float(uint32_t w, int j) {
+  return __uint_as_float(j == 3 ? (w >> 1) & 0x7F800000u : (w << (23 - 8 * j)) & 0x7F800000u);
+}
+
+__device__ __forceinline__ int ld_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
+// Waits end when the phase completes, when the budget runs out or when another warp of the block gave up.
+struct Waiter {
+  Shared* sh;
+  int* status;
+  uint64_t budget;
+  __device__ bool give_up() const {
+    *(volatile int*)&sh->abort = 1;
+    set_status(status, DEV_TIMEOUT);
+    return false;
+  }
+  __device__ bool bar(uint64_t* b, uint32_t parity) const {
+    if (mbar_test(b, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+      if (mbar_try_wait_suspend(b, parity, 20000u)) return true;
+      if (*(volatile int*)&sh->abort) return false;
+      if (globaltimer_ns() - t0 > budget) return give_up();
+    }
+  }
+  __device__ bool count(const int* p, int target) const {
+    if (ld_acquire(p) >= target) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (int i = 0;; ++i) {
+      if (ld_acquire(p) >= target) return true;
+      if ((i & 63) == 63) {
+        if (*(volatile int*)&sh->abort) return false;
+        if (globaltimer_ns() - t0 > budget) return give_up();
+      }
+    }
+  }
+};
+
+template <int NPL>
+__device__ __forceinline__ void select_token(const float* __restrict__ logits, const float* __restrict__ bias, int E,
+                                             int k, float route_scale, int32_t* ids, float* w) {
+  const int lane = threadIdx.x & 31;
+  float l[NPL], sc[NPL], sel[NPL];
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int e = lane + 32 * i;
+    l[i] = e < E ? __ldcg(logits + e) : 0.f;
+    sel[i] = e < E ? __ldg(bias + e) : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const bool in = lane + 32 * i < E;
+    sc[i] = in ? sqrtf(softplus_f(l[i])) : 0.f;
+    sel[i] = in ? sc[i] + sel[i] : -FLT_MAX;
+  }
+  warp_route_topk<NPL>(sc, sel, E, k, route_scale, ids, w);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    few_tokens_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant__ CUtensorMap tm2,
+                      const __grid_constant__ CUtensorMap tm13s, const __grid_constant__ CUtensorMap tm2s,
+                      const FewArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* s_x = ring + a.stages * kStageBytes;  // [T][2 d + 64]: the token's fp16 values
+  const int x_pitch = 2 * a.d + 64;              // 64 bytes off a multiple of 128: two tokens a phase, no conflicts
+  Shared& sh = *reinterpret_cast<Shared*>(s_x + a.T * x_pitch);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int T = a.T, E = a.E, k = a.k, d = a.d, f = a.f;
+  const Waiter wait{&sh, a.status, a.budget_ns};
+
+  // ---------------------------------------------------------------- set-up
+  if (tid == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.red_full[i], kMmaWarps);
+      mbar_init(&sh.red_empty[i], kEpiWarps);
+    }
+    mbar_fence_init();
+    sh.abort = 0;
+  }
+  if (tid < kMaxT) sh.e_max[tid] = -200;
+  for (int i = tid; i < 32; i += kThreads) sh.touched[i] = 0u;
+  for (int i = tid; i < kMaxSlots; i += kThreads) sh.slot_ready[i] = 0;
+  __syncthreads();
+
+  // ---------------------------------------------------------------- router logits and x
+  // Thread (warp, lane) holds 8 columns at 256 warp + 8 lane of every 4096; four lanes share an MX block.
+  if (warp < kMmaWarps) {
+    for (int e0 = blockIdx.x, first = 1; first || (a.router_w && e0 < E); e0 += 2 * gridDim.x, first = 0) {
+      const bool has0 = a.router_w && e0 < E, has1 = a.router_w && e0 + (int)gridDim.x < E;
+      float acc[2][kMaxT];
+#pragma unroll
+      for (int t = 0; t < kMaxT; ++t) acc[0][t] = acc[1][t] = 0.f;
+      for (int base = 0; base < d; base += kMmaWarps * 256) {
+        const int c = base + warp * 256 + lane * 8;
+        const bool in = c < d;
+        float4 w[2][2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          const float4* wp = reinterpret_cast<const float4*>(a.router_w + (size_t)(e0 + z * gridDim.x) * d + c);
+          const bool ok = in && (z ? has1 : has0);
+          w[z][0] = ok ? __ldg(wp) : make_float4(0.f, 0.f, 0.f, 0.f);
+          w[z][1] = ok ? __ldg(wp + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        uint4 raw[kMaxT];
+#pragma unroll
+        for (int t = 0; t < kMaxT; ++t)
+          raw[t] = in && t < T ? __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)t * d + c)) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int t = 0; t < kMaxT; ++t) {
+          if (t >= T) continue;
+          float v[8];
+          bf16x8_to_f32(raw[t], v);
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            acc[z][t] = fmaf(w[z][0].x, v[0], acc[z][t]);
+            acc[z][t] = fmaf(w[z][0].y, v[1], acc[z][t]);
+            acc[z][t] = fmaf(w[z][0].z, v[2], acc[z][t]);
+            acc[z][t] = fmaf(w[z][0].w, v[3], acc[z][t]);
+            acc[z][t] = fmaf(w[z][1].x, v[4], acc[z][t]);
+            acc[z][t] = fmaf(w[z][1].y, v[5], acc[z][t]);
+            acc[z][t] = fmaf(w[z][1].z, v[6], acc[z][t]);
+            acc[z][t] = fmaf(w[z][1].w, v[7], acc[z][t]);
+          }
+          if (first) {  // the raw row waits in its place for the token's largest block exponent
+            float amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+            const int e = __reduce_max_sync(0xFFFFFFFFu, amax > 0.f ? mxfp8_block_exp(amax) : -127);
+            if (lane == 0) atomicMax(&sh.e_max[t], e);
+            if (in) *reinterpret_cast<uint4*>(s_x + t * x_pitch + 2 * c) = raw[t];
+          }
+        }
+      }
+      if (a.router_w) {
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+          for (int t = 0; t < kMaxT; ++t) {
+            if (t >= T) continue;
+            float v = acc[z][t];
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+            if (lane == 0) sh.part[warp][z][t] = v;
+          }
+        asm volatile("bar.sync 1, %0;" ::"n"(kMmaWarps * 32) : "memory");
+        if (tid < 2 * kMaxT) {
+          const int z = tid / kMaxT, t = tid % kMaxT;
+          if (t < T && (z ? has1 : has0)) {
+            float v = 0.f;
+#pragma unroll
+            for (int i = 0; i < kMmaWarps; ++i) v += sh.part[i][z][t];
+            __stcg(a.logits + (size_t)t * E + e0 + z * gridDim.x, v);
+          }
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(kMmaWarps * 32) : "memory");
+      }
+    }
+    __threadfence();
+  }
+  __syncthreads();
+  if (a.router_w && tid == 0) atomicAdd(a.counters + kFewLogitsDone, 1);
+  // x: quantise (E4M3 codes and block exponents as moe_permute takes them) and hold as fp16 code * 2^(e - E + 7),
+  // E the token's largest block exponent
+  if (warp < kMmaWarps) {
+    for (int base = 0; base < d; base += kMmaWarps * 256) {
+      const int c = base + warp * 256 + lane * 8;
+      const bool in = c < d;
+      for (int t = 0; t < T; ++t) {
+        uint8_t* at = s_x + t * x_pitch + 2 * c;
+        const uint4 raw = in ? *reinterpret_cast<const uint4*>(at) : make_uint4(0u, 0u, 0u, 0u);
+        float v[8];
+        bf16x8_to_f32(raw, v);
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+        const int e = mxfp8_block_exp(amax);
+        const float mul = exp2_neg_int(e);
+        const float up = __uint_as_float((uint32_t)(127 + max(e - sh.e_max[t] + 7, -126)) << 23);
+        uint32_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint16_t code = e4m3x2(v[2 * i] * mul, v[2 * i + 1] * mul);
+          uint32_t h2;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(code));
+          const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+          const __half2 o = __floats2half2_rn(q.x * up, q.y * up);
+          h[i] = *reinterpret_cast<const uint32_t*>(&o);
+        }
+        if (in) *reinterpret_cast<uint4*>(at) = make_uint4(h[0], h[1], h[2], h[3]);
+      }
+    }
+  }
+  if (tid < T) sh.fx[tid] = ldexpf(1.f, sh.e_max[tid] - 7);
+
+  // ---------------------------------------------------------------- selection
+  if (warp < T) {
+    if (!a.router_w) {  // hash layer: the token's table row, ascending
+      if (lane == 0) {
+        int v = a.tok[warp];
+        if (v < 0 || v >= a.V) {
+          set_status(a.status, DEV_BAD_TOKEN_ID);
+          v = 0;
+        }
+        for (int j = 0; j < k; ++j) {
+          int e = a.table[(size_t)v * k + j];
+          if (e < 0 || e >= E) {
+            set_status(a.status, DEV_BAD_EXPERT_ID);
+            e = 0;
+          }
+          int b = j - 1;
+          while (b >= 0 && sh.ids[warp][b] > e) {
+            sh.ids[warp][b + 1] = sh.ids[warp][b];
+            --b;
+          }
+          sh.ids[warp][b + 1] = e;
+          sh.w[warp][j] = a.route_scale / (float)k;
+        }
+      }
+    } else {
+      bool ok = true;
+      if (lane == 0) ok = wait.count(a.counters + kFewLogitsDone, (int)gridDim.x);
+      ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
+      if (ok) {
+        const float* l = a.logits + (size_t)warp * E;
+        if (E <= 256)
+          select_token<8>(l, a.bias, E, k, a.route_scale, sh.ids[warp], sh.w[warp]);
+        else
+          select_token<16>(l, a.bias, E, k, a.route_scale, sh.ids[warp], sh.w[warp]);
+      }
+    }
+    __syncwarp();
+    if (lane < k && !*(volatile int*)&sh.abort) {
+      const int e = sh.ids[warp][lane];
+      const float w = sh.w[warp][lane];
+      if (blockIdx.x == 0) {
+        a.ws_ids[warp * k + lane] = e;
+        a.ws_w[warp * k + lane] = w;
+        if (a.out_ids) a.out_ids[warp * k + lane] = e;
+        if (a.out_w) a.out_w[warp * k + lane] = w;
+      }
+      atomicOr(&sh.touched[e >> 5], 1u << (e & 31));
+    }
+  }
+  __syncthreads();
+  // ---------------------------------------------------------------- slots: the shared expert, then experts ascending
+  const int has_shared = a.has_shared;
+  if (!sh.abort) {
+    if (warp == 0) {
+      const uint32_t bits = sh.touched[lane];
+      int before = __popc(bits);
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, before, off);
+        if (lane >= off) before += o;
+      }
+      if (lane == 31) sh.n_slots = before + has_shared;
+      int slot = before - __popc(bits) + has_shared;
+      for (uint32_t m = bits; m; m &= m - 1) sh.slot_expert[slot++] = lane * 32 + __ffs(m) - 1;
+      if (has_shared && lane == 0) {
+        sh.slot_expert[0] = -1;
+        sh.slot_cnt[0] = T;
+      }
+      if (has_shared && lane < T) {
+        sh.slot_tok[0][lane] = (uint8_t)lane;
+        sh.slot_j[0][lane] = (uint8_t)k;
+      }
+      // a token's repeated ids (only a faulty hash table has any) join their first choice
+      if (lane < T) {
+        uint32_t own = 0;
+        for (int j = 0; j < k; ++j) {
+          if (j && sh.ids[lane][j] == sh.ids[lane][j - 1]) {
+            int z = j - 1;
+            while (!((own >> z) & 1u)) --z;
+            sh.w[lane][z] += sh.w[lane][j];
+          } else {
+            own |= 1u << j;
+          }
+        }
+        sh.taken[lane] = own;
+        sh.rows_of[lane] = __popc(own) + has_shared;
+      }
+    }
+    __syncthreads();
+    for (int s = has_shared + tid; s < sh.n_slots; s += kThreads) {
+      const int e = sh.slot_expert[s];
+      int n = 0;
+      for (int t = 0; t < T; ++t)
+        for (int j = 0; j < k; ++j)
+          if (((sh.taken[t] >> j) & 1u) && sh.ids[t][j] == e) {
+            sh.slot_tok[s][n] = (uint8_t)t;
+            sh.slot_j[s][n] = (uint8_t)j;
+            ++n;
+          }
+      sh.slot_cnt[s] = n;
+    }
+  }
+  __syncthreads();
+  const int aborted = sh.abort;
+  __syncthreads();
+  if (!aborted) {
+  const int S = sh.n_slots;
+  const int n_up = f / 32, n_down = d / 64;  // items a slot
+  const int items_up = S * n_up, items = items_up + S * n_down;
+  const int kg_up = d / 128, kg_down = f / 128;
+
+  if (warp == kMmaWarps + kEpiWarps) {
+    // -------------------------------------------------------------- producer
+    if (lane == 0 && !a.stall) {
+      const uint64_t policy = l2_policy_evict_first();
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      int64_t issued = 0;
+      for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
+        const bool up = it < items_up;
+        const int j = up ? it : it - items_up, per = up ? n_up : n_down;
+        const int s = j / per, q = j - s * per;
+        const int e = sh.slot_expert[s];
+        const int KG = up ? kg_up : kg_down, MT = up ? f / 128 : d / 256;
+        const CUtensorMap* map = up ? (e < 0 ? &tm13s : &tm13) : (e < 0 ? &tm2s : &tm2);
+        const uint8_t* sf = up ? (e < 0 ? a.sf13s : a.sf13) : (e < 0 ? a.sf2s : a.sf2);
+        const int ex = max(e, 0);
+        for (int kg = 0; kg < KG; ++kg) {
+          if (!wait.bar(&sh.empty[stage], phase ^ 1u)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = ring + stage * kStageBytes;
+          const int slab = (ex * KG + kg) * MT + q / 4;
+          uint64_t* bar = &sh.full[stage];
+          if (up) {
+            mbar_arrive_expect_tx(bar, kTileBytes + 2 * kSfAtomBytes);
+            tma_load_2d(dst, map, 0, slab * 256 + (q & 3) * 32, bar, policy);
+            tma_load_2d(dst + kTileBytes / 2, map, 0, slab * 256 + 128 + (q & 3) * 32, bar, policy);
+            bulk_load(dst + kTileBytes, sf + (size_t)slab * 2 * kSfAtomBytes, 2 * kSfAtomBytes, bar);
+          } else {
+            mbar_arrive_expect_tx(bar, kTileBytes + kSfAtomBytes);
+            tma_load_2d(dst, map, 0, slab * 256 + (q & 3) * 64, bar, policy);
+            bulk_load(dst + kTileBytes, sf + ((size_t)slab * 2 + ((q & 3) >> 1)) * kSfAtomBytes, kSfAtomBytes, bar);
+          }
+          ++issued;
+          if (++stage == a.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // copies in flight must land before the block ends: every stage issued last must have completed its phase
+      const int64_t tail = issued < a.stages ? issued : a.stages;
+      for (int64_t i = issued - tail; i < issued; ++i) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait_suspend(&sh.full[i % a.stages], (uint32_t)((i / a.stages) & 1), 20000u))
+          if (globaltimer_ns() - t0 > a.budget_ns) {
+            wait.give_up();
+            break;
+          }
+      }
+    }
+  } else if (warp < kMmaWarps) {
+    // -------------------------------------------------------------- products
+    const int mt = warp & 3, ks = warp >> 2;  // row tile, K split
+    const int li = lane >> 2, lc = lane & 3;
+    const int lrow = lane & 15, lblk = lane >> 4;  // ldmatrix address: rows 0..15 of the tile, block pair member
+    int stage0 = 0;                                // ring position and phase of the item's first K group
+    uint32_t phase0 = 0;
+    int n_item = 0;
+    for (int it = blockIdx.x; it < items; it += gridDim.x, ++n_item) {
+      const bool up = it < items_up;
+      const int j = up ? it : it - items_up, per = up ? n_up : n_down;
+      const int s = j / per, q = j - s * per;
+      const int KG = up ? kg_up : kg_down;
+      const int cnt = sh.slot_cnt[s];
+      const int n = li < cnt ? li : 0;  // this lane's token (columns past the slot's tokens repeat the first)
+      const int tok = sh.slot_tok[s][n], ch = sh.slot_j[s][n];
+      const uint8_t* xrow = s_x + tok * x_pitch + lc * 16;
+      const size_t hrow = (size_t)tok * (k + 1) + ch;
+      const __half* hsrc = a.h + hrow * f + lc * 8;
+      // the scales of the accumulator's columns 2 lc, 2 lc + 1 come from those tokens' rows
+      const int n0 = min(2 * lc, cnt - 1), n1 = min(2 * lc + 1, cnt - 1);
+      const uint8_t* hexp0 = a.h_s + ((size_t)sh.slot_tok[s][n0] * (k + 1) + sh.slot_j[s][n0]) * (f / 32);
+      const uint8_t* hexp1 = a.h_s + ((size_t)sh.slot_tok[s][n1] * (k + 1) + sh.slot_j[s][n1]) * (f / 32);
+      if (!up && !*(volatile int*)&sh.slot_ready[s]) {
+        bool ok = true;
+        if (lane == 0) ok = wait.count(a.counters + kFewSlotDone + s, n_up * cnt);
+        if (!__shfl_sync(0xFFFFFFFFu, (int)ok, 0)) break;
+        if (lane == 0) {
+          __threadfence_block();
+          *(volatile int*)&sh.slot_ready[s] = 1;
+        }
+      }
+      __syncwarp();
+      // scale words of rows li, li + 8: gate-up tiles 0, 1 are gate rows (first atom), 2, 3 up rows (second)
+      const int r0 = up ? (mt & 1) * 16 : (mt & 1) * 16, quarter = up ? (q & 3) : ((q & 1) * 2 + (mt >> 1));
+      const uint32_t sf_at = kTileBytes + (up ? (mt >> 1) * kSfAtomBytes : 0) + (r0 + li) * 16 + quarter * 4;
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      bool ok = true;
+      int stage = stage0 + ks;
+      uint32_t phase = phase0;
+      for (int kg = ks; kg < KG; kg += 4, stage += 4) {
+        if (stage >= a.stages) {  // at least 8 stages: one step never passes the ring's end twice
+          stage -= a.stages;
+          phase ^= 1u;
+        }
+        uint4 xb[4];
+        uint32_t hs0 = 0, hs1 = 0;
+        if (!up) {
+#pragma unroll
+          for (int b = 0; b < 4; ++b) xb[b] = *reinterpret_cast<const uint4*>(hsrc + kg * 128 + b * 32);
+          hs0 = *reinterpret_cast<const uint32_t*>(hexp0 + kg * 4);
+          hs1 = *reinterpret_cast<const uint32_t*>(hexp1 + kg * 4);
+        } else {
+#pragma unroll
+          for (int b = 0; b < 4; ++b) xb[b] = *reinterpret_cast<const uint4*>(xrow + (kg * 128 + b * 32) * 2);
+        }
+        if (!wait.bar(&sh.full[stage], phase)) {
+          ok = false;
+          break;
+        }
+        const uint8_t* st = ring + stage * kStageBytes;
+        uint32_t wa[2][4];
+        const int row = mt * 16 + lrow;
+#pragma unroll
+        for (int p = 0; p < 2; ++p)  // blocks 2 p, 2 p + 1: [rows 0..7, 8..15] of each
+          ldsm4(smem_addr(st) + row * 64 + (((2 * p + lblk) ^ ((row >> 1) & 3)) * 16), wa[p]);
+        const uint32_t sw0 = *reinterpret_cast<const uint32_t*>(st + sf_at);
+        const uint32_t sw1 = *reinterpret_cast<const uint32_t*>(st + sf_at + 8 * 16);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.empty[stage]);  // everything this warp needs is in registers
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          uint32_t lo[4], hi[4];
+          e2m1_f16(wa[b >> 1][2 * (b & 1)], lo);
+          e2m1_f16(wa[b >> 1][2 * (b & 1) + 1], hi);
+          float dd[4];
+          mma_f16_zero(dd, lo[0], hi[0], lo[1], hi[1], xb[b].x, xb[b].y);
+          mma_f16(dd, lo[2], hi[2], lo[3], hi[3], xb[b].z, xb[b].w);
+          const float w0 = e8m0_float(sw0, b), w1 = e8m0_float(sw1, b);
+          if (up) {
+            acc[0] = fmaf(dd[0], w0, acc[0]);
+            acc[1] = fmaf(dd[1], w0, acc[1]);
+            acc[2] = fmaf(dd[2], w1, acc[2]);
+            acc[3] = fmaf(dd[3], w1, acc[3]);
+          } else {
+            const float h0 = e8m0_float(hs0, b), h1 = e8m0_float(hs1, b);
+            acc[0] = fmaf(dd[0] * h0, w0, acc[0]);
+            acc[1] = fmaf(dd[1] * h1, w0, acc[1]);
+            acc[2] = fmaf(dd[2] * h0, w1, acc[2]);
+            acc[3] = fmaf(dd[3] * h1, w1, acc[3]);
+          }
+        }
+      }
+      for (stage0 += KG; stage0 >= a.stages; stage0 -= a.stages) phase0 ^= 1u;
+      if (!ok) break;
+      const int buf = n_item & 1;
+      if (!wait.bar(&sh.red_empty[buf], (uint32_t)(((n_item >> 1) & 1) ^ 1))) break;
+      float* red = sh.red[buf] + (ks * 64 + mt * 16 + li) * kRedStride + 2 * lc;
+      red[0] = acc[0];
+      red[1] = acc[1];
+      red[8 * kRedStride] = acc[2];
+      red[8 * kRedStride + 1] = acc[3];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.red_full[buf]);
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int ew = warp - kMmaWarps;
+    int n_item = 0;
+    for (int it = blockIdx.x; it < items; it += gridDim.x, ++n_item) {
+      const bool up = it < items_up;
+      const int j = up ? it : it - items_up, per = up ? n_up : n_down;
+      const int s = j / per, q = j - s * per;
+      const int cnt = sh.slot_cnt[s];
+      const int buf = n_item & 1;
+      if (!wait.bar(&sh.red_full[buf], (uint32_t)((n_item >> 1) & 1))) break;
+      // token n of this item belongs to warp (n + n_item) % kEpiWarps
+      const int first = (ew + kEpiWarps - n_item % kEpiWarps) % kEpiWarps;
+      float v0[kEpiTok], v1[kEpiTok];
+#pragma unroll
+      for (int i = 0; i < kEpiTok; ++i) {
+        const int n = first + i * kEpiWarps;
+        v0[i] = v1[i] = 0.f;
+        if (n < cnt) {
+          const float* red = sh.red[buf] + lane * kRedStride + n;
+#pragma unroll
+          for (int z = 0; z < 4; ++z) {
+            v0[i] += red[z * 64 * kRedStride];
+            v1[i] += red[z * 64 * kRedStride + 32 * kRedStride];
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.red_empty[buf]);
+#pragma unroll
+      for (int i = 0; i < kEpiTok; ++i) {
+        const int n = first + i * kEpiWarps;
+        if (n >= cnt) break;
+        const int t = sh.slot_tok[s][n], ch = sh.slot_j[s][n];
+        const size_t row = (size_t)t * (k + 1) + ch;
+        if (up) {  // lane = column of the MX block
+          const float g = fminf(v0[i] * sh.fx[t], a.limit);
+          const float u = fminf(fmaxf(v1[i] * sh.fx[t], -a.limit), a.limit);
+          const float hv = g / (1.f + expf(-g)) * u;
+          float amax = fabsf(hv);
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
+          const int e = mxfp8_block_exp(amax);
+          const uint16_t code = e4m3x2(hv * exp2_neg_int(e), 0.f);
+          uint32_t h2;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(code));
+          a.h[row * f + q * 32 + lane] = __low2half(*reinterpret_cast<const __half2*>(&h2));
+          if (lane == 0) a.h_s[row * (f / 32) + q] = (uint8_t)(e + 127);
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) atomicAdd(a.counters + kFewSlotDone + s, 1);
+        } else {
+          const float w = ch < k ? sh.w[t][ch] : 1.f;
+          float* dst = a.rows + row * d + q * 64;
+          __stcg(dst + lane, v0[i] * w);
+          __stcg(dst + 32 + lane, v1[i] * w);
+          __threadfence();
+          __syncwarp();
+          int last = 0;
+          if (lane == 0) last = atomicAdd(a.counters + kFewColsDone + q * kMaxT + t, 1) == sh.rows_of[t] - 1;
+          if (__shfl_sync(0xFFFFFFFFu, last, 0)) {  // the token's rows are complete in these columns
+            __threadfence();
+            const float* src = a.rows + (size_t)t * (k + 1) * d + q * 64 + 2 * lane;
+            float2 y = make_float2(0.f, 0.f);
+            const uint32_t own = sh.taken[t];
+#pragma unroll 8
+            for (int z = 0; z <= k; ++z) {
+              if (z < k ? !((own >> z) & 1u) : !has_shared) continue;
+              const float2 r = __ldcg(reinterpret_cast<const float2*>(src + (size_t)z * d));
+              y.x += r.x;
+              y.y += r.y;
+            }
+            *reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)t * d + q * 64 + 2 * lane) = __floats2bfloat162_rn(y.x, y.y);
+          }
+        }
+      }
+    }
+  }
+  }
+  // ---------------------------------------------------------------- the last block to end clears the counters
+  __syncthreads();
+  if (tid == 0) {
+    __threadfence();
+    sh.n_slots = atomicAdd(a.counters + kFewBlocksDone, 1) == (int)gridDim.x - 1;
+  }
+  __syncthreads();
+  if (sh.n_slots) {
+    __threadfence();
+    const int n = few_counters(d);
+    for (int i = tid; i < n; i += kThreads) a.counters[i] = 0;
+  }
+}
+
+}  // namespace
+
+int few_stages(int T, int d) {
+  const long long room = 232448 - 1024 - (long long)sizeof(Shared) - (long long)T * (2 * d + 64);
+  const long long n = room / kStageBytes;
+  return n < 8 ? 0 : (int)std::min<long long>(n, kMaxStages);
+}
+
+cudaError_t launch_few_tokens(const CUtensorMap& tm13, const CUtensorMap& tm2, const CUtensorMap& tm13s,
+                              const CUtensorMap& tm2s, FewArgs a, int num_sms, cudaStream_t s) {
+  a.stages = few_stages(a.T, a.d);
+  if (!a.stages) return cudaErrorInvalidValue;
+  const size_t smem = 1024 + (size_t)a.stages * kStageBytes + (size_t)a.T * (2 * a.d + 64) + sizeof(Shared);
+  static PerDeviceOnce once;
+  cudaError_t e = once.run(
+      [] { return cudaFuncSetAttribute(few_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448); });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(num_sms);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;  // the blocks wait on one another: all of them must be resident
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, few_tokens_kernel, tm13, tm2, tm13s, tm2s, a);
+}
+
+}  // namespace moe

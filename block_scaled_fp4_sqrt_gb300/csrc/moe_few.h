@@ -1,0 +1,49 @@
+// The one-kernel layer for a few tokens: what its host side and its kernel share.
+#pragma once
+
+#include "moe_internal.h"
+
+namespace moe {
+
+constexpr int kFewMaxT = 8;
+constexpr int kFewMaxSlots = kFewMaxT * 16 + 1;  // touched experts: at most T * top_k, and the shared one
+
+// Counters in the workspace, all zero between calls.
+constexpr int kFewLogitsDone = 0;                          // blocks whose logits are written
+constexpr int kFewBlocksDone = 1;                          // blocks that have ended
+constexpr int kFewSlotDone = 2;                            // [slot] h blocks written
+constexpr int kFewColsDone = kFewSlotDone + kFewMaxSlots;  // [d / 64][T] expert rows written in these columns
+inline __host__ __device__ int few_counters(int d) { return kFewColsDone + d / 64 * kFewMaxT; }
+
+struct FewArgs {
+  const __nv_bfloat16* x;   // [T, d]
+  const float* router_w;    // [E, d], NULL on a hash layer
+  const float* bias;        // [E]
+  const int32_t* tok;       // [T] (hash layer)
+  const int32_t* table;     // [V, k]
+  const uint8_t *sf13, *sf2, *sf13s, *sf2s;  // weight scale atoms, routed and shared
+  float* logits;            // [T, E]
+  __half* h;                // [T, k + 1, f] E4M3 codes as fp16
+  uint8_t* h_s;             // [T, k + 1, f / 32]
+  float* rows;              // [T, k + 1, d] weighted expert rows
+  int* counters;
+  int32_t* ws_ids;
+  float* ws_w;
+  int32_t* out_ids;         // may be NULL
+  float* out_w;             // may be NULL
+  __nv_bfloat16* out;       // [T, d]
+  int* status;
+  uint64_t budget_ns;
+  int T, d, f, E, k, V, has_shared, stages;
+  int stall;                // issue no weight copies (moe_testing_stall_loads)
+  float route_scale, limit;
+};
+
+// Stages of the weight ring that fit beside T rows of d columns; 0 if too few.
+int few_stages(int T, int d);
+
+// The tensor maps: packed codes in rows of 64 bytes, 64-byte swizzle, boxes of 32 rows (W13) and 64 rows (W2).
+cudaError_t launch_few_tokens(const CUtensorMap& tm13, const CUtensorMap& tm2, const CUtensorMap& tm13s,
+                              const CUtensorMap& tm2s, FewArgs a, int num_sms, cudaStream_t s);
+
+}  // namespace moe

@@ -1,11 +1,12 @@
 /*
  * moe_decode.h -- the operators around the MoE layer in a decode or verify step: the residual addition with
- * its root-mean-square norm, and the paged key-value cache (its writer and the attention that reads it).
+ * its root-mean-square norm, the paged key-value cache (its writer and the attention that reads it), and the
+ * whole MoE layer for a few tokens in one kernel.
  *
  * A decoder block of one step, T = n_seqs * L rows (L new tokens of every request; L = 8 in the verify batch of
  * 64 requests x 8 rows that moe.h describes):
  *   moe_add_rms_norm -> (q, k, v projections) -> moe_kv_append -> moe_paged_attention -> (output projection)
- *   -> moe_add_rms_norm -> moe_forward.
+ *   -> moe_add_rms_norm -> moe_forward, or moe_forward_few for up to MOE_FEW_MAX_T rows.
  *
  * The conventions of moe.h hold: device pointers, asynchronous on `stream`, no allocation inside a call, the
  * returned status covers host-side checks and launch errors.  Strides are counted in elements.  Every call is
@@ -124,6 +125,19 @@ typedef struct {
 MOE_API size_t moe_paged_attention_workspace(const moe_kv_cache_t* cache, int32_t n_q_heads, int32_t L);
 MOE_API moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_attention_t* args,
                                          moe_stream_t stream);
+
+/*
+ * moe_forward for a batch of at most MOE_FEW_MAX_T rows, in one kernel: the same routing, MXFP8 activations,
+ * experts and combine (see moe.h), with the weighted expert rows summed in fp32 as they are.  Arguments and
+ * errors are moe_forward's; the expert sets must use MOE_ACT_MXFP8, and n_experts <= 512 for the learned router.
+ * topk_ids int32 [T, top_k] and topk_w fp32 [T, top_k] receive the routing (each may be NULL).  Uses the
+ * workspace of `experts`.  The kernel's blocks wait on one another: it is launched cooperatively, one block per
+ * SM, and every wait is bounded by the handle's wait budget (moe_check reports MOE_ERR_TIMEOUT).
+ */
+#define MOE_FEW_MAX_T 8
+MOE_API moe_status_t moe_forward_few(const moe_input_t* x, const float* router_w, const float* router_bias,
+                                     moe_experts_t experts, moe_experts_t shared, void* out_bf16, int32_t* topk_ids,
+                                     float* topk_w, moe_stream_t stream);
 
 #ifdef __cplusplus
 }
