@@ -34,8 +34,7 @@ struct moe_experts_s {
   CUtensorMap tm2h;
   CUtensorMap tm_sf13;  // the scale atoms as rows of 256 B, 4-row boxes (both atoms of a slab)
   CUtensorMap tm_sf2;
-  CUtensorMap tm13f;  // packed codes in 32-row boxes (W13) and 64-row boxes (W2): the one-kernel layer's tiles
-  CUtensorMap tm2f;
+  FewMaps few;        // the one-kernel layer's maps over the same codes and scale atoms
   int act_fp4 = 0;    // activation format: 0 = MXFP8, 1 = MXFP4 (moe_experts_set_activation_format)
   __nv_bfloat16* router_split = nullptr;  // owned: resident router weight planes (moe_experts_set_router)
   float* router_w32 = nullptr;            // owned: the resident router weights in fp32 (small batches)
@@ -167,6 +166,37 @@ moe_status_t make_map_bf16(CUtensorMap* m, const void* base, uint64_t K, uint64_
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled (bf16) failed (%d)", (int)r);
+  return MOE_OK;
+}
+
+// The maps of FewMaps (moe_few.h) over an expert set's packed codes and scale atoms.
+moe_status_t make_few_maps(FewMaps* m, const void* w13, const void* w2, const void* sf13, const void* sf2, int n, int d,
+                           int f) {
+  auto fn = encode_fn();
+  if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t up_tiles = f / 128, up_groups = (cuuint64_t)n * (d / 128);
+  const cuuint64_t dn_tiles = d / 256, dn_groups = (cuuint64_t)n * (f / 128);
+  const struct {
+    CUtensorMap* map;
+    const void* base;
+    bool words;  // scale atoms, as 32-bit words
+    cuuint32_t rank;
+    cuuint64_t dim[5], stride[4];
+    cuuint32_t box[5];
+  } maps[] = {
+      {&m->w13, w13, false, 5, {64, 128, 2, up_tiles, up_groups}, {64, 8192, 16384, up_tiles * 16384}, {64, 32, 2, 1, 4}},
+      {&m->w2, w2, false, 4, {64, 256, dn_tiles, dn_groups}, {64, 16384, dn_tiles * 16384}, {64, 64, 1, 4}},
+      {&m->sf13, sf13, true, 4, {128, 2, up_tiles, up_groups}, {512, 1024, up_tiles * 1024}, {128, 2, 1, 4}},
+      {&m->sf2, sf2, true, 4, {128, 2, dn_tiles, dn_groups}, {512, 1024, dn_tiles * 1024}, {128, 1, 1, 4}},
+  };
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  for (const auto& p : maps) {
+    const CUresult r = fn(p.map, p.words ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT8, p.rank,
+                          const_cast<void*>(p.base), p.dim, p.stride, p.box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          p.words ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled (few-token tiles) failed (%d)", (int)r);
+  }
   return MOE_OK;
 }
 
@@ -340,8 +370,7 @@ moe_status_t moe_experts_create(const moe_config_t* cfg, int32_t n, const uint8_
   if (st == MOE_OK) st = make_map(&h->tm2h, h->w2, true, 128, (uint64_t)n * d * (f / 128), 128);
   if (st == MOE_OK) st = make_map_atoms(&h->tm_sf13, h->sf13, sf13_bytes / 256, 4);
   if (st == MOE_OK) st = make_map_atoms(&h->tm_sf2, h->sf2, sf2_bytes / 256, 4);
-  if (st == MOE_OK) st = make_map_packed(&h->tm13f, h->w13, 64, (uint64_t)n * 2 * f * (d / 128), 32);
-  if (st == MOE_OK) st = make_map_packed(&h->tm2f, h->w2, 64, (uint64_t)n * d * (f / 128), 64);
+  if (st == MOE_OK) st = make_few_maps(&h->few, h->w13, h->w2, h->sf13, h->sf2, n, d, f);
   if (st != MOE_OK) {
     moe_experts_destroy(h);
     return st;
@@ -791,9 +820,6 @@ moe_status_t moe_forward_few(const moe_input_t* x, const float* router_w, const 
     if (E > 512) return fail(MOE_ERR_UNSUPPORTED, "the learned router supports up to 512 experts");
     if (!resident && !aligned(router_w, 16)) return fail(MOE_ERR_INVALID_ARG, "router_w must be 16-byte aligned");
   }
-  // tile coordinates are 32-bit row numbers of the packed codes
-  if ((uint64_t)h->n * 2 * f * (d / 128) > 0x7fffffffull || (uint64_t)h->n * d * (f / 128) > 0x7fffffffull)
-    return fail(MOE_ERR_UNSUPPORTED, "moe_forward_few: expert set too large");
   if (T > 0 && !few_stages(T, d))
     return fail(MOE_ERR_UNSUPPORTED, "moe_forward_few: %d rows of %d columns leave no shared memory for the weights", T, d);
   if (T == 0) {
@@ -810,10 +836,6 @@ moe_status_t moe_forward_few(const moe_input_t* x, const float* router_w, const 
     a.router_w = resident ? h->router_w32 : router_w;
     a.bias = resident ? h->router_bias : router_bias;
   }
-  a.sf13 = h->sf13;
-  a.sf2 = h->sf2;
-  a.sf13s = sh ? sh->sf13 : h->sf13;
-  a.sf2s = sh ? sh->sf2 : h->sf2;
   a.logits = h->ws.logits;
   a.h = h->ws.few_h;
   a.h_s = h->ws.few_h_s;
@@ -835,8 +857,7 @@ moe_status_t moe_forward_few(const moe_input_t* x, const float* router_w, const 
   a.route_scale = h->cfg.route_scale;
   a.limit = h->cfg.swiglu_limit;
   a.stall = h->stall_loads;
-  MOE_CUDA(launch_few_tokens(h->tm13f, h->tm2f, sh ? sh->tm13f : h->tm13f, sh ? sh->tm2f : h->tm2f, a, h->num_sms,
-                             reinterpret_cast<cudaStream_t>(stream)),
+  MOE_CUDA(launch_few_tokens(h->few, sh ? sh->few : h->few, a, h->num_sms, reinterpret_cast<cudaStream_t>(stream)),
            "few-token layer");
   h->last_T = T;
   h->last_fwd_T = -1;  // its rows are not moe_forward's: nothing to read back

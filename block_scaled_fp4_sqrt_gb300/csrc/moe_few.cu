@@ -16,7 +16,7 @@
 //  3. A down item's rows, times their routing weight, go to fp32 rows [token][choice][d]; the last item of a
 //     (64 columns, token) pair sums the token's rows in order (choices, then the shared expert) and rounds once.
 //
-// A block: 1 producer warp (TMA: 64-row, 128-deep weight tiles of 4 KB and their scale atoms, 64-byte swizzle), 16
+// A block: 1 producer warp (TMA: stages of 64 weight rows x 512, 16 KB with 64-byte swizzle, and their scale atoms, two copies a stage), 16
 // product warps (4 row tiles x 4 ways of splitting the K groups), 3 epilogue warps.
 //
 // Products run on mma.sync m16n8k16 with the weight rows as M and up to 8 tokens as N: E2M1 weights become fp16 by
@@ -41,12 +41,14 @@ constexpr int kMmaWarps = 16, kEpiWarps = 3;          // 20 warps with the produ
 constexpr int kEpiTok = (kFewMaxT + kEpiWarps - 1) / kEpiWarps;
 constexpr int kThreads = 32 * (kMmaWarps + kEpiWarps + 1);
 constexpr int kTileBytes = 64 * 64;                     // 64 weight rows x 128 E2M1
-constexpr int kStageBytes = kTileBytes + 2 * kSfAtomBytes;
+constexpr int kStageKg = 4;                             // K groups of 128 in a stage, one to a K split
+constexpr int kStageBytes = kStageKg * (kTileBytes + 2 * kSfAtomBytes);
+constexpr int kStageSf = kStageKg * kTileBytes;         // the scale atoms follow the codes
 constexpr int kMaxK = 16;
 constexpr int kMaxSlots = kFewMaxSlots;
 constexpr int kRedStride = 9;                           // floats a row of the partial products (8 tokens)
 constexpr int kRedFloats = 4 * 64 * kRedStride;
-constexpr int kMaxStages = 32;
+constexpr int kMaxStages = 12;
 
 struct Shared {  // fixed-size part of the block's shared memory
   uint64_t full[kMaxStages], empty[kMaxStages], red_full[2], red_empty[2];
@@ -100,6 +102,31 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 // E8M0 byte j of w as a float (byte 0, 2^-127, reads as 0).
 __device__ __forceinline__ float e8m0_float(uint32_t w, int j) {
   return __uint_as_float(j == 3 ? (w >> 1) & 0x7F800000u : (w << (23 - 8 * j)) & 0x7F800000u);
+}
+
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, int c4,
+                                            uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_addr(bar)), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d_hint(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                                 uint64_t* bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar)), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}],"
+      " [%6];" ::"r"(smem_addr(dst)),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_addr(bar))
+      : "memory");
 }
 
 __device__ __forceinline__ int ld_acquire(const int* p) {
@@ -163,6 +190,8 @@ __device__ __forceinline__ void select_token(const float* __restrict__ logits, c
 __global__ void __launch_bounds__(kThreads, 1)
     few_tokens_kernel(const __grid_constant__ CUtensorMap tm13, const __grid_constant__ CUtensorMap tm2,
                       const __grid_constant__ CUtensorMap tm13s, const __grid_constant__ CUtensorMap tm2s,
+                      const __grid_constant__ CUtensorMap sf13, const __grid_constant__ CUtensorMap sf2,
+                      const __grid_constant__ CUtensorMap sf13s, const __grid_constant__ CUtensorMap sf2s,
                       const FewArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -177,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < a.stages; ++i) {
       mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 4);
+      mbar_init(&sh.empty[i], kMmaWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.red_full[i], kMmaWarps);
@@ -427,27 +456,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int j = up ? it : it - items_up, per = up ? n_up : n_down;
         const int s = j / per, q = j - s * per;
         const int e = sh.slot_expert[s];
-        const int KG = up ? kg_up : kg_down, MT = up ? f / 128 : d / 256;
+        const int KG = up ? kg_up : kg_down;
         const CUtensorMap* map = up ? (e < 0 ? &tm13s : &tm13) : (e < 0 ? &tm2s : &tm2);
-        const uint8_t* sf = up ? (e < 0 ? a.sf13s : a.sf13) : (e < 0 ? a.sf2s : a.sf2);
+        const CUtensorMap* sf = up ? (e < 0 ? &sf13s : &sf13) : (e < 0 ? &sf2s : &sf2);
         const int ex = max(e, 0);
-        for (int kg = 0; kg < KG; ++kg) {
+        for (int kg = 0; kg < KG; kg += kStageKg) {  // a stage past KG brings the next rows along; nobody reads them
           if (!wait.bar(&sh.empty[stage], phase ^ 1u)) {
             ok = false;
             break;
           }
           uint8_t* dst = ring + stage * kStageBytes;
-          const int slab = (ex * KG + kg) * MT + q / 4;
           uint64_t* bar = &sh.full[stage];
           if (up) {
-            mbar_arrive_expect_tx(bar, kTileBytes + 2 * kSfAtomBytes);
-            tma_load_2d(dst, map, 0, slab * 256 + (q & 3) * 32, bar, policy);
-            tma_load_2d(dst + kTileBytes / 2, map, 0, slab * 256 + 128 + (q & 3) * 32, bar, policy);
-            bulk_load(dst + kTileBytes, sf + (size_t)slab * 2 * kSfAtomBytes, 2 * kSfAtomBytes, bar);
+            mbar_arrive_expect_tx(bar, kStageKg * (kTileBytes + 2 * kSfAtomBytes));
+            tma_load_5d(dst, map, 0, (q & 3) * 32, 0, q >> 2, ex * KG + kg, bar, policy);
+            tma_load_4d(dst + kStageSf, sf, 0, 0, q >> 2, ex * KG + kg, bar);
           } else {
-            mbar_arrive_expect_tx(bar, kTileBytes + kSfAtomBytes);
-            tma_load_2d(dst, map, 0, slab * 256 + (q & 3) * 64, bar, policy);
-            bulk_load(dst + kTileBytes, sf + ((size_t)slab * 2 + ((q & 3) >> 1)) * kSfAtomBytes, kSfAtomBytes, bar);
+            mbar_arrive_expect_tx(bar, kStageKg * (kTileBytes + kSfAtomBytes));
+            tma_load_4d_hint(dst, map, 0, (q & 3) * 64, q >> 2, ex * KG + kg, bar, policy);
+            tma_load_4d(dst + kStageSf, sf, 0, (q & 3) >> 1, q >> 2, ex * KG + kg, bar);
           }
           ++issued;
           if (++stage == a.stages) {
@@ -472,8 +499,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int mt = warp & 3, ks = warp >> 2;  // row tile, K split
     const int li = lane >> 2, lc = lane & 3;
     const int lrow = lane & 15, lblk = lane >> 4;  // ldmatrix address: rows 0..15 of the tile, block pair member
-    int stage0 = 0;                                // ring position and phase of the item's first K group
-    uint32_t phase0 = 0;
+    int stage = 0;
+    uint32_t phase = 0;
+    auto next_stage = [&]() {
+      if (++stage == a.stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    };
     int n_item = 0;
     for (int it = blockIdx.x; it < items; it += gridDim.x, ++n_item) {
       const bool up = it < items_up;
@@ -502,15 +535,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       // scale words of rows li, li + 8: gate-up tiles 0, 1 are gate rows (first atom), 2, 3 up rows (second)
       const int r0 = up ? (mt & 1) * 16 : (mt & 1) * 16, quarter = up ? (q & 3) : ((q & 1) * 2 + (mt >> 1));
-      const uint32_t sf_at = kTileBytes + (up ? (mt >> 1) * kSfAtomBytes : 0) + (r0 + li) * 16 + quarter * 4;
+      const uint32_t sf_at = kStageSf + (up ? (2 * ks + (mt >> 1)) * kSfAtomBytes : ks * kSfAtomBytes) + (r0 + li) * 16 + quarter * 4;
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
       bool ok = true;
-      int stage = stage0 + ks;
-      uint32_t phase = phase0;
-      for (int kg = ks; kg < KG; kg += 4, stage += 4) {
-        if (stage >= a.stages) {  // at least 8 stages: one step never passes the ring's end twice
-          stage -= a.stages;
-          phase ^= 1u;
+      for (int kg = ks; kg - ks < KG; kg += kStageKg) {
+        if (kg >= KG) {  // this split has no part in the last stage
+          if (!wait.bar(&sh.full[stage], phase)) {
+            ok = false;
+            break;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.empty[stage]);
+          next_stage();
+          break;
         }
         uint4 xb[4];
         uint32_t hs0 = 0, hs1 = 0;
@@ -532,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = mt * 16 + lrow;
 #pragma unroll
         for (int p = 0; p < 2; ++p)  // blocks 2 p, 2 p + 1: [rows 0..7, 8..15] of each
-          ldsm4(smem_addr(st) + row * 64 + (((2 * p + lblk) ^ ((row >> 1) & 3)) * 16), wa[p]);
+          ldsm4(smem_addr(st) + ks * kTileBytes + row * 64 + (((2 * p + lblk) ^ ((row >> 1) & 3)) * 16), wa[p]);
         const uint32_t sw0 = *reinterpret_cast<const uint32_t*>(st + sf_at);
         const uint32_t sw1 = *reinterpret_cast<const uint32_t*>(st + sf_at + 8 * 16);
         __syncwarp();
@@ -559,8 +596,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             acc[3] = fmaf(dd[3] * h1, w1, acc[3]);
           }
         }
+        next_stage();
       }
-      for (stage0 += KG; stage0 >= a.stages; stage0 -= a.stages) phase0 ^= 1u;
       if (!ok) break;
       const int buf = n_item & 1;
       if (!wait.bar(&sh.red_empty[buf], (uint32_t)(((n_item >> 1) & 1) ^ 1))) break;
@@ -670,11 +707,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 int few_stages(int T, int d) {
   const long long room = 232448 - 1024 - (long long)sizeof(Shared) - (long long)T * (2 * d + 64);
   const long long n = room / kStageBytes;
-  return n < 8 ? 0 : (int)std::min<long long>(n, kMaxStages);
+  return n < 3 ? 0 : (int)std::min<long long>(n, kMaxStages);
 }
 
-cudaError_t launch_few_tokens(const CUtensorMap& tm13, const CUtensorMap& tm2, const CUtensorMap& tm13s,
-                              const CUtensorMap& tm2s, FewArgs a, int num_sms, cudaStream_t s) {
+cudaError_t launch_few_tokens(const FewMaps& routed, const FewMaps& shared, FewArgs a, int num_sms, cudaStream_t s) {
   a.stages = few_stages(a.T, a.d);
   if (!a.stages) return cudaErrorInvalidValue;
   const size_t smem = 1024 + (size_t)a.stages * kStageBytes + (size_t)a.T * (2 * a.d + 64) + sizeof(Shared);
@@ -692,7 +728,8 @@ cudaError_t launch_few_tokens(const CUtensorMap& tm13, const CUtensorMap& tm2, c
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, few_tokens_kernel, tm13, tm2, tm13s, tm2s, a);
+  return cudaLaunchKernelEx(&cfg, few_tokens_kernel, routed.w13, routed.w2, shared.w13, shared.w2, routed.sf13,
+                            routed.sf2, shared.sf13, shared.sf2, a);
 }
 
 }  // namespace moe

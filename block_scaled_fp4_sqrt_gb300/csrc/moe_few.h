@@ -21,7 +21,6 @@ struct FewArgs {
   const float* bias;        // [E]
   const int32_t* tok;       // [T] (hash layer)
   const int32_t* table;     // [V, k]
-  const uint8_t *sf13, *sf2, *sf13s, *sf2s;  // weight scale atoms, routed and shared
   float* logits;            // [T, E]
   __half* h;                // [T, k + 1, f] E4M3 codes as fp16
   uint8_t* h_s;             // [T, k + 1, f / 32]
@@ -42,8 +41,14 @@ struct FewArgs {
 // Stages of the weight ring that fit beside T rows of d columns; 0 if too few.
 int few_stages(int T, int d);
 
-// The tensor maps: packed codes in rows of 64 bytes, 64-byte swizzle, boxes of 32 rows (W13) and 64 rows (W2).
-cudaError_t launch_few_tokens(const CUtensorMap& tm13, const CUtensorMap& tm2, const CUtensorMap& tm13s,
-                              const CUtensorMap& tm2s, FewArgs a, int num_sms, cudaStream_t s);
+// Tensor maps of one expert set for this kernel: a copy brings the K groups kg .. kg + 3 of 64 weight rows.
+//   w13   {64 B, 128 rows, gate / up, f / 128, experts * d / 128}, box {64, 32, 2, 1, 4}, 64-byte swizzle
+//   w2    {64 B, 256 rows, d / 256, experts * f / 128}, box {64, 64, 1, 4}, 64-byte swizzle
+//   sf13  {128 words, gate / up, f / 128, experts * d / 128}, box {128, 2, 1, 4}
+//   sf2   {128 words, row half, d / 256, experts * f / 128}, box {128, 1, 1, 4}
+struct FewMaps {
+  CUtensorMap w13, w2, sf13, sf2;
+};
+cudaError_t launch_few_tokens(const FewMaps& routed, const FewMaps& shared, FewArgs a, int num_sms, cudaStream_t s);
 
 }  // namespace moe
