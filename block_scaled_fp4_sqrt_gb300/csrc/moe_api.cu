@@ -284,7 +284,7 @@ size_t workspace_layout(int max_T, int d, int f, int E, int k, Workspace* ws, vo
   w.route_done = (int32_t*)take(4);
   const size_t few_T = std::min(max_T, kFewMaxT);
   w.few_counters = (int32_t*)take((size_t)few_counters(d) * 4);
-  w.few_h = (__half*)take(few_T * (k + 1) * f * 2);
+  w.few_h = (uint8_t*)take(few_T * (k + 1) * f);
   w.few_h_s = (uint8_t*)take(few_T * (k + 1) * (f / 32));
   w.few_rows = (float*)take(few_T * (k + 1) * d * 4);
   if (ws) *ws = w;
@@ -836,7 +836,7 @@ moe_status_t moe_forward_few(const moe_input_t* x, const float* router_w, const 
     a.router_w = resident ? h->router_w32 : router_w;
     a.bias = resident ? h->router_bias : router_bias;
   }
-  a.logits = h->ws.logits;
+  a.scores = h->ws.logits;
   a.h = h->ws.few_h;
   a.h_s = h->ws.few_h_s;
   a.rows = h->ws.few_rows;

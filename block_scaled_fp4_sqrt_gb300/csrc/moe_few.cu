@@ -16,15 +16,16 @@
 //  3. A down item's rows, times their routing weight, go to fp32 rows [token][choice][d]; the last item of a
 //     (64 columns, token) pair sums the token's rows in order (choices, then the shared expert) and rounds once.
 //
-// A block: 1 producer warp (TMA: stages of 64 weight rows x 512, 16 KB with 64-byte swizzle, and their scale atoms, two copies a stage), 16
-// product warps (4 row tiles x 4 ways of splitting the K groups), 3 epilogue warps.
+// A block: 1 producer warp (TMA: stages of 64 weight rows x 512, 16 KB with 64-byte swizzle, and their scale atoms,
+// two copies a stage), 16 product warps (4 row tiles x the stage's 4 K groups), 3 epilogue warps, and 4 warps that
+// bring the h slices of down stages into the ring.
 //
 // Products run on mma.sync m16n8k16 with the weight rows as M and up to 8 tokens as N: E2M1 weights become fp16 by
-// one conversion a pair (exact), x and h are held as fp16 (their E4M3 codes, x with its block scales folded in:
-// exact down to 2^-22 of the token's maximum, far below the fp32 sums' rounding), and the product of each block of
-// 32 is scaled in fp32.  tcgen05 would spend its 128-row operand on at most 8 tokens, and its issue chain and
-// accumulator hand-over are what bounds moe_forward's items here; mma.sync needs 16 of the 47 cycles that a
-// sub-partition has per 16 x 32 weights at full HBM rate.
+// one conversion a pair (exact); x and h are fp16 too: their E4M3 codes with the block scales folded in relative to
+// the row's largest (exact down to 2^-22 of the row's maximum, far below the fp32 sums' rounding).  The product of
+// each block of 32 is scaled by the weights' E8M0 byte in fp32.  tcgen05 would spend its 128-row operand on at most
+// 8 tokens, and its issue chain and accumulator hand-over are what bounds moe_forward's items at these sizes;
+// mma.sync needs 16 of the 47 cycles that a sub-partition has per 16 x 32 weights at full HBM rate.
 #include <float.h>
 
 #include <algorithm>
@@ -37,34 +38,41 @@ namespace moe {
 namespace {
 
 constexpr int kMaxT = kFewMaxT;
-constexpr int kMmaWarps = 16, kEpiWarps = 3;          // 20 warps with the producer: five a sub-partition
+constexpr int kMmaWarps = 16, kEpiWarps = 3, kHWarps = 4;
+constexpr int kThreads = 32 * (kMmaWarps + kEpiWarps + kHWarps + 1);  // 24 warps, six a sub-partition
+constexpr int kProducer = kMmaWarps + kEpiWarps + kHWarps;
 constexpr int kEpiTok = (kFewMaxT + kEpiWarps - 1) / kEpiWarps;
-constexpr int kThreads = 32 * (kMmaWarps + kEpiWarps + 1);
-constexpr int kTileBytes = 64 * 64;                     // 64 weight rows x 128 E2M1
-constexpr int kStageKg = 4;                             // K groups of 128 in a stage, one to a K split
-constexpr int kStageBytes = kStageKg * (kTileBytes + 2 * kSfAtomBytes);
-constexpr int kStageSf = kStageKg * kTileBytes;         // the scale atoms follow the codes
+constexpr int kTileBytes = 64 * 64;              // 64 weight rows x 128 E2M1
+constexpr int kStageKg = 4;                      // K groups of 128 in a stage, one to a K split
+constexpr int kStageSf = kStageKg * kTileBytes;  // a stage: codes, then scale atoms, then h rows
+constexpr int kStageH = kStageSf + kStageKg * 2 * kSfAtomBytes;
+constexpr int kHPitch = kStageKg * 128 * 2 + 64;  // bytes of a token's h slice: two tokens a phase, no conflicts
 constexpr int kMaxK = 16;
 constexpr int kMaxSlots = kFewMaxSlots;
-constexpr int kRedStride = 9;                           // floats a row of the partial products (8 tokens)
+constexpr int kRedStride = 9;                    // floats a row of the partial products (8 tokens)
 constexpr int kRedFloats = 4 * 64 * kRedStride;
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 10;
+constexpr int kFxItems = 16;                     // items in flight: at most the ring's and the two partial buffers'
+static_assert(kMaxStages + 2 < kFxItems, "a row factor must outlive its item");
+
+__host__ __device__ constexpr int stage_bytes(int T) { return kStageH + (T * kHPitch + 1023) / 1024 * 1024; }
 
 struct Shared {  // fixed-size part of the block's shared memory
   uint64_t full[kMaxStages], empty[kMaxStages], red_full[2], red_empty[2];
   float red[2][kRedFloats];      // [buffer][K split][row][token]
-  float part[kMmaWarps][2][kMaxT];
+  float part[kMmaWarps][2 * kMaxT];
   float fx[kMaxT];               // x = fp16 value * fx
+  float hfx[kFxItems][kMaxT];    // h = fp16 value * hfx, by item and token of the slot
   float w[kMaxT][kMaxK];
   int ids[kMaxT][kMaxK];
   int e_max[kMaxT];
-  int rows_of[kMaxT];            // expert rows the token's sum consists of
   uint32_t taken[kMaxT];         // choices j that are rows of their own (a repeated id joins its first choice)
   uint32_t touched[32];
+  int before[32];                // experts touched in lower words
   int n_slots;
   int abort;
   int slot_expert[kMaxSlots];    // -1: the shared expert
-  int slot_cnt[kMaxSlots];
+  uint32_t slot_mask[kMaxSlots]; // its tokens
   int slot_ready[kMaxSlots];
   uint8_t slot_tok[kMaxSlots][kMaxT];
   uint8_t slot_j[kMaxSlots][kMaxT];
@@ -168,23 +176,43 @@ struct Waiter {
 };
 
 template <int NPL>
-__device__ __forceinline__ void select_token(const float* __restrict__ logits, const float* __restrict__ bias, int E,
+__device__ __forceinline__ void select_token(const float* __restrict__ score, const float* __restrict__ bias, int E,
                                              int k, float route_scale, int32_t* ids, float* w) {
   const int lane = threadIdx.x & 31;
-  float l[NPL], sc[NPL], sel[NPL];
+  float sc[NPL], sel[NPL];
 #pragma unroll
   for (int i = 0; i < NPL; ++i) {
     const int e = lane + 32 * i;
-    l[i] = e < E ? __ldcg(logits + e) : 0.f;
+    sc[i] = e < E ? __ldcg(score + e) : 0.f;
     sel[i] = e < E ? __ldg(bias + e) : 0.f;
   }
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const bool in = lane + 32 * i < E;
-    sc[i] = in ? sqrtf(softplus_f(l[i])) : 0.f;
-    sel[i] = in ? sc[i] + sel[i] : -FLT_MAX;
-  }
+  for (int i = 0; i < NPL; ++i) sel[i] = lane + 32 * i < E ? sc[i] + sel[i] : -FLT_MAX;
   warp_route_topk<NPL>(sc, sel, E, k, route_scale, ids, w);
+}
+
+// The sums over the warp of 16 values a lane: value i's total ends up in lanes 2 i and 2 i + 1 (16 shuffles).
+__device__ __forceinline__ float warp_sum16(const float (&v)[16]) {
+  const int lane = threadIdx.x & 31;
+  float a[8], b[4], c[2];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float keep = lane & 16 ? v[i + 8] : v[i], give = lane & 16 ? v[i] : v[i + 8];
+    a[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 16);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float keep = lane & 8 ? a[i + 4] : a[i], give = lane & 8 ? a[i] : a[i + 4];
+    b[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 8);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float keep = lane & 4 ? b[i + 2] : b[i], give = lane & 4 ? b[i] : b[i + 2];
+    c[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 4);
+  }
+  const float keep = lane & 2 ? c[1] : c[0], give = lane & 2 ? c[0] : c[1];
+  const float s = keep + __shfl_xor_sync(0xFFFFFFFFu, give, 2);
+  return s + __shfl_xor_sync(0xFFFFFFFFu, s, 1);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -195,18 +223,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const FewArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* s_x = ring + a.stages * kStageBytes;  // [T][2 d + 64]: the token's fp16 values
-  const int x_pitch = 2 * a.d + 64;              // 64 bytes off a multiple of 128: two tokens a phase, no conflicts
-  Shared& sh = *reinterpret_cast<Shared*>(s_x + a.T * x_pitch);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int T = a.T, E = a.E, k = a.k, d = a.d, f = a.f;
+  const int kStageBytes = stage_bytes(T);
+  uint8_t* s_x = ring + a.stages * kStageBytes;  // [T][2 d + 64]: the token's fp16 values
+  const int x_pitch = 2 * d + 64;                // 64 bytes off a multiple of 128: two tokens a phase, no conflicts
+  Shared& sh = *reinterpret_cast<Shared*>(s_x + T * x_pitch);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Waiter wait{&sh, a.status, a.budget_ns};
 
-  // ---------------------------------------------------------------- set-up
-  if (tid == 0) {
+  // ---------------------------------------------------------------- set-up (the warps that compute no logits)
+  if (tid == kProducer * 32) {
     for (int i = 0; i < a.stages; ++i) {
-      mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], kMmaWarps);
+      mbar_init(&sh.full[i], 2);
+      mbar_init(&sh.empty[i], kMmaWarps + kHWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.red_full[i], kMmaWarps);
@@ -215,19 +244,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_fence_init();
     sh.abort = 0;
   }
-  if (tid < kMaxT) sh.e_max[tid] = -200;
-  for (int i = tid; i < 32; i += kThreads) sh.touched[i] = 0u;
-  for (int i = tid; i < kMaxSlots; i += kThreads) sh.slot_ready[i] = 0;
-  __syncthreads();
+  if (warp == kMmaWarps) {
+    sh.touched[lane] = 0u;
+    if (lane < kMaxT) sh.taken[lane] = 0u;
+  }
+  if (warp > kMmaWarps)
+    for (int i = tid - (kMmaWarps + 1) * 32; i < kMaxSlots; i += kThreads - (kMmaWarps + 1) * 32) {
+      sh.slot_ready[i] = 0;
+      sh.slot_mask[i] = 0u;
+    }
 
-  // ---------------------------------------------------------------- router logits and x
-  // Thread (warp, lane) holds 8 columns at 256 warp + 8 lane of every 4096; four lanes share an MX block.
+  // ---------------------------------------------------------------- router scores
+  // Thread (warp, lane) holds 8 columns at 256 warp + 8 lane of every 4096.  The raw x rows are left where their
+  // fp16 form will be.
   if (warp < kMmaWarps) {
+    if (tid < kMaxT) sh.e_max[tid] = -200;
     for (int e0 = blockIdx.x, first = 1; first || (a.router_w && e0 < E); e0 += 2 * gridDim.x, first = 0) {
       const bool has0 = a.router_w && e0 < E, has1 = a.router_w && e0 + (int)gridDim.x < E;
-      float acc[2][kMaxT];
+      float acc[2 * kMaxT];
 #pragma unroll
-      for (int t = 0; t < kMaxT; ++t) acc[0][t] = acc[1][t] = 0.f;
+      for (int t = 0; t < 2 * kMaxT; ++t) acc[t] = 0.f;
       for (int base = 0; base < d; base += kMmaWarps * 256) {
         const int c = base + warp * 256 + lane * 8;
         const bool in = c < d;
@@ -246,68 +282,70 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int t = 0; t < kMaxT; ++t) {
           if (t >= T) continue;
+          if (first && in) *reinterpret_cast<uint4*>(s_x + t * x_pitch + 2 * c) = raw[t];
           float v[8];
           bf16x8_to_f32(raw[t], v);
 #pragma unroll
           for (int z = 0; z < 2; ++z) {
-            acc[z][t] = fmaf(w[z][0].x, v[0], acc[z][t]);
-            acc[z][t] = fmaf(w[z][0].y, v[1], acc[z][t]);
-            acc[z][t] = fmaf(w[z][0].z, v[2], acc[z][t]);
-            acc[z][t] = fmaf(w[z][0].w, v[3], acc[z][t]);
-            acc[z][t] = fmaf(w[z][1].x, v[4], acc[z][t]);
-            acc[z][t] = fmaf(w[z][1].y, v[5], acc[z][t]);
-            acc[z][t] = fmaf(w[z][1].z, v[6], acc[z][t]);
-            acc[z][t] = fmaf(w[z][1].w, v[7], acc[z][t]);
-          }
-          if (first) {  // the raw row waits in its place for the token's largest block exponent
-            float amax = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-            const int e = __reduce_max_sync(0xFFFFFFFFu, amax > 0.f ? mxfp8_block_exp(amax) : -127);
-            if (lane == 0) atomicMax(&sh.e_max[t], e);
-            if (in) *reinterpret_cast<uint4*>(s_x + t * x_pitch + 2 * c) = raw[t];
+            float& s = acc[z * kMaxT + t];
+            s = fmaf(w[z][0].x, v[0], s);
+            s = fmaf(w[z][0].y, v[1], s);
+            s = fmaf(w[z][0].z, v[2], s);
+            s = fmaf(w[z][0].w, v[3], s);
+            s = fmaf(w[z][1].x, v[4], s);
+            s = fmaf(w[z][1].y, v[5], s);
+            s = fmaf(w[z][1].z, v[6], s);
+            s = fmaf(w[z][1].w, v[7], s);
           }
         }
       }
       if (a.router_w) {
-#pragma unroll
-        for (int z = 0; z < 2; ++z)
-#pragma unroll
-          for (int t = 0; t < kMaxT; ++t) {
-            if (t >= T) continue;
-            float v = acc[z][t];
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
-            if (lane == 0) sh.part[warp][z][t] = v;
-          }
+        const float v = warp_sum16(acc);
+        if (!(lane & 1)) sh.part[warp][lane >> 1] = v;
         asm volatile("bar.sync 1, %0;" ::"n"(kMmaWarps * 32) : "memory");
         if (tid < 2 * kMaxT) {
           const int z = tid / kMaxT, t = tid % kMaxT;
           if (t < T && (z ? has1 : has0)) {
-            float v = 0.f;
+            float l = 0.f;
 #pragma unroll
-            for (int i = 0; i < kMmaWarps; ++i) v += sh.part[i][z][t];
-            __stcg(a.logits + (size_t)t * E + e0 + z * gridDim.x, v);
+            for (int i = 0; i < kMmaWarps; ++i) l += sh.part[i][tid];
+            __stcg(a.scores + (size_t)t * E + e0 + z * gridDim.x, sqrtf(softplus_f(l)));
+            __threadfence();
           }
         }
         asm volatile("bar.sync 1, %0;" ::"n"(kMmaWarps * 32) : "memory");
       }
     }
-    __threadfence();
+    if (!a.router_w)
+      asm volatile("bar.sync 1, %0;" ::"n"(kMmaWarps * 32) : "memory");  // e_max is set (above: the sums' barriers)
+    else if (tid == 0)
+      atomicAdd(a.counters + kFewScoresDone, 1);
+    // x: the largest block exponent of each token (a warp's 256 columns at a time) ..
+    for (int base = 0; base < d; base += kMmaWarps * 256) {
+      const int c = base + warp * 256 + lane * 8;
+      if (c >= d) break;  // d is a multiple of 256
+      for (int t = 0; t < T; ++t) {
+        float v[8];
+        bf16x8_to_f32(*reinterpret_cast<const uint4*>(s_x + t * x_pitch + 2 * c), v);
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+        const int e = __reduce_max_sync(0xFFFFFFFFu, mxfp8_block_exp(amax));
+        if (lane == 0) atomicMax(&sh.e_max[t], e);
+      }
+    }
   }
   __syncthreads();
-  if (a.router_w && tid == 0) atomicAdd(a.counters + kFewLogitsDone, 1);
-  // x: quantise (E4M3 codes and block exponents as moe_permute takes them) and hold as fp16 code * 2^(e - E + 7),
-  // E the token's largest block exponent
+  // .. then its MXFP8 form (the codes and block exponents of moe_permute), held as fp16 code * 2^(e - E + 7) with E
+  // the token's largest block exponent.  Meanwhile the warps that hold no columns select the experts.
   if (warp < kMmaWarps) {
     for (int base = 0; base < d; base += kMmaWarps * 256) {
       const int c = base + warp * 256 + lane * 8;
-      const bool in = c < d;
+      if (c >= d) break;
       for (int t = 0; t < T; ++t) {
         uint8_t* at = s_x + t * x_pitch + 2 * c;
-        const uint4 raw = in ? *reinterpret_cast<const uint4*>(at) : make_uint4(0u, 0u, 0u, 0u);
         float v[8];
-        bf16x8_to_f32(raw, v);
+        bf16x8_to_f32(*reinterpret_cast<const uint4*>(at), v);
         float amax = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
@@ -326,17 +364,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           const __half2 o = __floats2half2_rn(q.x * up, q.y * up);
           h[i] = *reinterpret_cast<const uint32_t*>(&o);
         }
-        if (in) *reinterpret_cast<uint4*>(at) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(at) = make_uint4(h[0], h[1], h[2], h[3]);
       }
     }
-  }
-  if (tid < T) sh.fx[tid] = ldexpf(1.f, sh.e_max[tid] - 7);
-
-  // ---------------------------------------------------------------- selection
-  if (warp < T) {
-    if (!a.router_w) {  // hash layer: the token's table row, ascending
+    if (tid < T) sh.fx[tid] = ldexpf(1.f, sh.e_max[tid] - 7);
+  } else if (warp - kMmaWarps < T) {
+    const int t = warp - kMmaWarps;  // eight warps, up to eight tokens
+    if (!a.router_w) {               // hash layer: the token's table row, ascending
       if (lane == 0) {
-        int v = a.tok[warp];
+        int v = a.tok[t];
         if (v < 0 || v >= a.V) {
           set_status(a.status, DEV_BAD_TOKEN_ID);
           v = 0;
@@ -348,35 +384,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             e = 0;
           }
           int b = j - 1;
-          while (b >= 0 && sh.ids[warp][b] > e) {
-            sh.ids[warp][b + 1] = sh.ids[warp][b];
+          while (b >= 0 && sh.ids[t][b] > e) {
+            sh.ids[t][b + 1] = sh.ids[t][b];
             --b;
           }
-          sh.ids[warp][b + 1] = e;
-          sh.w[warp][j] = a.route_scale / (float)k;
+          sh.ids[t][b + 1] = e;
+          sh.w[t][j] = a.route_scale / (float)k;
         }
       }
     } else {
       bool ok = true;
-      if (lane == 0) ok = wait.count(a.counters + kFewLogitsDone, (int)gridDim.x);
-      ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
-      if (ok) {
-        const float* l = a.logits + (size_t)warp * E;
+      if (lane == 0) ok = wait.count(a.counters + kFewScoresDone, (int)gridDim.x);
+      if (__shfl_sync(0xFFFFFFFFu, (int)ok, 0)) {
+        const float* s = a.scores + (size_t)t * E;
         if (E <= 256)
-          select_token<8>(l, a.bias, E, k, a.route_scale, sh.ids[warp], sh.w[warp]);
+          select_token<8>(s, a.bias, E, k, a.route_scale, sh.ids[t], sh.w[t]);
         else
-          select_token<16>(l, a.bias, E, k, a.route_scale, sh.ids[warp], sh.w[warp]);
+          select_token<16>(s, a.bias, E, k, a.route_scale, sh.ids[t], sh.w[t]);
+      } else {
+        if (lane < k) sh.ids[t][lane] = 0;  // the call fails; keep what follows in range
       }
     }
     __syncwarp();
-    if (lane < k && !*(volatile int*)&sh.abort) {
-      const int e = sh.ids[warp][lane];
-      const float w = sh.w[warp][lane];
+    if (lane < k) {
+      const int e = sh.ids[t][lane];
+      const float w = sh.w[t][lane];
       if (blockIdx.x == 0) {
-        a.ws_ids[warp * k + lane] = e;
-        a.ws_w[warp * k + lane] = w;
-        if (a.out_ids) a.out_ids[warp * k + lane] = e;
-        if (a.out_w) a.out_w[warp * k + lane] = w;
+        a.ws_ids[t * k + lane] = e;
+        a.ws_w[t * k + lane] = w;
+        if (a.out_ids) a.out_ids[t * k + lane] = e;
+        if (a.out_w) a.out_w[t * k + lane] = w;
       }
       atomicOr(&sh.touched[e >> 5], 1u << (e & 31));
     }
@@ -384,57 +421,47 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   // ---------------------------------------------------------------- slots: the shared expert, then experts ascending
   const int has_shared = a.has_shared;
-  if (!sh.abort) {
-    if (warp == 0) {
-      const uint32_t bits = sh.touched[lane];
-      int before = __popc(bits);
+  if (warp == 0) {
+    const uint32_t bits = sh.touched[lane];
+    int incl = __popc(bits);
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xFFFFFFFFu, before, off);
-        if (lane >= off) before += o;
-      }
-      if (lane == 31) sh.n_slots = before + has_shared;
-      int slot = before - __popc(bits) + has_shared;
-      for (uint32_t m = bits; m; m &= m - 1) sh.slot_expert[slot++] = lane * 32 + __ffs(m) - 1;
-      if (has_shared && lane == 0) {
-        sh.slot_expert[0] = -1;
-        sh.slot_cnt[0] = T;
-      }
-      if (has_shared && lane < T) {
-        sh.slot_tok[0][lane] = (uint8_t)lane;
-        sh.slot_j[0][lane] = (uint8_t)k;
-      }
-      // a token's repeated ids (only a faulty hash table has any) join their first choice
-      if (lane < T) {
-        uint32_t own = 0;
-        for (int j = 0; j < k; ++j) {
-          if (j && sh.ids[lane][j] == sh.ids[lane][j - 1]) {
-            int z = j - 1;
-            while (!((own >> z) & 1u)) --z;
-            sh.w[lane][z] += sh.w[lane][j];
-          } else {
-            own |= 1u << j;
-          }
-        }
-        sh.taken[lane] = own;
-        sh.rows_of[lane] = __popc(own) + has_shared;
-      }
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+      if (lane >= off) incl += o;
     }
-    __syncthreads();
-    for (int s = has_shared + tid; s < sh.n_slots; s += kThreads) {
-      const int e = sh.slot_expert[s];
-      int n = 0;
-      for (int t = 0; t < T; ++t)
-        for (int j = 0; j < k; ++j)
-          if (((sh.taken[t] >> j) & 1u) && sh.ids[t][j] == e) {
-            sh.slot_tok[s][n] = (uint8_t)t;
-            sh.slot_j[s][n] = (uint8_t)j;
-            ++n;
-          }
-      sh.slot_cnt[s] = n;
+    sh.before[lane] = incl - __popc(bits) + has_shared;
+    if (lane == 31) sh.n_slots = incl + has_shared;
+  }
+  __syncthreads();
+  // a thread per (token, choice); a token's repeated ids (only a faulty hash table has any) join their first choice
+  const int pt = tid / kMaxK, pj = tid % kMaxK;
+  const bool pair = pt < T && pj < k && (pj == 0 || sh.ids[pt][pj] != sh.ids[pt][pj - 1]);
+  int ps = 0;
+  float pw = 0.f;
+  if (pair) {
+    const int e = sh.ids[pt][pj];
+    ps = sh.before[e >> 5] + __popc(sh.touched[e >> 5] & ((1u << (e & 31)) - 1u));
+    sh.slot_expert[ps] = e;
+    atomicOr(&sh.slot_mask[ps], 1u << pt);
+    atomicOr(&sh.taken[pt], 1u << pj);
+    pw = sh.w[pt][pj];
+    for (int z = pj + 1; z < k && sh.ids[pt][z] == e; ++z) pw += sh.w[pt][z];
+  }
+  if (has_shared && tid < T) {
+    sh.slot_tok[0][tid] = (uint8_t)tid;
+    sh.slot_j[0][tid] = (uint8_t)k;
+    if (tid == 0) {
+      sh.slot_expert[0] = -1;
+      sh.slot_mask[0] = (1u << T) - 1u;
     }
   }
   __syncthreads();
+  if (pair) {
+    const int n = __popc(sh.slot_mask[ps] & ((1u << pt) - 1u));
+    sh.slot_tok[ps][n] = (uint8_t)pt;
+    sh.slot_j[ps][n] = (uint8_t)pj;
+    sh.w[pt][pj] = pw;
+  }
   const int aborted = sh.abort;
   __syncthreads();
   if (!aborted) {
@@ -443,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int items_up = S * n_up, items = items_up + S * n_down;
   const int kg_up = d / 128, kg_down = f / 128;
 
-  if (warp == kMmaWarps + kEpiWarps) {
+  if (warp == kProducer) {
     // -------------------------------------------------------------- producer
     if (lane == 0 && !a.stall) {
       const uint64_t policy = l2_policy_evict_first();
@@ -471,6 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(bar, kStageKg * (kTileBytes + 2 * kSfAtomBytes));
             tma_load_5d(dst, map, 0, (q & 3) * 32, 0, q >> 2, ex * KG + kg, bar, policy);
             tma_load_4d(dst + kStageSf, sf, 0, 0, q >> 2, ex * KG + kg, bar);
+            mbar_arrive(bar);  // no h to wait for
           } else {
             mbar_arrive_expect_tx(bar, kStageKg * (kTileBytes + kSfAtomBytes));
             tma_load_4d_hint(dst, map, 0, (q & 3) * 64, q >> 2, ex * KG + kg, bar, policy);
@@ -513,26 +541,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int j = up ? it : it - items_up, per = up ? n_up : n_down;
       const int s = j / per, q = j - s * per;
       const int KG = up ? kg_up : kg_down;
-      const int cnt = sh.slot_cnt[s];
+      const int cnt = __popc(sh.slot_mask[s]);
       const int n = li < cnt ? li : 0;  // this lane's token (columns past the slot's tokens repeat the first)
-      const int tok = sh.slot_tok[s][n], ch = sh.slot_j[s][n];
-      const uint8_t* xrow = s_x + tok * x_pitch + lc * 16;
-      const size_t hrow = (size_t)tok * (k + 1) + ch;
-      const __half* hsrc = a.h + hrow * f + lc * 8;
-      // the scales of the accumulator's columns 2 lc, 2 lc + 1 come from those tokens' rows
-      const int n0 = min(2 * lc, cnt - 1), n1 = min(2 * lc + 1, cnt - 1);
-      const uint8_t* hexp0 = a.h_s + ((size_t)sh.slot_tok[s][n0] * (k + 1) + sh.slot_j[s][n0]) * (f / 32);
-      const uint8_t* hexp1 = a.h_s + ((size_t)sh.slot_tok[s][n1] * (k + 1) + sh.slot_j[s][n1]) * (f / 32);
-      if (!up && !*(volatile int*)&sh.slot_ready[s]) {
-        bool ok = true;
-        if (lane == 0) ok = wait.count(a.counters + kFewSlotDone + s, n_up * cnt);
-        if (!__shfl_sync(0xFFFFFFFFu, (int)ok, 0)) break;
-        if (lane == 0) {
-          __threadfence_block();
-          *(volatile int*)&sh.slot_ready[s] = 1;
-        }
-      }
-      __syncwarp();
+      const uint8_t* xrow = s_x + sh.slot_tok[s][n] * x_pitch + lc * 16;
+      const int hrow = kStageH + n * kHPitch + ks * 256 + lc * 16;
       // scale words of rows li, li + 8: gate-up tiles 0, 1 are gate rows (first atom), 2, 3 up rows (second)
       const int r0 = up ? (mt & 1) * 16 : (mt & 1) * 16, quarter = up ? (q & 3) : ((q & 1) * 2 + (mt >> 1));
       const uint32_t sf_at = kStageSf + (up ? (2 * ks + (mt >> 1)) * kSfAtomBytes : ks * kSfAtomBytes) + (r0 + li) * 16 + quarter * 4;
@@ -549,17 +561,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           next_stage();
           break;
         }
-        uint4 xb[4];
-        uint32_t hs0 = 0, hs1 = 0;
-        if (!up) {
-#pragma unroll
-          for (int b = 0; b < 4; ++b) xb[b] = *reinterpret_cast<const uint4*>(hsrc + kg * 128 + b * 32);
-          hs0 = *reinterpret_cast<const uint32_t*>(hexp0 + kg * 4);
-          hs1 = *reinterpret_cast<const uint32_t*>(hexp1 + kg * 4);
-        } else {
-#pragma unroll
-          for (int b = 0; b < 4; ++b) xb[b] = *reinterpret_cast<const uint4*>(xrow + (kg * 128 + b * 32) * 2);
-        }
         if (!wait.bar(&sh.full[stage], phase)) {
           ok = false;
           break;
@@ -572,6 +573,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ldsm4(smem_addr(st) + ks * kTileBytes + row * 64 + (((2 * p + lblk) ^ ((row >> 1) & 3)) * 16), wa[p]);
         const uint32_t sw0 = *reinterpret_cast<const uint32_t*>(st + sf_at);
         const uint32_t sw1 = *reinterpret_cast<const uint32_t*>(st + sf_at + 8 * 16);
+        const uint8_t* xp = up ? xrow + kg * 256 : st + hrow;
+        uint4 xb[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) xb[b] = *reinterpret_cast<const uint4*>(xp + b * 64);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[stage]);  // everything this warp needs is in registers
 #pragma unroll
@@ -583,18 +588,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_f16_zero(dd, lo[0], hi[0], lo[1], hi[1], xb[b].x, xb[b].y);
           mma_f16(dd, lo[2], hi[2], lo[3], hi[3], xb[b].z, xb[b].w);
           const float w0 = e8m0_float(sw0, b), w1 = e8m0_float(sw1, b);
-          if (up) {
-            acc[0] = fmaf(dd[0], w0, acc[0]);
-            acc[1] = fmaf(dd[1], w0, acc[1]);
-            acc[2] = fmaf(dd[2], w1, acc[2]);
-            acc[3] = fmaf(dd[3], w1, acc[3]);
-          } else {
-            const float h0 = e8m0_float(hs0, b), h1 = e8m0_float(hs1, b);
-            acc[0] = fmaf(dd[0] * h0, w0, acc[0]);
-            acc[1] = fmaf(dd[1] * h1, w0, acc[1]);
-            acc[2] = fmaf(dd[2] * h0, w1, acc[2]);
-            acc[3] = fmaf(dd[3] * h1, w1, acc[3]);
-          }
+          acc[0] = fmaf(dd[0], w0, acc[0]);
+          acc[1] = fmaf(dd[1], w0, acc[1]);
+          acc[2] = fmaf(dd[2], w1, acc[2]);
+          acc[3] = fmaf(dd[3], w1, acc[3]);
         }
         next_stage();
       }
@@ -609,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.red_full[buf]);
     }
-  } else {
+  } else if (warp < kMmaWarps + kEpiWarps) {
     // -------------------------------------------------------------- epilogue
     const int ew = warp - kMmaWarps;
     int n_item = 0;
@@ -617,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool up = it < items_up;
       const int j = up ? it : it - items_up, per = up ? n_up : n_down;
       const int s = j / per, q = j - s * per;
-      const int cnt = sh.slot_cnt[s];
+      const int cnt = __popc(sh.slot_mask[s]);
       const int buf = n_item & 1;
       if (!wait.bar(&sh.red_full[buf], (uint32_t)((n_item >> 1) & 1))) break;
       // token n of this item belongs to warp (n + n_item) % kEpiWarps
@@ -653,22 +650,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
           const int e = mxfp8_block_exp(amax);
           const uint16_t code = e4m3x2(hv * exp2_neg_int(e), 0.f);
-          uint32_t h2;
-          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(code));
-          a.h[row * f + q * 32 + lane] = __low2half(*reinterpret_cast<const __half2*>(&h2));
+          a.h[row * f + q * 32 + lane] = (uint8_t)code;
           if (lane == 0) a.h_s[row * (f / 32) + q] = (uint8_t)(e + 127);
           __threadfence();
           __syncwarp();
           if (lane == 0) atomicAdd(a.counters + kFewSlotDone + s, 1);
         } else {
-          const float w = ch < k ? sh.w[t][ch] : 1.f;
+          const float w = ch < k ? sh.w[t][ch] : 1.f, fx = sh.hfx[n_item % kFxItems][n];
           float* dst = a.rows + row * d + q * 64;
-          __stcg(dst + lane, v0[i] * w);
-          __stcg(dst + 32 + lane, v1[i] * w);
+          __stcg(dst + lane, v0[i] * fx * w);
+          __stcg(dst + 32 + lane, v1[i] * fx * w);
           __threadfence();
           __syncwarp();
           int last = 0;
-          if (lane == 0) last = atomicAdd(a.counters + kFewColsDone + q * kMaxT + t, 1) == sh.rows_of[t] - 1;
+          if (lane == 0) last = atomicAdd(a.counters + kFewColsDone + q * kMaxT + t, 1) == __popc(sh.taken[t]) + has_shared - 1;
           if (__shfl_sync(0xFFFFFFFFu, last, 0)) {  // the token's rows are complete in these columns
             __threadfence();
             const float* src = a.rows + (size_t)t * (k + 1) * d + q * 64 + 2 * lane;
@@ -683,6 +678,79 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             *reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)t * d + q * 64 + 2 * lane) = __floats2bfloat162_rn(y.x, y.y);
           }
+        }
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- h slices of the down stages
+    // Warp i takes every fourth stage: the slot's tokens' next 512 columns of h, as fp16 code * 2^(e - E + 7) with E
+    // the row's largest block exponent.
+    const int hw = warp - kMmaWarps - kEpiWarps;
+    int stage = 0, turn = 0, n_item = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int it = blockIdx.x; it < items && ok; it += gridDim.x, ++n_item) {
+      const bool up = it < items_up;
+      const int j = up ? it : it - items_up, per = up ? n_up : n_down;
+      const int s = j / per, KG = up ? kg_up : kg_down;
+      const uint32_t mask = sh.slot_mask[s];
+      const int cnt = __popc(mask);
+      for (int kg = 0; kg < KG; kg += kStageKg) {
+        // Every warp waits for and releases every stage, up stages and the other warps' included: it can then be
+        // neither ahead of the ring nor a whole turn behind it, where a phase's parity would mislead it.
+        if (lane == 0) ok = wait.bar(&sh.empty[stage], phase ^ 1u);
+        const bool own = !up && (turn++ & (kHWarps - 1)) == hw;
+        if (own && lane == 0 && ok && !*(volatile int*)&sh.slot_ready[s]) {
+          ok = wait.count(a.counters + kFewSlotDone + s, n_up * cnt);
+          __threadfence_block();
+          if (ok) *(volatile int*)&sh.slot_ready[s] = 1;
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
+        if (!ok) break;
+        if (own) {
+          const int c = kg * 128 + lane * 16;  // this lane's 16 columns, half an MX block
+          const bool in = c < f;
+          uint4 code[kMaxT];
+          uint32_t eb[kMaxT], top[kMaxT];
+#pragma unroll
+          for (int n = 0; n < kMaxT; ++n) {
+            if (n >= cnt) continue;
+            const size_t row = (size_t)sh.slot_tok[s][n] * (k + 1) + sh.slot_j[s][n];
+            code[n] = in ? __ldcg(reinterpret_cast<const uint4*>(a.h + row * f + c)) : make_uint4(0u, 0u, 0u, 0u);
+            eb[n] = in ? __ldcg(a.h_s + row * (f / 32) + c / 32) : 0u;
+            uint32_t m = 0;
+            for (int i = lane * 4; i < f / 32; i += 128)
+              m = __vmaxu4(m, __ldcg(reinterpret_cast<const uint32_t*>(a.h_s + row * (f / 32) + i)));
+            top[n] = m;
+          }
+          uint8_t* dst = ring + stage * kStageBytes + kStageH + lane * 32;
+#pragma unroll
+          for (int n = 0; n < kMaxT; ++n) {
+            if (n >= cnt) continue;
+            uint32_t m = __vmaxu2(top[n] & 0x00FF00FFu, (top[n] >> 8) & 0x00FF00FFu);
+            m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+            const int x = (int)eb[n] - (int)m + 7;  // 2^x in fp16, subnormal below -14, 0 below -24
+            const uint32_t p = x >= -14 ? (uint32_t)(x + 15) << 10 : x >= -24 ? 1u << (x + 24) : 0u;
+            const uint32_t p2 = p | (p << 16);
+            const uint32_t cw[4] = {code[n].x, code[n].y, code[n].z, code[n].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              uint32_t h2;
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(cw[i >> 1] >> (16 * (i & 1)))));
+              asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(h2), "r"(p2));
+            }
+            *reinterpret_cast<uint4*>(dst + n * kHPitch) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(dst + n * kHPitch + 16) = make_uint4(o[4], o[5], o[6], o[7]);
+            if (kg == 0 && lane == 0) sh.hfx[n_item % kFxItems][n] = ldexpf(1.f, (int)m - 134);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.full[stage]);
+        }
+        if (lane == 0) mbar_arrive(&sh.empty[stage]);
+        if (++stage == a.stages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
     }
@@ -706,14 +774,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 int few_stages(int T, int d) {
   const long long room = 232448 - 1024 - (long long)sizeof(Shared) - (long long)T * (2 * d + 64);
-  const long long n = room / kStageBytes;
-  return n < 3 ? 0 : (int)std::min<long long>(n, kMaxStages);
+  const long long n = room / stage_bytes(T);
+  return n < 2 ? 0 : (int)std::min<long long>(n, kMaxStages);
 }
 
 cudaError_t launch_few_tokens(const FewMaps& routed, const FewMaps& shared, FewArgs a, int num_sms, cudaStream_t s) {
   a.stages = few_stages(a.T, a.d);
   if (!a.stages) return cudaErrorInvalidValue;
-  const size_t smem = 1024 + (size_t)a.stages * kStageBytes + (size_t)a.T * (2 * a.d + 64) + sizeof(Shared);
+  const size_t smem = 1024 + (size_t)a.stages * stage_bytes(a.T) + (size_t)a.T * (2 * a.d + 64) + sizeof(Shared);
   static PerDeviceOnce once;
   cudaError_t e = once.run(
       [] { return cudaFuncSetAttribute(few_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448); });

@@ -9,7 +9,7 @@ constexpr int kFewMaxT = 8;
 constexpr int kFewMaxSlots = kFewMaxT * 16 + 1;  // touched experts: at most T * top_k, and the shared one
 
 // Counters in the workspace, all zero between calls.
-constexpr int kFewLogitsDone = 0;                          // blocks whose logits are written
+constexpr int kFewScoresDone = 0;                          // blocks whose router scores are written
 constexpr int kFewBlocksDone = 1;                          // blocks that have ended
 constexpr int kFewSlotDone = 2;                            // [slot] h blocks written
 constexpr int kFewColsDone = kFewSlotDone + kFewMaxSlots;  // [d / 64][T] expert rows written in these columns
@@ -21,8 +21,8 @@ struct FewArgs {
   const float* bias;        // [E]
   const int32_t* tok;       // [T] (hash layer)
   const int32_t* table;     // [V, k]
-  float* logits;            // [T, E]
-  __half* h;                // [T, k + 1, f] E4M3 codes as fp16
+  float* scores;            // [T, E] sqrt(softplus(logit))
+  uint8_t* h;               // [T, k + 1, f] E4M3 codes
   uint8_t* h_s;             // [T, k + 1, f / 32]
   float* rows;              // [T, k + 1, d] weighted expert rows
   int* counters;
