@@ -190,7 +190,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
   constexpr int kCols = D / kWarps;            // output columns of a warp: 32 or 16
   constexpr int kNT = kCols / 8;               // 8-column tiles of a warp
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
+  // (pointer arithmetic on the array keeps the accesses below shared-memory ones)
+  uint8_t* smem = smem_raw + ((128u - (smem_addr(smem_raw) & 127u)) & 127u);
   uint8_t* s_q = smem + C::kStages * C::kStageBytes;          // q, bf16 or (MXFP8) fp16
   uint8_t* s_p = C::kQRegs ? s_q : s_q + C::kQBytes;          // p of the current tile
   float* s_mx = reinterpret_cast<float*>(s_q + C::kQPBytes);  // [warp][row]

@@ -16,8 +16,8 @@
 //  3. A down item's rows, times their routing weight, go to fp32 rows [token][choice][d]; the last item of a
 //     (64 columns, token) pair sums the token's rows in order (choices, then the shared expert) and rounds once.
 //
-// A block: 1 producer warp (TMA: stages of 64 weight rows x 512, 16 KB with 64-byte swizzle, and their scale atoms,
-// two copies a stage), 16 product warps (4 row tiles x the stage's 4 K groups), 3 epilogue warps, and 4 warps that
+// A block: 2 producer warps (TMA: stages of 64 weight rows x 512, 16 KB with 64-byte swizzle, and their scale atoms,
+// two copies a stage), 16 product warps (4 row tiles x the stage's 4 K groups), 2 epilogue warps, and 4 warps that
 // bring the h slices of down stages into the ring.
 //
 // Products run on mma.sync m16n8k16 with the weight rows as M and up to 8 tokens as N: E2M1 weights become fp16 by
@@ -38,8 +38,8 @@ namespace moe {
 namespace {
 
 constexpr int kMaxT = kFewMaxT;
-constexpr int kMmaWarps = 16, kEpiWarps = 3, kHWarps = 4;
-constexpr int kThreads = 32 * (kMmaWarps + kEpiWarps + kHWarps + 1);  // 24 warps, six a sub-partition
+constexpr int kMmaWarps = 16, kEpiWarps = 2, kHWarps = 4, kProducers = 2;
+constexpr int kThreads = 32 * (kMmaWarps + kEpiWarps + kHWarps + kProducers);  // 24 warps, six a sub-partition
 constexpr int kProducer = kMmaWarps + kEpiWarps + kHWarps;
 constexpr int kEpiTok = (kFewMaxT + kEpiWarps - 1) / kEpiWarps;
 constexpr int kTileBytes = 64 * 64;              // 64 weight rows x 128 E2M1
@@ -222,7 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap sf13s, const __grid_constant__ CUtensorMap sf2s,
                       const FewArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (pointer arithmetic on the array keeps the accesses below shared-memory ones)
+  uint8_t* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   const int T = a.T, E = a.E, k = a.k, d = a.d, f = a.f;
   const int kStageBytes = stage_bytes(T);
   uint8_t* s_x = ring + a.stages * kStageBytes;  // [T][2 d + 64]: the token's fp16 values
@@ -470,14 +471,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int items_up = S * n_up, items = items_up + S * n_down;
   const int kg_up = d / 128, kg_down = f / 128;
 
-  if (warp == kProducer) {
-    // -------------------------------------------------------------- producer
+  if (warp >= kProducer) {
+    // -------------------------------------------------------------- producers
+    // Two warps take the stages in turn: beside busy product warps one thread's waits and copies do not keep up.  The
+    // ring has an even number of stages, so that a slot always belongs to the same producer.
     if (lane == 0 && !a.stall) {
       const uint64_t policy = l2_policy_evict_first();
-      int stage = 0;
+      const int mine = warp - kProducer;
+      int stage = 0, n = 0;  // ring slot and number of the next stage of the block
       uint32_t phase = 0;
       bool ok = true;
-      int64_t issued = 0;
       for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
         const bool up = it < items_up;
         const int j = up ? it : it - items_up, per = up ? n_up : n_down;
@@ -486,34 +489,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int KG = up ? kg_up : kg_down;
         const CUtensorMap* map = up ? (e < 0 ? &tm13s : &tm13) : (e < 0 ? &tm2s : &tm2);
         const CUtensorMap* sf = up ? (e < 0 ? &sf13s : &sf13) : (e < 0 ? &sf2s : &sf2);
-        const int ex = max(e, 0);
-        for (int kg = 0; kg < KG; kg += kStageKg) {  // a stage past KG brings the next rows along; nobody reads them
-          if (!wait.bar(&sh.empty[stage], phase ^ 1u)) {
-            ok = false;
-            break;
+        const int c1 = up ? (q & 3) * 32 : (q & 3) * 64, c3 = q >> 2, half = up ? 0 : (q & 3) >> 1;
+        int row = max(e, 0) * KG;  // the K group's row of the maps
+        // a stage past KG brings the next rows along; nobody reads them
+        for (int kg = 0; kg < KG; kg += kStageKg, row += kStageKg, ++n) {
+          if ((n & 1) == mine) {
+            if (!wait.bar(&sh.empty[stage], phase ^ 1u)) {
+              ok = false;
+              break;
+            }
+            uint8_t* dst = ring + stage * kStageBytes;
+            uint64_t* bar = &sh.full[stage];
+            if (up) {
+              mbar_arrive_expect_tx(bar, kStageKg * (kTileBytes + 2 * kSfAtomBytes));
+              tma_load_5d(dst, map, 0, c1, 0, c3, row, bar, policy);
+              tma_load_4d(dst + kStageSf, sf, 0, 0, c3, row, bar);
+              mbar_arrive(bar);  // no h to wait for
+            } else {
+              mbar_arrive_expect_tx(bar, kStageKg * (kTileBytes + kSfAtomBytes));
+              tma_load_4d_hint(dst, map, 0, c1, c3, row, bar, policy);
+              tma_load_4d(dst + kStageSf, sf, 0, half, c3, row, bar);
+            }
           }
-          uint8_t* dst = ring + stage * kStageBytes;
-          uint64_t* bar = &sh.full[stage];
-          if (up) {
-            mbar_arrive_expect_tx(bar, kStageKg * (kTileBytes + 2 * kSfAtomBytes));
-            tma_load_5d(dst, map, 0, (q & 3) * 32, 0, q >> 2, ex * KG + kg, bar, policy);
-            tma_load_4d(dst + kStageSf, sf, 0, 0, q >> 2, ex * KG + kg, bar);
-            mbar_arrive(bar);  // no h to wait for
-          } else {
-            mbar_arrive_expect_tx(bar, kStageKg * (kTileBytes + kSfAtomBytes));
-            tma_load_4d_hint(dst, map, 0, (q & 3) * 64, q >> 2, ex * KG + kg, bar, policy);
-            tma_load_4d(dst + kStageSf, sf, 0, (q & 3) >> 1, q >> 2, ex * KG + kg, bar);
-          }
-          ++issued;
           if (++stage == a.stages) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      // copies in flight must land before the block ends: every stage issued last must have completed its phase
-      const int64_t tail = issued < a.stages ? issued : a.stages;
-      for (int64_t i = issued - tail; i < issued; ++i) {
+      // copies in flight must land before the block ends: this producer's stages issued last must have completed
+      for (int i = max(n - a.stages, 0); i < n; ++i) {
+        if ((i & 1) != mine) continue;
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait_suspend(&sh.full[i % a.stages], (uint32_t)((i / a.stages) & 1), 20000u))
           if (globaltimer_ns() - t0 > a.budget_ns) {
@@ -775,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 int few_stages(int T, int d) {
   const long long room = 232448 - 1024 - (long long)sizeof(Shared) - (long long)T * (2 * d + 64);
   const long long n = room / stage_bytes(T);
-  return n < 2 ? 0 : (int)std::min<long long>(n, kMaxStages);
+  return n < 2 ? 0 : (int)std::min<long long>(n, kMaxStages) & ~1;  // an even number: see the producers
 }
 
 cudaError_t launch_few_tokens(const FewMaps& routed, const FewMaps& shared, FewArgs a, int num_sms, cudaStream_t s) {
