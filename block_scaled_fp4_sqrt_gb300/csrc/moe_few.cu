@@ -17,7 +17,8 @@
 //     (64 columns, token) pair sums the token's rows in order (choices, then the shared expert) and rounds once.
 //
 // A block: 2 producer warps (TMA: stages of 64 weight rows x 512, 16 KB with 64-byte swizzle, and their scale atoms,
-// two copies a stage), 16 product warps (4 row tiles x the stage's 4 K groups), 2 epilogue warps, and 4 warps that
+// two copies a stage), 16 product warps (two
+// groups that take the stages in turn; in a group the stage's 4 K groups x 2 pairs of row tiles), 2 epilogue warps, and 4 warps that
 // bring the h slices of down stages into the ring.
 //
 // Products run on mma.sync m16n8k16 with the weight rows as M and up to 8 tokens as N: E2M1 weights become fp16 by
@@ -43,14 +44,17 @@ constexpr int kThreads = 32 * (kMmaWarps + kEpiWarps + kHWarps + kProducers);  /
 constexpr int kProducer = kMmaWarps + kEpiWarps + kHWarps;
 constexpr int kEpiTok = (kFewMaxT + kEpiWarps - 1) / kEpiWarps;
 constexpr int kTileBytes = 64 * 64;              // 64 weight rows x 128 E2M1
-constexpr int kStageKg = 4;                      // K groups of 128 in a stage, one to a K split
+constexpr int kStageKg = 4;                      // K groups of 128 in a stage
+constexpr int kGroups = 2;                       // product groups
+constexpr int kGroupWarps = kMmaWarps / kGroups; // one K group of a stage and half of the rows each
+constexpr int kSplits = kGroups * kStageKg;      // K splits of an item's sums
 constexpr int kStageSf = kStageKg * kTileBytes;  // a stage: codes, then scale atoms, then h rows
 constexpr int kStageH = kStageSf + kStageKg * 2 * kSfAtomBytes;
 constexpr int kHPitch = kStageKg * 128 * 2 + 64;  // bytes of a token's h slice: two tokens a phase, no conflicts
 constexpr int kMaxK = 16;
 constexpr int kMaxSlots = kFewMaxSlots;
 constexpr int kRedStride = 9;                    // floats a row of the partial products (8 tokens)
-constexpr int kRedFloats = 4 * 64 * kRedStride;
+constexpr int kRedFloats = kSplits * 64 * kRedStride;
 constexpr int kMaxStages = 10;
 constexpr int kFxItems = 16;                     // items in flight: at most the ring's and the two partial buffers'
 static_assert(kMaxStages + 2 < kFxItems, "a row factor must outlive its item");
@@ -59,7 +63,6 @@ __host__ __device__ constexpr int stage_bytes(int T) { return kStageH + (T * kHP
 
 struct Shared {  // fixed-size part of the block's shared memory
   uint64_t full[kMaxStages], empty[kMaxStages], red_full[2], red_empty[2];
-  float red[2][kRedFloats];      // [buffer][K split][row][token]
   float part[kMmaWarps][2 * kMaxT];
   float fx[kMaxT];               // x = fp16 value * fx
   float hfx[kFxItems][kMaxT];    // h = fp16 value * hfx, by item and token of the slot
@@ -110,6 +113,17 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 // E8M0 byte j of w as a float (byte 0, 2^-127, reads as 0).
 __device__ __forceinline__ float e8m0_float(uint32_t w, int j) {
   return __uint_as_float(j == 3 ? (w >> 1) & 0x7F800000u : (w << (23 - 8 * j)) & 0x7F800000u);
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, int c4,
@@ -228,7 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kStageBytes = stage_bytes(T);
   uint8_t* s_x = ring + a.stages * kStageBytes;  // [T][2 d + 64]: the token's fp16 values
   const int x_pitch = 2 * d + 64;                // 64 bytes off a multiple of 128: two tokens a phase, no conflicts
-  Shared& sh = *reinterpret_cast<Shared*>(s_x + T * x_pitch);
+  float* s_red = reinterpret_cast<float*>(s_x + T * x_pitch);  // [buffer][K split][row][token] partial products
+  Shared& sh = *reinterpret_cast<Shared*>(s_red + (a.red_shift + 1) * kRedFloats);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Waiter wait{&sh, a.status, a.budget_ns};
 
@@ -236,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == kProducer * 32) {
     for (int i = 0; i < a.stages; ++i) {
       mbar_init(&sh.full[i], 2);
-      mbar_init(&sh.empty[i], kMmaWarps + kHWarps);
+      mbar_init(&sh.empty[i], kGroupWarps + kHWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.red_full[i], kMmaWarps);
@@ -530,17 +545,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp < kMmaWarps) {
     // -------------------------------------------------------------- products
-    const int mt = warp & 3, ks = warp >> 2;  // row tile, K split
+    // Group grp takes every second stage of the block; the ring's stages are even in number, so that a slot always
+    // belongs to the same group, which sees each of its phases.  While one group waits and loads, the other computes.
+    const int grp = warp / kGroupWarps, ks = warp % kGroupWarps >> 1, mh = warp & 1;  // K group of a stage, row half
     const int li = lane >> 2, lc = lane & 3;
     const int lrow = lane & 15, lblk = lane >> 4;  // ldmatrix address: rows 0..15 of the tile, block pair member
-    int stage = 0;
+    int stage = grp, next = grp;  // ring slot and number of this group's next stage
     uint32_t phase = 0;
-    auto next_stage = [&]() {
-      if (++stage == a.stages) {
-        stage = 0;
-        phase ^= 1u;
-      }
-    };
+    int first = 0;                // number of the item's first stage
     int n_item = 0;
     for (int it = blockIdx.x; it < items; it += gridDim.x, ++n_item) {
       const bool up = it < items_up;
@@ -551,64 +563,79 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = li < cnt ? li : 0;  // this lane's token (columns past the slot's tokens repeat the first)
       const uint8_t* xrow = s_x + sh.slot_tok[s][n] * x_pitch + lc * 16;
       const int hrow = kStageH + n * kHPitch + ks * 256 + lc * 16;
-      // scale words of rows li, li + 8: gate-up tiles 0, 1 are gate rows (first atom), 2, 3 up rows (second)
-      const int r0 = up ? (mt & 1) * 16 : (mt & 1) * 16, quarter = up ? (q & 3) : ((q & 1) * 2 + (mt >> 1));
-      const uint32_t sf_at = kStageSf + (up ? (2 * ks + (mt >> 1)) * kSfAtomBytes : ks * kSfAtomBytes) + (r0 + li) * 16 + quarter * 4;
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      // Scale words of rows li, li + 8 of the warp's two row tiles: the row half is the gate (first atom) or the up rows
+      // (second), or 32 of a down item's rows.
+      const int quarter = up ? (q & 3) : (q & 1) * 2 + mh;
+      const uint32_t sf_at = smem_addr(ring) + kStageSf + (up ? (2 * ks + mh) * kSfAtomBytes : ks * kSfAtomBytes) +
+                             li * 16 + quarter * 4;
+      const uint32_t row_at = smem_addr(ring) + ks * kTileBytes + (mh * 32 + lrow) * 64;
+      const uint32_t x_at = smem_addr(xrow) + ks * 256, h_at = smem_addr(ring) + hrow;
+      const int n_st = (KG + kStageKg - 1) / kStageKg;
+      float acc[2][4];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
       bool ok = true;
-      for (int kg = ks; kg - ks < KG; kg += kStageKg) {
-        if (kg >= KG) {  // this split has no part in the last stage
-          if (!wait.bar(&sh.full[stage], phase)) {
-            ok = false;
-            break;
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.empty[stage]);
-          next_stage();
-          break;
-        }
+      for (; next < first + n_st; next += kGroups) {
         if (!wait.bar(&sh.full[stage], phase)) {
           ok = false;
           break;
         }
-        const uint8_t* st = ring + stage * kStageBytes;
-        uint32_t wa[2][4];
-        const int row = mt * 16 + lrow;
-#pragma unroll
-        for (int p = 0; p < 2; ++p)  // blocks 2 p, 2 p + 1: [rows 0..7, 8..15] of each
-          ldsm4(smem_addr(st) + ks * kTileBytes + row * 64 + (((2 * p + lblk) ^ ((row >> 1) & 3)) * 16), wa[p]);
-        const uint32_t sw0 = *reinterpret_cast<const uint32_t*>(st + sf_at);
-        const uint32_t sw1 = *reinterpret_cast<const uint32_t*>(st + sf_at + 8 * 16);
-        const uint8_t* xp = up ? xrow + kg * 256 : st + hrow;
+        const uint32_t off = stage * kStageBytes;
+        const int kg = (next - first) * kStageKg + ks;  // this warp's K group; the last stage may not have it
+        uint32_t wa[2][2][4], sw[2][2];
         uint4 xb[4];
+        if (kg < KG) {
+          const uint32_t xp = up ? x_at + (next - first) * (kStageKg * 256) : h_at + off;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) xb[b] = *reinterpret_cast<const uint4*>(xp + b * 64);
+          for (int m = 0; m < 2; ++m) {
+            const int sz = (lrow >> 1) & 3;  // 64-byte swizzle
+#pragma unroll
+            for (int p = 0; p < 2; ++p)  // blocks 2 p, 2 p + 1: [rows 0..7, 8..15] of each
+              ldsm4(row_at + off + m * 16 * 64 + (((2 * p + lblk) ^ sz) * 16), wa[m][p]);
+            sw[m][0] = lds32(sf_at + off + m * 16 * 16);
+            sw[m][1] = lds32(sf_at + off + m * 16 * 16 + 8 * 16);
+          }
+#pragma unroll
+          for (int b = 0; b < 4; ++b) xb[b] = lds128(xp + b * 64);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.empty[stage]);  // everything this warp needs is in registers
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          uint32_t lo[4], hi[4];
-          e2m1_f16(wa[b >> 1][2 * (b & 1)], lo);
-          e2m1_f16(wa[b >> 1][2 * (b & 1) + 1], hi);
-          float dd[4];
-          mma_f16_zero(dd, lo[0], hi[0], lo[1], hi[1], xb[b].x, xb[b].y);
-          mma_f16(dd, lo[2], hi[2], lo[3], hi[3], xb[b].z, xb[b].w);
-          const float w0 = e8m0_float(sw0, b), w1 = e8m0_float(sw1, b);
-          acc[0] = fmaf(dd[0], w0, acc[0]);
-          acc[1] = fmaf(dd[1], w0, acc[1]);
-          acc[2] = fmaf(dd[2], w1, acc[2]);
-          acc[3] = fmaf(dd[3], w1, acc[3]);
+        if ((stage += kGroups) == a.stages + grp) {
+          stage = grp;
+          phase ^= 1u;
         }
-        next_stage();
+        if (kg >= KG) continue;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            uint32_t lo[4], hi[4];
+            e2m1_f16(wa[m][b >> 1][2 * (b & 1)], lo);
+            e2m1_f16(wa[m][b >> 1][2 * (b & 1) + 1], hi);
+            float dd[4];
+            mma_f16_zero(dd, lo[0], hi[0], lo[1], hi[1], xb[b].x, xb[b].y);
+            mma_f16(dd, lo[2], hi[2], lo[3], hi[3], xb[b].z, xb[b].w);
+            const float w0 = e8m0_float(sw[m][0], b), w1 = e8m0_float(sw[m][1], b);
+            acc[m][0] = fmaf(dd[0], w0, acc[m][0]);
+            acc[m][1] = fmaf(dd[1], w0, acc[m][1]);
+            acc[m][2] = fmaf(dd[2], w1, acc[m][2]);
+            acc[m][3] = fmaf(dd[3], w1, acc[m][3]);
+          }
       }
+      // The split is counted from the item's first stage: a row's sum does not depend on where the item came in the
+      // block's sequence.
+      const int split = ((grp + first) & (kGroups - 1)) * kStageKg + ks;
+      first += n_st;
       if (!ok) break;
-      const int buf = n_item & 1;
-      if (!wait.bar(&sh.red_empty[buf], (uint32_t)(((n_item >> 1) & 1) ^ 1))) break;
-      float* red = sh.red[buf] + (ks * 64 + mt * 16 + li) * kRedStride + 2 * lc;
-      red[0] = acc[0];
-      red[1] = acc[1];
-      red[8 * kRedStride] = acc[2];
-      red[8 * kRedStride + 1] = acc[3];
+      const int buf = n_item & a.red_shift;
+      if (!wait.bar(&sh.red_empty[buf], (uint32_t)(((n_item >> a.red_shift) & 1) ^ 1))) break;
+      float* red = s_red + buf * kRedFloats + (split * 64 + mh * 32 + li) * kRedStride + 2 * lc;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) red[(m * 16 + (i >> 1) * 8) * kRedStride + (i & 1)] = acc[m][i];
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.red_full[buf]);
     }
@@ -621,8 +648,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int j = up ? it : it - items_up, per = up ? n_up : n_down;
       const int s = j / per, q = j - s * per;
       const int cnt = __popc(sh.slot_mask[s]);
-      const int buf = n_item & 1;
-      if (!wait.bar(&sh.red_full[buf], (uint32_t)((n_item >> 1) & 1))) break;
+      const int buf = n_item & a.red_shift;
+      if (!wait.bar(&sh.red_full[buf], (uint32_t)((n_item >> a.red_shift) & 1))) break;
       // token n of this item belongs to warp (n + n_item) % kEpiWarps
       const int first = (ew + kEpiWarps - n_item % kEpiWarps) % kEpiWarps;
       float v0[kEpiTok], v1[kEpiTok];
@@ -631,9 +658,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = first + i * kEpiWarps;
         v0[i] = v1[i] = 0.f;
         if (n < cnt) {
-          const float* red = sh.red[buf] + lane * kRedStride + n;
+          const float* red = s_red + buf * kRedFloats + lane * kRedStride + n;
 #pragma unroll
-          for (int z = 0; z < 4; ++z) {
+          for (int z = 0; z < kSplits; ++z) {
             v0[i] += red[z * 64 * kRedStride];
             v1[i] += red[z * 64 * kRedStride + 32 * kRedStride];
           }
@@ -778,16 +805,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-int few_stages(int T, int d) {
-  const long long room = 232448 - 1024 - (long long)sizeof(Shared) - (long long)T * (2 * d + 64);
-  const long long n = room / stage_bytes(T);
-  return n < 2 ? 0 : (int)std::min<long long>(n, kMaxStages) & ~1;  // an even number: see the producers
+// Shared memory: [ring][x][partial products][Shared].  Two buffers of partial products, one where the second would
+// leave the ring too short.
+static size_t few_smem(int T, int d, int stages, int red_shift) {
+  return 1024 + (size_t)stages * stage_bytes(T) + (size_t)T * (2 * d + 64) + (size_t)(red_shift + 1) * kRedFloats * 4 +
+         sizeof(Shared);
+}
+
+int few_stages(int T, int d, int* red_shift) {
+  for (int rs = 1; rs >= 0; --rs) {
+    int n = kMaxStages & ~1;  // an even number: see the producers
+    while (n > 0 && few_smem(T, d, n, rs) > 232448) n -= 2;
+    if (n) {
+      if (red_shift) *red_shift = rs;
+      return n;
+    }
+  }
+  return 0;
 }
 
 cudaError_t launch_few_tokens(const FewMaps& routed, const FewMaps& shared, FewArgs a, int num_sms, cudaStream_t s) {
-  a.stages = few_stages(a.T, a.d);
+  a.stages = few_stages(a.T, a.d, &a.red_shift);
   if (!a.stages) return cudaErrorInvalidValue;
-  const size_t smem = 1024 + (size_t)a.stages * stage_bytes(a.T) + (size_t)a.T * (2 * a.d + 64) + sizeof(Shared);
+  const size_t smem = few_smem(a.T, a.d, a.stages, a.red_shift);
   static PerDeviceOnce once;
   cudaError_t e = once.run(
       [] { return cudaFuncSetAttribute(few_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448); });

@@ -34,12 +34,13 @@ struct FewArgs {
   int* status;
   uint64_t budget_ns;
   int T, d, f, E, k, V, has_shared, stages;
+  int red_shift;            // buffers of partial products: 2 (1) or 1 (0)
   int stall;                // issue no weight copies (moe_testing_stall_loads)
   float route_scale, limit;
 };
 
 // Stages of the weight ring that fit beside T rows of d columns; 0 if too few.
-int few_stages(int T, int d);
+int few_stages(int T, int d, int* red_shift = nullptr);
 
 // Tensor maps of one expert set for this kernel: a copy brings the K groups kg .. kg + 3 of 64 weight rows.
 //   w13   {64 B, 128 rows, gate / up, f / 128, experts * d / 128}, box {64, 32, 2, 1, 4}, 64-byte swizzle
