@@ -55,7 +55,7 @@ constexpr int kMaxK = 16;
 constexpr int kMaxSlots = kFewMaxSlots;
 constexpr int kRedStride = 9;                    // floats a row of the partial products (8 tokens)
 constexpr int kRedFloats = kSplits * 64 * kRedStride;
-constexpr int kMaxStages = 10;
+constexpr int kMaxStages = 8;                    // the ring has 2, 4 or 8 stages
 constexpr int kFxItems = 16;                     // items in flight: at most the ring's and the two partial buffers'
 static_assert(kMaxStages + 2 < kFxItems, "a row factor must outlive its item");
 
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == kProducer * 32) {
     for (int i = 0; i < a.stages; ++i) {
       mbar_init(&sh.full[i], 2);
-      mbar_init(&sh.empty[i], kGroupWarps + kHWarps);
+      mbar_init(&sh.empty[i], kGroupWarps + 1);  // a group's warps and an h warp
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.red_full[i], kMmaWarps);
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kProducer) {
     // -------------------------------------------------------------- producers
     // Two warps take the stages in turn: beside busy product warps one thread's waits and copies do not keep up.  The
-    // ring has an even number of stages, so that a slot always belongs to the same producer.
+    // ring's 2, 4 or 8 stages are even in number: a slot always belongs to the same producer.
     if (lane == 0 && !a.stall) {
       const uint64_t policy = l2_policy_evict_first();
       const int mine = warp - kProducer;
@@ -716,74 +716,113 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // -------------------------------------------------------------- h slices of the down stages
-    // Warp i takes every fourth stage: the slot's tokens' next 512 columns of h, as fp16 code * 2^(e - E + 7) with E
-    // the row's largest block exponent.
-    const int hw = warp - kMmaWarps - kEpiWarps;
-    int stage = 0, turn = 0, n_item = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int it = blockIdx.x; it < items && ok; it += gridDim.x, ++n_item) {
-      const bool up = it < items_up;
-      const int j = up ? it : it - items_up, per = up ? n_up : n_down;
-      const int s = j / per, KG = up ? kg_up : kg_down;
-      const uint32_t mask = sh.slot_mask[s];
-      const int cnt = __popc(mask);
-      for (int kg = 0; kg < KG; kg += kStageKg) {
-        // Every warp waits for and releases every stage, up stages and the other warps' included: it can then be
-        // neither ahead of the ring nor a whole turn behind it, where a phase's parity would mislead it.
-        if (lane == 0) ok = wait.bar(&sh.empty[stage], phase ^ 1u);
-        const bool own = !up && (turn++ & (kHWarps - 1)) == hw;
-        if (own && lane == 0 && ok && !*(volatile int*)&sh.slot_ready[s]) {
-          ok = wait.count(a.counters + kFewSlotDone + s, n_up * cnt);
-          __threadfence_block();
-          if (ok) *(volatile int*)&sh.slot_ready[s] = 1;
+    // Warp hw owns the ring slots hw, hw + n_own, .. (n_own divides the ring): into the down stages there it puts the
+    // slot's tokens' next 512 columns of h, as fp16 code * 2^(e - E + 7) with E the row's largest block exponent.  It
+    // waits for and releases all stages of its slots, up stages too, so that it sees each of their phases.
+    const int n_own = min(kHWarps, a.stages), hw = warp - kMmaWarps - kEpiWarps;
+    if (hw < n_own) {
+      // The block's down stages are numbered from n_up_st, per_item to a down item; its first down item is it0.
+      const int up_st = (kg_up + kStageKg - 1) / kStageKg, per_item = (kg_down + kStageKg - 1) / kStageKg;
+      const int G = gridDim.x, b0 = blockIdx.x;
+      const int n_ups = b0 < items_up ? (items_up - 1 - b0) / G + 1 : 0;
+      const int it0 = b0 + n_ups * G;
+      const int n_downs = it0 < items ? (items - 1 - it0) / G + 1 : 0;
+      const int n_up_st = n_ups * up_st, n_st = n_up_st + n_downs * per_item;
+      // Codes, block scales and row maxima of one stage for up to four tokens of its slot, fetched while earlier stages
+      // run, if the slot is complete by then.
+      constexpr int kAhead = 4;
+      uint4 code[kAhead];
+      uint32_t eb[kAhead], top[kAhead];
+      auto fetch = [&](int s, int n, int part, uint4& cd, uint32_t& e, uint32_t& m) {
+        const size_t row = (size_t)sh.slot_tok[s][n] * (k + 1) + sh.slot_j[s][n];
+        const int c = part * kStageKg * 128 + lane * 16;  // this lane's 16 columns, half an MX block
+        const bool in = c < f;
+        cd = in ? __ldcg(reinterpret_cast<const uint4*>(a.h + row * f + c)) : make_uint4(0u, 0u, 0u, 0u);
+        e = in ? __ldcg(a.h_s + row * (f / 32) + c / 32) : 0u;
+        m = 0;
+        for (int i = lane * 4; i < f / 32; i += 128)
+          m = __vmaxu4(m, __ldcg(reinterpret_cast<const uint32_t*>(a.h_s + row * (f / 32) + i)));
+      };
+      auto place = [&](uint8_t* dst, float* fx, const uint4& cd, uint32_t e, uint32_t top4) {
+        uint32_t m = __vmaxu2(top4 & 0x00FF00FFu, (top4 >> 8) & 0x00FF00FFu);
+        m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
+        const int x = (int)e - (int)m + 7;  // 2^x in fp16, subnormal below -14, 0 below -24
+        const uint32_t p = x >= -14 ? (uint32_t)(x + 15) << 10 : x >= -24 ? 1u << (x + 24) : 0u;
+        const uint32_t p2 = p | (p << 16);
+        const uint32_t cw[4] = {cd.x, cd.y, cd.z, cd.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint32_t h2;
+          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(cw[i >> 1] >> (16 * (i & 1)))));
+          asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(h2), "r"(p2));
         }
-        ok = __shfl_sync(0xFFFFFFFFu, (int)ok, 0);
-        if (!ok) break;
-        if (own) {
-          const int c = kg * 128 + lane * 16;  // this lane's 16 columns, half an MX block
-          const bool in = c < f;
-          uint4 code[kMaxT];
-          uint32_t eb[kMaxT], top[kMaxT];
+        *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>(dst + 16) = make_uint4(o[4], o[5], o[6], o[7]);
+        if (fx && lane == 0) *fx = ldexpf(1.f, (int)m - 134);
+      };
+      // whether slot s has all its h blocks; wait_for: wait until it has
+      auto slot_complete = [&](int s, int cnt, bool wait_for) {
+        bool yes = true;
+        if (lane == 0 && !*(volatile int*)&sh.slot_ready[s]) {
+          const int* c = a.counters + kFewSlotDone + s;
+          yes = wait_for ? wait.count(c, n_up * cnt) : ld_acquire(c) >= n_up * cnt;
+          __threadfence_block();
+          if (yes) *(volatile int*)&sh.slot_ready[s] = 1;
+        }
+        return (bool)__shfl_sync(0xFFFFFFFFu, (int)yes, 0);
+      };
+      int slot = hw, s = 0, cnt = 0, di = 0, part = 0;
+      uint32_t phase = 0;
+      bool fetched = false, located = false;
+      for (int o = hw; o < n_st; o += n_own) {
+        const bool down = o >= n_up_st;
+        if (down && !located) {  // stage o: part `part` of the block's down item di, slot s
+          di = (o - n_up_st) / per_item;
+          part = o - n_up_st - di * per_item;
+          s = (it0 + di * G - items_up) / n_down;
+          cnt = __popc(sh.slot_mask[s]);
+        }
+        bool ok = true;
+        if (lane == 0) ok = wait.bar(&sh.empty[slot], phase ^ 1u);
+        if (!__shfl_sync(0xFFFFFFFFu, (int)ok, 0)) break;
+        if (down) {
+          if (!fetched && !slot_complete(s, cnt, true)) break;
+          uint8_t* dst = ring + slot * kStageBytes + kStageH + lane * 32;
+          float* fx = part == 0 ? sh.hfx[(n_ups + di) % kFxItems] : nullptr;
+          for (int n0 = 0; n0 < cnt; n0 += kAhead) {
+            if (!fetched) {
 #pragma unroll
-          for (int n = 0; n < kMaxT; ++n) {
-            if (n >= cnt) continue;
-            const size_t row = (size_t)sh.slot_tok[s][n] * (k + 1) + sh.slot_j[s][n];
-            code[n] = in ? __ldcg(reinterpret_cast<const uint4*>(a.h + row * f + c)) : make_uint4(0u, 0u, 0u, 0u);
-            eb[n] = in ? __ldcg(a.h_s + row * (f / 32) + c / 32) : 0u;
-            uint32_t m = 0;
-            for (int i = lane * 4; i < f / 32; i += 128)
-              m = __vmaxu4(m, __ldcg(reinterpret_cast<const uint32_t*>(a.h_s + row * (f / 32) + i)));
-            top[n] = m;
-          }
-          uint8_t* dst = ring + stage * kStageBytes + kStageH + lane * 32;
-#pragma unroll
-          for (int n = 0; n < kMaxT; ++n) {
-            if (n >= cnt) continue;
-            uint32_t m = __vmaxu2(top[n] & 0x00FF00FFu, (top[n] >> 8) & 0x00FF00FFu);
-            m = __reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16));
-            const int x = (int)eb[n] - (int)m + 7;  // 2^x in fp16, subnormal below -14, 0 below -24
-            const uint32_t p = x >= -14 ? (uint32_t)(x + 15) << 10 : x >= -24 ? 1u << (x + 24) : 0u;
-            const uint32_t p2 = p | (p << 16);
-            const uint32_t cw[4] = {code[n].x, code[n].y, code[n].z, code[n].w};
-            uint32_t o[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              uint32_t h2;
-              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)(cw[i >> 1] >> (16 * (i & 1)))));
-              asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(o[i]) : "r"(h2), "r"(p2));
+              for (int i = 0; i < kAhead; ++i)
+                if (n0 + i < cnt) fetch(s, n0 + i, part, code[i], eb[i], top[i]);
             }
-            *reinterpret_cast<uint4*>(dst + n * kHPitch) = make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(dst + n * kHPitch + 16) = make_uint4(o[4], o[5], o[6], o[7]);
-            if (kg == 0 && lane == 0) sh.hfx[n_item % kFxItems][n] = ldexpf(1.f, (int)m - 134);
+            fetched = false;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+              if (n0 + i < cnt) place(dst + (n0 + i) * kHPitch, fx ? fx + n0 + i : nullptr, code[i], eb[i], top[i]);
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.full[stage]);
+          if (lane == 0) mbar_arrive(&sh.full[slot]);
         }
-        if (lane == 0) mbar_arrive(&sh.empty[stage]);
-        if (++stage == a.stages) {
-          stage = 0;
+        if (lane == 0) mbar_arrive(&sh.empty[slot]);
+        if ((slot += n_own) >= a.stages) {
+          slot = hw;
           phase ^= 1u;
+        }
+        located = false;
+        const int next = o + n_own;
+        if (next >= n_up_st && next < n_st) {  // fetch ahead
+          di = (next - n_up_st) / per_item;
+          part = next - n_up_st - di * per_item;
+          s = (it0 + di * G - items_up) / n_down;
+          cnt = __popc(sh.slot_mask[s]);
+          located = true;
+          if (cnt <= kAhead && slot_complete(s, cnt, false)) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+              if (i < cnt) fetch(s, i, part, code[i], eb[i], top[i]);
+            fetched = true;
+          }
         }
       }
     }
@@ -806,21 +845,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 // Shared memory: [ring][x][partial products][Shared].  Two buffers of partial products, one where the second would
-// leave the ring too short.
+// shorten the ring.
 static size_t few_smem(int T, int d, int stages, int red_shift) {
   return 1024 + (size_t)stages * stage_bytes(T) + (size_t)T * (2 * d + 64) + (size_t)(red_shift + 1) * kRedFloats * 4 +
          sizeof(Shared);
 }
 
 int few_stages(int T, int d, int* red_shift) {
-  for (int rs = 1; rs >= 0; --rs) {
-    int n = kMaxStages & ~1;  // an even number: see the producers
-    while (n > 0 && few_smem(T, d, n, rs) > 232448) n -= 2;
-    if (n) {
-      if (red_shift) *red_shift = rs;
-      return n;
-    }
-  }
+  for (int n = kMaxStages; n >= 2; n /= 2)
+    for (int rs = 1; rs >= 0; --rs)
+      if (few_smem(T, d, n, rs) <= 232448) {
+        if (red_shift) *red_shift = rs;
+        return n;
+      }
   return 0;
 }
 
