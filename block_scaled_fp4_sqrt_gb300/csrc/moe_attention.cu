@@ -57,6 +57,7 @@ struct AttnParams {
   float* lse;
   int64_t q_stride, out_stride;
   int L, group, rows, row_tiles, Hq;  // rows = L * group
+  uint32_t page_units, row_units, head_units;  // the cache's strides in 16-byte units
   float scale_log2;                   // scale * log2(e)
   PageDiv pd;
   int* counters;    // [n_seqs * kv heads * row_tiles], zero between calls
@@ -174,12 +175,16 @@ struct Cfg {
   // p may take q's place once the fragments are in registers
   static constexpr int kQPBytes = kQRegs ? (kQBytes > kPBytes ? kQBytes : kPBytes) : kQBytes + kPBytes;
   static constexpr int kStatBytes = (2 * kWarps + 2) * kRows * 4;
-  // Blocks an SM holds: three, or two where a stage (32 KB) or the registers (64 rows) leave no room for more.
-  static constexpr int kBlocks = kStageBytes > 20 * 1024 || MT == 4 ? 2 : 3;
+  // Blocks an SM holds: three, or two where the registers leave no room for more: 64 rows, and 32 rows of a quantised
+  // cache (64 requests x 8 rows: 161 us with three blocks, 143 us with two).  A bf16 cache of 128 columns keeps only two
+  // stages beside three blocks and is still faster (64 x 8 rows 117 against 128 us, 64 x 1 rows 80 against 88 us with
+  // two blocks of three stages).
+  static constexpr int kBlocks = MT == 4 || (MT == 2 && MX) ? 2 : 3;
   static constexpr int kBudget = (kBlocks == 2 ? 113 : 75) * 1024 - kQPBytes - kStatBytes - 256;
   static constexpr int kFit = kBudget / kStageBytes;
   static constexpr int kStages = kFit < 2 ? 2 : kFit > 6 ? 6 : kFit;
-  static constexpr int kSmem = kStages * kStageBytes + kQPBytes + kStatBytes + 128;
+  static constexpr int kSmem = kStages * kStageBytes + kQPBytes + kStatBytes + 256;
+  static_assert(kStageBytes % kRowBytes == 0 && 256 % kRowBytes == 0, "the loader flips address bits inside a row");
 };
 
 template <int D, bool MX, int MT>
@@ -191,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
   constexpr int kNT = kCols / 8;               // 8-column tiles of a warp
   extern __shared__ uint8_t smem_raw[];
   // (pointer arithmetic on the array keeps the accesses below shared-memory ones)
-  uint8_t* smem = smem_raw + ((128u - (smem_addr(smem_raw) & 127u)) & 127u);
+  uint8_t* smem = smem_raw + ((256u - (smem_addr(smem_raw) & 255u)) & 255u);
   uint8_t* s_q = smem + C::kStages * C::kStageBytes;          // q, bf16 or (MXFP8) fp16
   uint8_t* s_p = C::kQRegs ? s_q : s_q + C::kQBytes;          // p of the current tile
   float* s_mx = reinterpret_cast<float*>(s_q + C::kQPBytes);  // [warp][row]
@@ -280,10 +285,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
   auto swz = [](int row, int chunk) {
     return (kChunks >= 8 ? (chunk ^ (row & 7)) : (chunk ^ ((row >> 1) & 3))) * 16;
   };
-  // page of this lane's token (lanes 0..15) of the tile that will be loaded next, or -1; looked up one tile ahead,
-  // so that the table's latency is not in front of the loads
+  // Lane t < 16 knows where its token t of the tile that will be loaded next lies (looked up one tile ahead, so that the
+  // table's latency is not in front of the loads); kChunks lanes then fetch a token's row together, taking the place
+  // from that lane as a 32-bit count of 16-byte (MXFP8: 16-column) units.  (Two lanes a token, with no exchange, halve
+  // the instructions but spread each over 16 rows: 172 instead of 144 us for three long bf16 requests.)
+  constexpr int kPerIter = 32 / kChunks;  // tokens a warp instruction covers
+  const uint32_t ld_dst = smem_base + (tok_first + lane / kChunks) * C::kRowBytes + swz(lane / kChunks, lane % kChunks);
+  const uint8_t* const k_src = static_cast<const uint8_t*>(p.c.k) + lane % kChunks * 16;
+  const uint8_t* const v_src = static_cast<const uint8_t*>(p.c.v) + lane % kChunks * 16;
+  constexpr uint32_t kNoRow = 0xFFFFFFFFu;
   Cursor ld = cur;
-  int64_t ld_left = t1 - t0;
+  int ld_left = (int)(t1 - t0 < 0x7fffffff ? t1 - t0 : 0x7fffffff);
   int nxt_page = -1, nxt_row = 0;
   auto lookup = [&]() {
     nxt_page = -1;
@@ -307,30 +319,33 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
       late_dst = 0;
     }
     if (ld_left > 0) {
-      const int64_t off =
-          nxt_page >= 0 ? nxt_page * p.c.page_stride + nxt_row * p.c.row_stride + ld.head * p.c.head_stride : -1;
-      const uint32_t kbase = smem_base + stage * C::kStageBytes;
-      constexpr int kPerIter = 32 / kChunks;  // tokens a warp instruction covers
+      constexpr int kUnit = MX ? 16 : 8;  // columns of a unit; every stride is a multiple of it
+      const uint32_t off = nxt_page >= 0 ? (uint32_t)nxt_page * p.page_units + (uint32_t)nxt_row * p.row_units +
+                                               (uint32_t)ld.head * p.head_units
+                                         : kNoRow;
+      const uint32_t dst0 = ld_dst + stage * C::kStageBytes;
+      static_assert(kUnit * (MX ? 1 : 2) == 16, "a unit is 16 bytes");
 #pragma unroll
       for (int i = 0; i < kWarpTok; i += kPerIter) {
-        const int tk = i + lane / kChunks, ch = lane % kChunks;
-        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, tk);
-        const bool ok = o >= 0;
-        const uint32_t dst = kbase + (tok_first + tk) * C::kRowBytes + swz(tok_first + tk, ch);
-        const int64_t byte = (ok ? o : 0) * (MX ? 1 : 2) + ch * 16;
-        cp_async16(dst, static_cast<const uint8_t*>(p.c.k) + byte, ok);
-        cp_async16(dst + C::kHalf, static_cast<const uint8_t*>(p.c.v) + byte, ok);
+        const uint32_t o = __shfl_sync(0xFFFFFFFFu, off, i + lane / kChunks);
+        const bool ok = o != kNoRow;
+        const int64_t byte = ok ? (int64_t)o * 16 : (int64_t)0;
+        // row i + lane / kChunks: the swizzle of row i comes on top of the lane's own
+        const uint32_t dst = (dst0 ^ swz(i, 0)) + i * C::kRowBytes;
+        cp_async16(dst, k_src + byte, ok);
+        cp_async16(dst + C::kHalf, v_src + byte, ok);
       }
       if constexpr (MX) {  // lane t: K scales, lane 16 + t: V scales
         const int tk = lane % kWarpTok;
-        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, tk);
-        const bool v = lane >= kWarpTok;
-        const uint32_t dst = kbase + 2 * C::kHalf + (v ? kTile * C::kScale : 0) + (tok_first + tk) * C::kScale;
-        const uint8_t* src = (v ? p.c.v_s : p.c.k_s) + ((o >= 0 ? o : 0) >> 5);
+        const uint32_t o = __shfl_sync(0xFFFFFFFFu, off, tk);
+        const bool ok = o != kNoRow, v = lane >= kWarpTok;
+        const uint32_t dst = smem_base + stage * C::kStageBytes + 2 * C::kHalf + (v ? kTile * C::kScale : 0) +
+                             (tok_first + tk) * C::kScale;
+        const uint8_t* src = (v ? p.c.v_s : p.c.k_s) + (ok ? o >> 1 : 0u);  // two units a scale byte
         if constexpr (D == 128) {
-          cp_async4(dst, src, o >= 0);
+          cp_async4(dst, src, ok);
         } else {  // two bytes, less than cp.async copies: through a register, stored one tile later
-          late_val = o >= 0 ? __ldg(reinterpret_cast<const uint16_t*>(src)) : (uint16_t)0;
+          late_val = ok ? __ldg(reinterpret_cast<const uint16_t*>(src)) : (uint16_t)0;
           late_dst = dst;
         }
       }
@@ -1036,6 +1051,11 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   Sizes z{};
   st = plan(c, a->n_q_heads, a->L, 1, "moe_paged_attention", &z);
   if (st != MOE_OK) return st;
+  // rows are addressed by 32-bit counts of 16-byte units
+  const __int128 last = (__int128)(c.n_pages > 0 ? c.n_pages - 1 : 0) * c.page_stride +
+                        (__int128)(c.page_size - 1) * c.row_stride + (__int128)(c.n_kv_heads - 1) * c.head_stride;
+  if (last / (c.format == MOE_KV_MXFP8 ? 16 : 8) >= 0xFFFFFFFFll)
+    return decode_fail(MOE_ERR_UNSUPPORTED, "moe_paged_attention: k or v spans 64 GB or more");
   if (!std::isfinite(a->scale)) return decode_fail(MOE_ERR_INVALID_ARG, "moe_paged_attention: scale is not finite");
   const int64_t width = (int64_t)a->n_q_heads * c.head_dim;
   const int64_t qs = a->q_stride ? a->q_stride : width, os = a->out_stride ? a->out_stride : width;
@@ -1071,6 +1091,10 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   p.Hq = a->n_q_heads;
   p.scale_log2 = a->scale * kLog2e;
   p.pd = page_div((uint32_t)c.page_size);
+  const int64_t unit = c.format == MOE_KV_MXFP8 ? 16 : 8;
+  p.page_units = (uint32_t)(c.page_stride / unit);
+  p.row_units = (uint32_t)(c.row_stride / unit);
+  p.head_units = (uint32_t)(c.head_stride / unit);
   p.counters = static_cast<int*>(a->workspace);
   p.group_counters = p.counters + z.units;
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + z.counters);
