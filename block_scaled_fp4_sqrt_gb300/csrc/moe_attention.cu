@@ -5,9 +5,10 @@
 // The cache is read once, so a step's few rows a key-value head (heads of the group x L) leave it memory-bound.
 // Layout of the work:
 //  * A unit is (request, kv head, row tile): the rows r = l * group + j of the query heads that share the kv head,
-//    16 MT of them at a time.  Every unit is cut into tiles of 64 tokens; the tiles of all units, in order, are
-//    dealt to the grid in equal contiguous runs, computed by every block from the lengths alone.  A long request is
-//    thus spread over the GPU and short ones share a block, whatever the mix of lengths.
+//    16 MT of them at a time.  Every unit is cut into tiles of 64 tokens; the tiles of all units, in order and with
+//    kUnitCost places in front of each unit's first, are dealt to the grid in equal contiguous runs of places, computed by
+//    every block from the lengths alone.  A long request is thus spread over the GPU and short ones share a block,
+//    whatever the mix of lengths.
 //  * A block is four warps.  For a tile each warp fetches 16 tokens (cp.async, a ring of stages), computes the
 //    scores of these 16 tokens for all rows, and leaves p in shared memory; after a barrier each warp accumulates
 //    a quarter of the columns over all 64 tokens.  The accumulators then take 16 MT D / 128 / 4 registers a thread
@@ -46,6 +47,10 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kWarpTok = kTile / kWarps;  // tokens of a tile that a warp fetches and scores
 constexpr int kPPitch = kTile * 2 + 16;   // bytes of a row of p: eight rows fall on distinct banks
 constexpr int kJoin = 16;                 // parts that are joined in one step
+// What beginning and ending a unit costs, in tiles, when the work is dealt.  64 requests of 100 to 8000 tokens, us at a
+// cost of 0 / 2 / 4 / 7: 8 rows MXFP8 145 / 107 / 105 / 114, 8 rows bf16 117 / 93 / 93 / 95; 200 requests of up to 1500
+// tokens 17.8 / 13.9 / 14.6 / 16.0; long requests do not depend on it.
+constexpr int kUnitCost = 3;
 constexpr float kGrow = 8.f;              // log2 units by which a score may exceed the running maximum
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -212,11 +217,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
   pdl_trigger();
   pdl_wait();
 
-  // ---- this block's run of tiles
+  // ---- this block's run of places
   const int B = p.c.n_seqs, H = p.c.n_kv_heads, HR = H * p.row_tiles;
   auto tiles_of = [](int len) { return len > 0 ? (len + kTile - 1) / kTile : 1; };
   int64_t sum = 0;
-  for (int b = tid; b < B; b += kThreads) sum += tiles_of(seq_len_of(p.c, b));
+  for (int b = tid; b < B; b += kThreads) sum += tiles_of(seq_len_of(p.c, b)) + kUnitCost;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
   if (lane == 0) s_part[warp] = sum;
@@ -230,11 +235,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
   if (t0 >= t1) return;
   Cursor cur;
   {
-    const int64_t want = t0 / HR;  // in tiles of one unit per request
+    const int64_t want = t0 / HR;  // in places of one unit per request
     int64_t carry = 0;
     for (int b0 = 0; b0 < B; b0 += kThreads) {
       const int b = b0 + tid;
-      const int n = b < B ? tiles_of(seq_len_of(p.c, b)) : 0;
+      const int n = b < B ? tiles_of(seq_len_of(p.c, b)) + kUnitCost : 0;
       int64_t incl = n;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -261,22 +266,30 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
     cur.len = seq_len_of(p.c, cur.b);
     cur.nt = tiles_of(cur.len);
     const int64_t off = t0 - s_first * HR;
-    const int w = (int)(off / cur.nt);
-    cur.t = (int)(off - (int64_t)w * cur.nt);
+    const int w = (int)(off / (cur.nt + kUnitCost));
+    cur.t = (int)(off - (int64_t)w * (cur.nt + kUnitCost)) - kUnitCost;
     cur.head = w / p.row_tiles;
     cur.rt = w - cur.head * p.row_tiles;
   }
-  auto advance = [&](Cursor& c) {
-    if (++c.t < c.nt) return;
+  int64_t pos = t0;  // place of the tile cur
+  if (cur.t < 0) {   // the run begins in front of a unit's first tile
+    pos -= cur.t;
+    cur.t = 0;
+  }
+  if (pos >= t1) return;
+  // to the next tile; returns how many places further it lies
+  auto advance = [&](Cursor& c) -> int {
+    if (++c.t < c.nt) return 1;
     c.t = 0;
-    if (++c.rt < p.row_tiles) return;
+    if (++c.rt < p.row_tiles) return 1 + kUnitCost;
     c.rt = 0;
-    if (++c.head < H) return;
+    if (++c.head < H) return 1 + kUnitCost;
     c.head = 0;
     if (++c.b < B) {
       c.len = seq_len_of(p.c, c.b);
       c.nt = tiles_of(c.len);
     }
+    return 1 + kUnitCost;
   };
 
   // ---- loading: a warp fetches 16 tokens of a tile
@@ -295,12 +308,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
   const uint8_t* const v_src = static_cast<const uint8_t*>(p.c.v) + lane % kChunks * 16;
   constexpr uint32_t kNoRow = 0xFFFFFFFFu;
   Cursor ld = cur;
-  int ld_left = (int)(t1 - t0 < 0x7fffffff ? t1 - t0 : 0x7fffffff);
+  int64_t ld_pos = pos;
   int nxt_page = -1, nxt_row = 0;
   auto lookup = [&]() {
     nxt_page = -1;
     const int t = ld.t * kTile + tok_first + lane;
-    if (ld_left > 0 && lane < kWarpTok && t < ld.len) {
+    if (ld_pos < t1 && lane < kWarpTok && t < ld.len) {
       const int j = page_of(t, p.pd, p.c.page_size, &nxt_row);
       nxt_page = __ldg(p.c.block_table + (int64_t)ld.b * p.c.max_pages + j);
       if ((unsigned)nxt_page >= (unsigned)p.c.n_pages) {
@@ -318,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
       if (late_dst) asm volatile("st.shared.u16 [%0], %1;" ::"r"(late_dst), "h"(late_val) : "memory");
       late_dst = 0;
     }
-    if (ld_left > 0) {
+    if (ld_pos < t1) {
       constexpr int kUnit = MX ? 16 : 8;  // columns of a unit; every stride is a multiple of it
       const uint32_t off = nxt_page >= 0 ? (uint32_t)nxt_page * p.page_units + (uint32_t)nxt_row * p.row_units +
                                                (uint32_t)ld.head * p.head_units
@@ -349,8 +362,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
           late_dst = dst;
         }
       }
-      --ld_left;
-      advance(ld);
+      ld_pos += advance(ld);
       lookup();
     }
     cp_async_commit();
@@ -740,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
 
   // ---- a unit's end: write the rows, or this block's part of them
   constexpr size_t kSlot = (size_t)C::kRows * (D + 2);
-  auto end_unit = [&](int64_t unit_first) {
+  auto end_unit = [&](int64_t unit_first) {  // the first place of the unit, kUnitCost before its first tile
     const int row0 = cur.rt * C::kRows;
     const int nrows = min(C::kRows, p.rows - row0);
 #pragma unroll
@@ -759,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
         const int r = a * 16 + li + 8 * h;
         l[a][h] = (s_l[r] + s_l[C::kRows + r]) + (s_l[2 * C::kRows + r] + s_l[3 * C::kRows + r]);
       }
-    const int64_t unit_end = unit_first + cur.nt;
+    const int64_t first_tile = unit_first + kUnitCost, unit_end = first_tile + cur.nt;
     // this thread's rows of the final result: o / l and the logarithm of the sum
     auto write_rows = [&]() {
 #pragma unroll
@@ -790,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
             p.lse[token * p.Hq + head] = m[a][h] == -INFINITY ? -INFINITY : (m[a][h] + log2f(z)) * kLn2;
         }
     };
-    if (unit_first >= t0 && unit_end <= t1) {  // the whole unit was this block's
+    if (first_tile >= t0 && unit_end <= t1) {  // the whole unit was this block's
       write_rows();
       return;
     }
@@ -885,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
       return true;
     };
     // slot 0 of a block is the unit its run begins in, slot 1 the one that it ends in
-    const int b0 = (int)(unit_first / per), b1 = (int)((unit_end - 1) / per), parts = b1 - b0 + 1;
+    const int b0 = (int)(first_tile / per), b1 = (int)((unit_end - 1) / per), parts = b1 - b0 + 1;
     auto block_slot = [&](int b) {
       return p.partial + ((size_t)b * 2 + (unit_first > b * per ? 1 : 0)) * kSlot;
     };
@@ -912,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
   // ---- the run
   int stage = 0;
   bool fresh = true;
-  for (int64_t pos = t0; pos < t1;) {
+  while (pos < t1) {
     if (fresh) {
       begin_unit();
       fresh = false;
@@ -966,13 +978,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
       for (int h = 0; h < 2; ++h) l[a][h] += add[a][h];
     values(stage);
     stage = stage == C::kStages - 1 ? 0 : stage + 1;
-    ++pos;
-    if (cur.t + 1 == cur.nt || pos == t1) {
+    if (cur.t + 1 == cur.nt || pos + 1 == t1) {
       __syncthreads();  // p is no longer read: its place may take the next unit's q
-      end_unit(pos - 1 - cur.t);
+      end_unit(pos - cur.t - kUnitCost);
       fresh = true;
     }
-    advance(cur);
+    pos += advance(cur);
   }
   cp_async_wait<0>();
 }
