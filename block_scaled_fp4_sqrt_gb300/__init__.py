@@ -146,10 +146,15 @@ def _p(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _raw_stream(stream) -> int:
+    """The cudaStream_t of a torch stream (None: the current one), or an integer handle as it is."""
+    if stream is None:  # torch.cuda.current_stream() builds a Stream object, 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return ctypes.c_void_p(_raw_stream(stream))
 
 
 def _input(x: torch.Tensor, token_ids: torch.Tensor | None = None) -> moe_input_t:

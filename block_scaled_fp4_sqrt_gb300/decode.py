@@ -7,24 +7,23 @@ kernels, asynchronously on the given stream (default: the current one).
 from __future__ import annotations
 
 import ctypes
-import math
 
 import torch
 
-from . import (MOE_OK, MoEError, _ok, _stream, lib, moe_attention_t, moe_kv_cache_t, moe_norm_t)
+from . import MOE_OK, MoEError, _ok, _raw_stream, lib, moe_attention_t, moe_kv_cache_t, moe_norm_t
 
 MOE_KV_BF16, MOE_KV_MXFP8 = 0, 1
 KV_STATUS = {1: "a sequence length outside the block table", 2: "a page index outside the cache"}
 
 
 def _rows(t: torch.Tensor | None, name: str, shape, dtype=torch.bfloat16) -> int | None:
-    """Address of a row-strided 2-D tensor with contiguous columns."""
+    """Address of a row-strided 2-D CUDA tensor with contiguous columns."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_cuda:
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(1) != 1 and shape[1] > 1:
         raise ValueError(f"the columns of {name} must be contiguous")
     return t.data_ptr()
 
@@ -37,22 +36,32 @@ def moe_add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None, weight: tor
     x, residual, sum_out, y: bf16 [T, d] (row-strided views allowed); weight: bf16 or fp32 [d]; y_q: uint8
     [T, d] E4M3 codes and y_s: uint8 [T, d / 32] E8M0 bytes, contiguous, as ``moe_permute`` writes them.
     residual and each output may be None; sum_out may be x or residual, y may be x."""
-    T, d = x.shape
-    if weight.dtype not in (torch.bfloat16, torch.float32) or weight.shape != (d,) or not weight.is_contiguous():
-        raise ValueError(f"weight must be a contiguous bf16 or fp32 tensor of {d} columns")
-    a = moe_norm_t(_rows(x, "x", (T, d)), _rows(residual, "residual", (T, d)), weight.data_ptr(),
-                   _rows(sum_out, "sum_out", (T, d)), _rows(y, "y", (T, d)),
-                   _rows(y_q, "y_q", (T, d), torch.uint8), _rows(y_s, "y_s", (T, d // 32), torch.uint8))
-    for t, name in ((y_q, "y_q"), (y_s, "y_s")):
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    if T > 1:  # the stride of a lone row means nothing
-        a.x_stride = x.stride(0)
-        a.residual_stride = 0 if residual is None else residual.stride(0)
-        a.sum_stride = 0 if sum_out is None else sum_out.stride(0)
-        a.y_stride = 0 if y is None else y.stride(0)
-    a.T, a.d, a.weight_f32, a.eps = T, d, weight.dtype == torch.float32, eps
-    _ok("moe_add_rms_norm", lib().moe_add_rms_norm(ctypes.byref(a), _stream(stream)))
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x must be [T, d], got {tuple(shape)}")
+    T, d = shape
+    w32 = weight.dtype is torch.float32
+    if not (w32 or weight.dtype is torch.bfloat16) or weight.shape != (d,) or not weight.is_contiguous() or \
+            not weight.is_cuda:
+        raise ValueError(f"weight must be a contiguous bf16 or fp32 CUDA tensor of {d} columns")
+    qp = sp = None
+    if y_q is not None:
+        qp = _rows(y_q, "y_q", shape, torch.uint8)
+        if not y_q.is_contiguous():
+            raise ValueError("y_q must be contiguous")
+    if y_s is not None:
+        sp = _rows(y_s, "y_s", (T, d // 32), torch.uint8)
+        if not y_s.is_contiguous():
+            raise ValueError("y_s must be contiguous")
+    lone = T <= 1  # the stride of a lone row means nothing
+    a = moe_norm_t(_rows(x, "x", shape), _rows(residual, "residual", shape), weight.data_ptr(),
+                   _rows(sum_out, "sum_out", shape), _rows(y, "y", shape), qp, sp,
+                   0 if lone else x.stride(0), 0 if lone or residual is None else residual.stride(0),
+                   0 if lone or sum_out is None else sum_out.stride(0), 0 if lone or y is None else y.stride(0),
+                   T, d, w32, eps)
+    status = lib().moe_add_rms_norm(ctypes.byref(a), _raw_stream(stream))
+    if status:
+        _ok("moe_add_rms_norm", status)
 
 
 class PagedKVCache:
@@ -115,11 +124,12 @@ class PagedKVCache:
 
     def _step_rows(self, t: torch.Tensor, name: str, heads: int | None = None, dtype=torch.bfloat16):
         """(L, heads, row stride) of [n_seqs, L, heads, head_dim] whose rows (b, l) lie at one stride."""
-        if t.dim() != 4 or t.dtype != dtype or t.device != self.device or t.shape[0] != self.n_seqs or \
-                t.shape[3] != self.head_dim or (heads is not None and t.shape[2] != heads):
+        shape = t.shape
+        if len(shape) != 4 or t.dtype is not dtype or t.device != self.device or shape[0] != self.n_seqs or \
+                shape[3] != self.head_dim or (heads is not None and shape[2] != heads):
             raise ValueError(f"{name} must be {dtype} [{self.n_seqs}, L, {heads or 'heads'}, {self.head_dim}] on "
                              f"{self.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
-        B, L, h, d = t.shape
+        B, L, h, d = shape
         sb, sl, sh, sd = t.stride()
         if sd != 1 or (h > 1 and sh != d) or (B > 1 and L > 1 and sb != L * sl):
             raise ValueError(f"{name}: heads must be contiguous and the rows (request, token) at one stride")
@@ -132,18 +142,21 @@ class PagedKVCache:
         Lv, _, vs = self._step_rows(v_new, "v_new", self.n_kv_heads)
         if L != Lv:
             raise ValueError("k_new and v_new hold different numbers of tokens")
-        _ok("moe_kv_append", lib().moe_kv_append(self._ref, k_new.data_ptr(), ks, v_new.data_ptr(), vs, L,
-                                                 _stream(stream)))
+        status = lib().moe_kv_append(self._ref, k_new.data_ptr(), ks, v_new.data_ptr(), vs, L, _raw_stream(stream))
+        if status:
+            _ok("moe_kv_append", status)
 
-    def workspace(self, n_q_heads: int, L: int, stream) -> torch.Tensor:
-        """The attention's workspace for calls on this stream, made (zeroed, on that stream) at first use."""
-        key = (n_q_heads, L, stream.cuda_stream)
+    def _workspace(self, n_q_heads: int, L: int, stream) -> torch.Tensor:
+        """The attention's workspace for calls on this stream, made (and zeroed there) at first use."""
+        key = (n_q_heads, L, _raw_stream(stream))
         ws = self._workspaces.get(key)
         if ws is None:
             n = int(lib().moe_paged_attention_workspace(self._ref, n_q_heads, L))
             if n == 0:
                 raise MoEError("moe_paged_attention_workspace", 1, lib().moe_last_error().decode())
-            with torch.cuda.stream(stream):
+            if stream is not None and not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+            with torch.cuda.stream(stream):  # None: the current stream
                 ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
             self._workspaces[key] = ws
         return ws
@@ -164,12 +177,13 @@ class PagedKVCache:
             raise ValueError(f"lse must be a contiguous fp32 tensor of shape {tuple(q.shape[:3])}")
         if q.numel() == 0:
             return out
-        stream = torch.cuda.current_stream(self.device) if stream is None else stream
-        ws = self.workspace(heads, L, stream)
+        ws = self._workspace(heads, L, stream)
         a = moe_attention_t(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(),
                             ws.numel(), qs, os_, heads, L,
-                            1.0 / math.sqrt(self.head_dim) if scale is None else scale)
-        _ok("moe_paged_attention", lib().moe_paged_attention(self._ref, ctypes.byref(a), _stream(stream)))
+                            self.head_dim ** -0.5 if scale is None else scale)
+        status = lib().moe_paged_attention(self._ref, ctypes.byref(a), _raw_stream(stream))
+        if status:
+            _ok("moe_paged_attention", status)
         return out
 
     def check(self) -> None:
