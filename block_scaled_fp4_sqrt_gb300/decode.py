@@ -158,7 +158,9 @@ class PagedKVCache:
                 stream = torch.cuda.ExternalStream(int(stream), device=self.device)
             with torch.cuda.stream(stream):  # None: the current stream
                 ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
-            self._workspaces[key] = ws
+                capturing = torch.cuda.is_current_stream_capturing()
+            if not capturing:  # a captured fill has not run yet: such a workspace serves its graph alone
+                self._workspaces[key] = ws
         return ws
 
     def attend(self, q: torch.Tensor, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
