@@ -151,10 +151,14 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 // Bytes 0 and 2 (bytes 1 and 3) of four E4M3 codes as a bf16 pair, times 2^-120: the code's exponent and mantissa
 // bits at bf16's lowest exponent bits.  Subnormal codes become subnormal bf16 numbers, which the multiplication
 // that follows reads as such.
-__device__ __forceinline__ uint32_t e4m3_even_bf16(uint32_t r) {
-  return ((r << 8) & 0x80008000u) | ((r << 4) & 0x07F007F0u);
+// top: the largest magnitude bits met, kNanBits for a NaN code (which the moved bits would read as 480).
+constexpr uint32_t kNanBits = 0x07F0u;
+__device__ __forceinline__ void e4m3_bf16(uint32_t r, uint32_t& even, uint32_t& odd, uint32_t& top) {
+  const uint32_t e = (r << 4) & 0x07F007F0u, o = (r >> 4) & 0x07F007F0u;
+  even = ((r << 8) & 0x80008000u) | e;
+  odd = (r & 0x80008000u) | o;
+  top = __vimax3_u16x2(top, e, o);
 }
-__device__ __forceinline__ uint32_t e4m3_odd_bf16(uint32_t r) { return (r & 0x80008000u) | ((r >> 4) & 0x07F007F0u); }
 
 // E8M0 byte j of w as a float; byte 0 (2^-127) reads as 0: what it scales is below 2^-118.
 __device__ __forceinline__ float e8m0_float(uint32_t w, int j) {
@@ -602,12 +606,16 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
       }
     }
   };
+  // column of o[.][n][2 h + y] inside the warp's columns
+  auto col_of = [&](int n, int y) { return MX ? (n / 2) * 16 + 4 * lc + (n & 1) + 2 * y : n * 8 + 2 * lc + y; };
+
   // MXFP8.  A warp's columns lie in one block of 32, so a token has one scale here.  pair[ks][i]: scale bytes of
   // tokens 16 ks + 8 i + 2 lc and the next, in 16-bit halves: what a B fragment register holds.
   // A scale above 2^7 does not fit the one multiplier 2^(byte - 127 + 120): LARGE adds a second one.
   auto values_mx = [&](uint32_t vb, const uint32_t (&pair)[kTile / 16][2], auto large) {
     constexpr bool LARGE = decltype(large)::value;
     constexpr int kZ = kCols / 16;  // 16-byte chunks of a warp's columns
+    uint32_t top = 0;
 #pragma unroll
     for (int ks = 0; ks < kTile / 16; ++ks) {
       uint32_t vf[4];
@@ -637,8 +645,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
       for (int z = 0; z < kZ; ++z)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          bf[z][0][i] = mul_bf16x2(e4m3_even_bf16(vf[2 * z + i]), mul[i]);
-          bf[z][1][i] = mul_bf16x2(e4m3_odd_bf16(vf[2 * z + i]), mul[i]);
+          e4m3_bf16(vf[2 * z + i], bf[z][0][i], bf[z][1][i], top);
+          bf[z][0][i] = mul_bf16x2(bf[z][0][i], mul[i]);
+          bf[z][1][i] = mul_bf16x2(bf[z][1][i], mul[i]);
           if constexpr (LARGE) {
             bf[z][0][i] = mul_bf16x2(bf[z][0][i], rest[i]);
             bf[z][1][i] = mul_bf16x2(bf[z][1][i], rest[i]);
@@ -655,10 +664,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
         }
       }
     }
+    if (__any_sync(0xFFFFFFFFu, (top & 0xFFFFu) == kNanBits || (top >> 16) == kNanBits)) {
+      // a NaN among the values, and every row sees the tile's tokens: its column becomes NaN
+      for (int tk = 0; tk < kTile; ++tk)
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int col = warp * kCols + col_of(n, y);
+            uint32_t code;
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(code) : "r"(vb + tk * C::kRowBytes + swz(tk, col / 16) + col % 16));
+            if ((code & 0x7Fu) == 0x7Fu) {
+#pragma unroll
+              for (int a = 0; a < MT; ++a) o[a][n][y] = o[a][n][2 + y] = __uint_as_float(0x7FC00000u);
+            }
+          }
+    }
   };
-  // column of o[.][n][2 h + y] inside the warp's columns
-  auto col_of = [&](int n, int y) { return MX ? (n / 2) * 16 + 4 * lc + (n & 1) + 2 * y : n * 8 + 2 * lc + y; };
-
   // Token by token, leaving out the tokens with p = 0.
   auto values_one_by_one = [&](uint32_t vb, uint32_t sb) {
     for (int tk = 0; tk < kTile; ++tk) {
@@ -715,7 +737,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
                      : "r"(vb + row * C::kRowBytes + swz(row, warp * kPer + i % kPer)));
 #pragma unroll
         for (int z = 0; z < 4; ++z)
-          odd |= MX ? __vcmpeq4(w[z] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0u : __vcmpeq2(w[z] & 0x7F807F80u, 0x7F807F80u) != 0u;
+          odd |= MX ? (((w[z] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u
+                    : __vcmpeq2(w[z] & 0x7F807F80u, 0x7F807F80u) != 0u;
+      }
+      if constexpr (MX) {  // a scale at which 448 times it leaves bf16's range
+        for (int tk = lane; tk < kTile; tk += 32) {
+          uint32_t e;
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(sb + tk * C::kScale + warp * kCols / 32));
+          odd |= e > 246u;
+        }
       }
       if (__any_sync(0xFFFFFFFFu, odd)) {
         values_one_by_one(vb, sb);

@@ -457,3 +457,36 @@ def test_attend_empty_calls(moe):
                             torch.empty(0, dtype=torch.int32, device=DEV))
     assert none.attend(torch.empty(0, 2, 2, 64, dtype=BF, device=DEV)).shape == (0, 2, 2, 64)
     none.append(*(torch.empty(0, 2, 1, 64, dtype=BF, device=DEV) for _ in "kv"))
+
+
+@pytest.mark.parametrize("fmt,D", [("bf16", 64), ("mxfp8", 64), ("mxfp8", 128)])
+@pytest.mark.parametrize("L", [1, 3])
+def test_attend_a_nan_value_reaches_the_rows_that_see_it(moe, fmt, D, L):
+    """A NaN among the values of an old token, in one column: that column of its head is NaN, the others are not."""
+    lens, kv, group = [150, 40], 2, 2
+    cache, g = make_cache(moe, lens, kv, D, 16, fmt, seed=91)
+    fill(cache, g, lens)
+    q = randn(g, 2, L, kv * group, D).to(BF)
+    want = cache.attend(q).clone()
+    page, col = int(cache.tab[0, 70 // 16]), D // 2 + 5
+    cache.v[page, 70 % 16, 1, col] = float("nan") if fmt == "bf16" else 0xFF
+    got = cache.attend(q)
+    assert torch.isnan(got[0, :, group:, col]).all()
+    got[0, :, group:, col] = want[0, :, group:, col]
+    # the tile with the NaN may be computed by other instructions, to the same bounds
+    assert torch.allclose(got.float(), want.float(), rtol=2 * HALF_ULP, atol=2 * HALF_ULP)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_a_later_token_of_the_largest_scale_stays_out(moe, D):
+    """448 2^127 leaves bf16's range: a token that a row does not see must not turn the row into 0 times infinity."""
+    lens, kv, group, L = [90], 1, 2, 3
+    cache, g = make_cache(moe, lens, kv, D, 16, "mxfp8", seed=95)
+    fill(cache, g, lens)
+    q = randn(g, 1, L, kv * group, D).to(BF)
+    want = cache.attend(q).clone()
+    page, row = int(cache.tab[0, 89 // 16]), 89 % 16  # seen by the last row alone
+    cache.v[page, row] = 0x7E
+    cache.v_scales[page, row] = 254
+    got = cache.attend(q)
+    assert torch.allclose(got[:, :2].float(), want[:, :2].float(), rtol=2 * HALF_ULP, atol=2 * HALF_ULP)
