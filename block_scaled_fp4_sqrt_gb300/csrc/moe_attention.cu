@@ -860,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
           }
         }
     };
-    // o, m, l = the parts 0 .. n_parts - 1 joined in this order; each step loads one part of all rows
+    // o, m, l = the parts 0 .. n_parts - 1 joined in this order
     auto join = [&](int n_parts, auto slot_of) {
 #pragma unroll
       for (int a = 0; a < MT; ++a)
@@ -871,46 +871,56 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
 #pragma unroll
           for (int n = 0; n < kNT; ++n) o[a][n][2 * h] = o[a][n][2 * h + 1] = 0.f;
         }
-#pragma unroll 2
-      for (int i = 0; i < n_parts; ++i) {
-        const float* src = slot_of(i);
-        float pm[MT][2], pl[MT][2], po[MT][2][2 * kNT];
+      // kIn parts are under way at once, the last ones repeated where fewer are left
+      constexpr int kIn = 2;
+      for (int i0 = 0; i0 < n_parts; i0 += kIn) {
+        float pm[kIn][MT][2], pl[kIn][MT][2], po[kIn][MT][2][2 * kNT];
 #pragma unroll
-        for (int a = 0; a < MT; ++a)
+        for (int u = 0; u < kIn; ++u) {
+          const float* src = slot_of(min(i0 + u, n_parts - 1));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int r = min(a * 16 + li + 8 * h, nrows - 1);  // idle rows repeat the last one's loads
-            pm[a][h] = __ldcg(src + C::kRows * D + r);
-            pl[a][h] = __ldcg(src + C::kRows * (D + 1) + r);
-            const float* row = src + r * D + warp * kCols;
-            if constexpr (MX) {
+          for (int a = 0; a < MT; ++a)
 #pragma unroll
-              for (int n = 0; n < kNT; n += 2) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(row + n * 8 + 4 * lc));
-                po[a][h][2 * n] = x.x, po[a][h][2 * n + 2] = x.y, po[a][h][2 * n + 1] = x.z, po[a][h][2 * n + 3] = x.w;
-              }
-            } else {
+            for (int h = 0; h < 2; ++h) {
+              const int r = min(a * 16 + li + 8 * h, nrows - 1);  // idle rows repeat the last one's loads
+              pm[u][a][h] = __ldcg(src + C::kRows * D + r);
+              pl[u][a][h] = __ldcg(src + C::kRows * (D + 1) + r);
+              const float* row = src + r * D + warp * kCols;
+              float(&o1)[2 * kNT] = po[u][a][h];
+              if constexpr (MX) {
 #pragma unroll
-              for (int n = 0; n < kNT; ++n) {
-                const float2 x = __ldcg(reinterpret_cast<const float2*>(row + n * 8 + 2 * lc));
-                po[a][h][2 * n] = x.x, po[a][h][2 * n + 1] = x.y;
+                for (int n = 0; n < kNT; n += 2) {
+                  const float4 x = __ldcg(reinterpret_cast<const float4*>(row + n * 8 + 4 * lc));
+                  o1[2 * n] = x.x, o1[2 * n + 2] = x.y, o1[2 * n + 1] = x.z, o1[2 * n + 3] = x.w;
+                }
+              } else {
+#pragma unroll
+                for (int n = 0; n < kNT; ++n) {
+                  const float2 x = __ldcg(reinterpret_cast<const float2*>(row + n * 8 + 2 * lc));
+                  o1[2 * n] = x.x, o1[2 * n + 1] = x.y;
+                }
               }
             }
-          }
+        }
 #pragma unroll
-        for (int a = 0; a < MT; ++a)
+        for (int u = 0; u < kIn; ++u) {
+          if (i0 + u >= n_parts) break;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float nm = fmaxf(m[a][h], pm[a][h]);
-            const float c0 = m[a][h] == nm ? 1.f : ex2(m[a][h] - nm), c1 = pm[a][h] == nm ? 1.f : ex2(pm[a][h] - nm);
-            m[a][h] = nm;
-            l[a][h] = fmaf(pl[a][h], c1, l[a][h] * c0);
+          for (int a = 0; a < MT; ++a)
 #pragma unroll
-            for (int n = 0; n < kNT; ++n)
+            for (int h = 0; h < 2; ++h) {
+              const float nm = fmaxf(m[a][h], pm[u][a][h]);
+              const float c0 = m[a][h] == nm ? 1.f : ex2(m[a][h] - nm);
+              const float c1 = pm[u][a][h] == nm ? 1.f : ex2(pm[u][a][h] - nm);
+              m[a][h] = nm;
+              l[a][h] = fmaf(pl[u][a][h], c1, l[a][h] * c0);
 #pragma unroll
-              for (int y = 0; y < 2; ++y)
-                o[a][n][2 * h + y] = fmaf(po[a][h][2 * n + y], c1, o[a][n][2 * h + y] * c0);
-          }
+              for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                  o[a][n][2 * h + y] = fmaf(po[u][a][h][2 * n + y], c1, o[a][n][2 * h + y] * c0);
+            }
+        }
       }
     };
     // counts this block in; true for the last of n
