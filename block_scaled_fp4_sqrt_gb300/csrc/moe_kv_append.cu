@@ -4,7 +4,8 @@
 // bf16 or 8 bytes of E4M3 twice.  The loads of the new values do not wait for the page lookup.
 // Memory-bound for prompts, latency-bound (length -> page -> store) for a step's few rows.  All index arithmetic is 32-bit
 // with divisions by multiplication: with 64-bit divisions, and K and V in threads of their own, instructions were the
-// bound (81 % of the issue slots, 15.2 us for a prompt of 8191 tokens, 8 heads of 128 in bf16).
+// bound (81 % of the issue slots, 15.2 us for a prompt of 8191 tokens, 8 heads of 128 in bf16).  Measured now: that prompt
+// 7.0 us where it stays in the L2 cache, 32,000 tokens 43.7 us (6.0 TB/s), a step of 64 x 8 rows in MXFP8 2.2 us.
 #include <algorithm>
 
 #include "moe_decode_device.cuh"
