@@ -490,3 +490,21 @@ def test_attend_a_later_token_of_the_largest_scale_stays_out(moe, D):
     cache.v_scales[page, row] = 254
     got = cache.attend(q)
     assert torch.allclose(got[:, :2].float(), want[:, :2].float(), rtol=2 * HALF_ULP, atol=2 * HALF_ULP)
+
+
+def test_append_more_rows_than_one_launch_takes(moe):
+    """2^27 and some tokens of a head of 64 (17 GB of keys): beyond 2^30 units the call goes on in a second launch."""
+    L, D, page = 2 ** 27 + 1003, 64, 2 ** 20
+    n_pages = -(-L // page)
+    bits = torch.arange(L * D // 4, dtype=torch.int64, device=DEV) * 0x0001000300050007  # four columns, none alike
+    new = bits.view(BF).view(1, L, 1, D)
+    table = torch.arange(n_pages, dtype=torch.int32, device=DEV).flip(0).reshape(1, -1).contiguous()
+    cache = moe.PagedKVCache(*(torch.zeros(n_pages, page, 1, D, dtype=BF, device=DEV) for _ in "kv"), table,
+                             torch.tensor([L], dtype=torch.int32, device=DEV))
+    cache.append(new, new)
+    cache.check()
+    rows = new.view(torch.int16).view(L, D)
+    for pages in (cache.k, cache.v):
+        for j in range(n_pages):
+            n = min(page, L - j * page)
+            assert torch.equal(pages[n_pages - 1 - j, :n, 0].view(torch.int16), rows[j * page:j * page + n])
