@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Warp hw owns the ring slots hw, hw + n_own, .. (n_own divides the ring): into the down stages there it puts the
     // slot's tokens' next 512 columns of h, as fp16 code * 2^(e - E + 7) with E the row's largest block exponent.  It
     // waits for and releases all stages of its slots, up stages too, so that it sees each of their phases.
-    const int n_own = min(kHWarps, a.stages), hw = warp - kMmaWarps - kEpiWarps;
+    const int n_own = a.stages == 6 ? 3 : min(kHWarps, a.stages), hw = warp - kMmaWarps - kEpiWarps;
     if (hw < n_own) {
       // The block's down stages are numbered from n_up_st, per_item to a down item; its first down item is it0.
       const int up_st = (kg_up + kStageKg - 1) / kStageKg, per_item = (kg_down + kStageKg - 1) / kStageKg;
@@ -857,7 +857,7 @@ static size_t few_smem(int T, int d, int stages, int red_shift) {
 }
 
 int few_stages(int T, int d, int* red_shift) {
-  for (int n = kMaxStages; n >= 2; n /= 2)
+  for (int n = kMaxStages; n >= 2; n -= 2)
     for (int rs = 1; rs >= 0; --rs)
       if (few_smem(T, d, n, rs) <= 232448) {
         if (red_shift) *red_shift = rs;
