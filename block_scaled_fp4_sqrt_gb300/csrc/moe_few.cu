@@ -673,6 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.red_empty[buf]);
+      // all tokens' rows first: one fence and one round of counting for them together
 #pragma unroll
       for (int i = 0; i < kEpiTok; ++i) {
         const int n = first + i * kEpiWarps;
@@ -690,33 +691,41 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint16_t code = e4m3x2(hv * exp2_neg_int(e), 0.f);
           a.h[row * f + q * 32 + lane] = (uint8_t)code;
           if (lane == 0) a.h_s[row * (f / 32) + q] = (uint8_t)(e + 127);
-          __threadfence();
-          __syncwarp();
-          if (lane == 0) atomicAdd(a.counters + kFewSlotDone + s, 1);
         } else {
           const float w = ch < k ? sh.w[t][ch] : 1.f, fx = sh.hfx[n_item % kFxItems][n];
           float* dst = a.rows + row * d + q * 64;
           __stcg(dst + lane, v0[i] * fx * w);
           __stcg(dst + 32 + lane, v1[i] * fx * w);
-          __threadfence();
-          __syncwarp();
-          int last = 0;
-          if (lane == 0) last = atomicAdd(a.counters + kFewColsDone + q * kMaxT + t, 1) == __popc(sh.taken[t]) + has_shared - 1;
-          if (__shfl_sync(0xFFFFFFFFu, last, 0)) {  // the token's rows are complete in these columns
-            __threadfence();
-            const float* src = a.rows + (size_t)t * (k + 1) * d + q * 64 + 2 * lane;
-            float2 y = make_float2(0.f, 0.f);
-            const uint32_t own = sh.taken[t];
-#pragma unroll 8
-            for (int z = 0; z <= k; ++z) {
-              if (z < k ? !((own >> z) & 1u) : !has_shared) continue;
-              const float2 r = __ldcg(reinterpret_cast<const float2*>(src + (size_t)z * d));
-              y.x += r.x;
-              y.y += r.y;
-            }
-            *reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)t * d + q * 64 + 2 * lane) = __floats2bfloat162_rn(y.x, y.y);
-          }
         }
+      }
+      const int mine = first < cnt ? (cnt - first + kEpiWarps - 1) / kEpiWarps : 0;  // tokens of this warp
+      if (mine == 0) continue;
+      __threadfence();
+      __syncwarp();
+      if (up) {
+        if (lane == 0) atomicAdd(a.counters + kFewSlotDone + s, mine);
+        continue;
+      }
+      bool last = false;  // lane i, token i: its rows are complete in these columns
+      if (lane < mine) {
+        const int t = sh.slot_tok[s][first + lane * kEpiWarps];
+        last = atomicAdd(a.counters + kFewColsDone + q * kMaxT + t, 1) == __popc(sh.taken[t]) + has_shared - 1;
+      }
+      uint32_t complete = __ballot_sync(0xFFFFFFFFu, last);
+      if (complete) __threadfence();
+      for (; complete; complete &= complete - 1) {
+        const int t = sh.slot_tok[s][first + (__ffs(complete) - 1) * kEpiWarps];
+        const float* src = a.rows + (size_t)t * (k + 1) * d + q * 64 + 2 * lane;
+        float2 y = make_float2(0.f, 0.f);
+        const uint32_t own = sh.taken[t];
+#pragma unroll 8
+        for (int z = 0; z <= k; ++z) {
+          if (z < k ? !((own >> z) & 1u) : !has_shared) continue;
+          const float2 r = __ldcg(reinterpret_cast<const float2*>(src + (size_t)z * d));
+          y.x += r.x;
+          y.y += r.y;
+        }
+        *reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)t * d + q * 64 + 2 * lane) = __floats2bfloat162_rn(y.x, y.y);
       }
     }
   } else {
