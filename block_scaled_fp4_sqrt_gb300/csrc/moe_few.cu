@@ -5,26 +5,26 @@
 // token, about 0.6 GB for eight), so a step should take their time at HBM rate.  What moe_forward loses against that at
 // these sizes are the gaps between its five kernels; here one persistent block per SM keeps a ring of weight
 // tiles in flight from the routing to the end.
-// Measured (d = 4096, f = 2048, 256 experts, graph replays; moe_forward beside it): one token 32.3 us against 42.5
+// Measured (d = 4096, f = 2048, 256 experts, graph replays; moe_forward beside it): one token 31.2 us against 42.5
 // (14.6 at HBM rate: a cooperative launch takes about 5, the routing 5.7, the weights then arrive at 5.7 TB/s), two 45
-// against 62, three 64 against 63, four 80 against 81, eight 136 against 118 (90.8 at HBM rate).  From three tokens
-// on the two are level, and at eight moe_forward leads: x, the partial products and the h slices of eight tokens leave
-// shared memory for four stages, and the instructions (60 % of the issue slots) get in each other's way.
+// against 61, three 63 against 62, four 80 against 79, five 96 against 97, eight 132 against 116 (90.8 at HBM rate).
+// From three tokens on the two are level, and at eight moe_forward leads: x, the partial products and the h slices of
+// eight tokens leave shared memory for four stages, and the instructions (60 % of the issue slots) get in each other's
+// way.  What it keeps is that a token's row has the same bits alone and in any company.
 //
 //  1. Router.  Block b computes the fp32 logits of experts b, b + grid, .. for all tokens (its warps split d);
 //     the same pass loads x and quantises it to MXFP8.  A grid-wide count, then every block selects the top-k of
 //     every token for itself and lists the touched experts (slots) with their tokens.
 //  2. Work items, dealt to the blocks in turn: for every slot f/32 gate-up items (32 gate and 32 up rows of W13, one
-//     MX block of h), then for every slot d/64 down items (64 rows of W2).  The blocks never meet in between: a
+//     MX block of h), then for every slot d/64 down items (64 rows of W2); the shared expert is the first slot.  The blocks never meet in between: a
 //     down item waits for its own slot's gate-up items (a counter a slot), which came earlier in the list, and
 //     its weights are already in the ring by then.
 //  3. A down item's rows, times their routing weight, go to fp32 rows [token][choice][d]; the last item of a
 //     (64 columns, token) pair sums the token's rows in order (choices, then the shared expert) and rounds once.
 //
 // A block: 2 producer warps (TMA: stages of 64 weight rows x 512, 16 KB with 64-byte swizzle, and their scale atoms,
-// two copies a stage), 16 product warps (two
-// groups that take the stages in turn; in a group the stage's 4 K groups x 2 pairs of row tiles), 2 epilogue warps, and 4 warps that
-// bring the h slices of down stages into the ring.
+// two copies a stage), 16 product warps (two groups that take the stages in turn; in a group the stage's 4 K groups x 2
+// pairs of row tiles), 2 epilogue warps, and 4 warps that bring the h slices of down stages into the ring.
 //
 // Products run on mma.sync m16n8k16 with the weight rows as M and up to 8 tokens as N: E2M1 weights become fp16 by
 // one conversion a pair (exact); x and h are fp16 too: their E4M3 codes with the block scales folded in relative to
@@ -60,7 +60,7 @@ constexpr int kMaxK = 16;
 constexpr int kMaxSlots = kFewMaxSlots;
 constexpr int kRedStride = 9;                    // floats a row of the partial products (8 tokens)
 constexpr int kRedFloats = kSplits * 64 * kRedStride;
-constexpr int kMaxStages = 8;                    // the ring has 2, 4 or 8 stages
+constexpr int kMaxStages = 8;                    // the ring has 2, 4, 6 or 8 stages
 constexpr int kFxItems = 16;                     // items in flight: at most the ring's and the two partial buffers'
 static_assert(kMaxStages + 2 < kFxItems, "a row factor must outlive its item");
 
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kProducer) {
     // -------------------------------------------------------------- producers
     // Two warps take the stages in turn: beside busy product warps one thread's waits and copies do not keep up.  The
-    // ring's 2, 4 or 8 stages are even in number: a slot always belongs to the same producer.
+    // ring's 2, 4, 6 or 8 stages are even in number: a slot always belongs to the same producer.
     if (lane == 0 && !a.stall) {
       const uint64_t policy = l2_policy_evict_first();
       const int mine = warp - kProducer;
