@@ -128,7 +128,8 @@ MOE_API moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_
 
 /*
  * moe_forward for a batch of at most MOE_FEW_MAX_T rows, in one kernel: the same routing, MXFP8 activations,
- * experts and combine (see moe.h), with the weighted expert rows summed in fp32 as they are.  Arguments and
+ * experts and combine (see moe.h), with the weighted expert rows summed in fp32 as they are; a token's row has the
+ * same bits alone and in any company.  The faster call for one or two rows; above four moe_forward is.  Arguments and
  * errors are moe_forward's; the expert sets must use MOE_ACT_MXFP8, and n_experts <= 512 for the learned router.
  * topk_ids int32 [T, top_k] and topk_w fp32 [T, top_k] receive the routing (each may be NULL).  Uses the
  * workspace of `experts`.  The kernel's blocks wait on one another: it is launched cooperatively, one block per
