@@ -16,16 +16,15 @@ MOE_KV_BF16, MOE_KV_MXFP8 = 0, 1
 KV_STATUS = {1: "a sequence length outside the block table", 2: "a page index outside the cache"}
 
 
-def _rows(t: torch.Tensor | None, name: str, shape, dtype=torch.bfloat16) -> int | None:
-    """Address of a row-strided 2-D CUDA tensor with contiguous columns."""
-    if t is None:
-        return None
+def _rows(t: torch.Tensor, name: str, shape, dtype=torch.bfloat16) -> tuple[int, int]:
+    """Address and row stride of a row-strided 2-D CUDA tensor with contiguous columns."""
     if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
-    if t.stride(1) != 1 and shape[1] > 1:
+    row, col = t.stride()
+    if col != 1 and shape[1] > 1:
         raise ValueError(f"the columns of {name} must be contiguous")
-    return t.data_ptr()
+    return t.data_ptr(), row
 
 
 def moe_add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None, weight: torch.Tensor, eps: float = 1e-6,
@@ -44,22 +43,23 @@ def moe_add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None, weight: tor
     if not (w32 or weight.dtype is torch.bfloat16) or weight.shape != (d,) or not weight.is_contiguous() or \
             not weight.is_cuda:
         raise ValueError(f"weight must be a contiguous bf16 or fp32 CUDA tensor of {d} columns")
+    xp, xs = _rows(x, "x", shape)
+    rp, rs = (None, 0) if residual is None else _rows(residual, "residual", shape)
+    up, us = (None, 0) if sum_out is None else _rows(sum_out, "sum_out", shape)
+    yp, ys = (None, 0) if y is None else _rows(y, "y", shape)
     qp = sp = None
     if y_q is not None:
-        qp = _rows(y_q, "y_q", shape, torch.uint8)
-        if not y_q.is_contiguous():
+        qp, row = _rows(y_q, "y_q", shape, torch.uint8)
+        if row != d and T > 1:
             raise ValueError("y_q must be contiguous")
     if y_s is not None:
-        sp = _rows(y_s, "y_s", (T, d // 32), torch.uint8)
-        if not y_s.is_contiguous():
+        sp, row = _rows(y_s, "y_s", (T, d // 32), torch.uint8)
+        if row != d // 32 and T > 1:
             raise ValueError("y_s must be contiguous")
-    lone = T <= 1  # the stride of a lone row means nothing
-    a = moe_norm_t(_rows(x, "x", shape), _rows(residual, "residual", shape), weight.data_ptr(),
-                   _rows(sum_out, "sum_out", shape), _rows(y, "y", shape), qp, sp,
-                   0 if lone else x.stride(0), 0 if lone or residual is None else residual.stride(0),
-                   0 if lone or sum_out is None else sum_out.stride(0), 0 if lone or y is None else y.stride(0),
-                   T, d, w32, eps)
-    status = lib().moe_add_rms_norm(ctypes.byref(a), _raw_stream(stream))
+    if T <= 1:  # the stride of a lone row means nothing
+        xs = rs = us = ys = 0
+    status = lib().moe_add_rms_norm(moe_norm_t(xp, rp, weight.data_ptr(), up, yp, qp, sp, xs, rs, us, ys, T, d, w32, eps),
+                                    _raw_stream(stream))
     if status:
         _ok("moe_add_rms_norm", status)
 
@@ -108,6 +108,7 @@ class PagedKVCache:
                                  heads, d, self.n_seqs, block_table.shape[1])
         self._ref = ctypes.byref(self._c)
         self._workspaces = {}
+        self._index = k.get_device()
 
     @classmethod
     def allocate(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, block_table: torch.Tensor,
@@ -125,7 +126,7 @@ class PagedKVCache:
     def _step_rows(self, t: torch.Tensor, name: str, heads: int | None = None, dtype=torch.bfloat16):
         """(L, heads, row stride) of [n_seqs, L, heads, head_dim] whose rows (b, l) lie at one stride."""
         shape = t.shape
-        if len(shape) != 4 or t.dtype is not dtype or t.device != self.device or shape[0] != self.n_seqs or \
+        if len(shape) != 4 or t.dtype is not dtype or t.get_device() != self._index or shape[0] != self.n_seqs or \
                 shape[3] != self.head_dim or (heads is not None and shape[2] != heads):
             raise ValueError(f"{name} must be {dtype} [{self.n_seqs}, L, {heads or 'heads'}, {self.head_dim}] on "
                              f"{self.device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
@@ -175,7 +176,7 @@ class PagedKVCache:
         if Lo != L:
             raise ValueError("q and out hold different numbers of tokens")
         if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:3] or not lse.is_contiguous() or
-                                lse.device != self.device):
+                                lse.get_device() != self._index):
             raise ValueError(f"lse must be a contiguous fp32 tensor of shape {tuple(q.shape[:3])}")
         if q.numel() == 0:
             return out
