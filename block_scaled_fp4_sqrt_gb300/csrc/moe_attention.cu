@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
     }
   };
 
-  // ---- the scores of this warp's 16 tokens, in log2 units, and their masks
+  // ---- the scores of this warp's 16 tokens, in log2 units less the running maximum (or 0), and their masks
   float s[MT][2][4];
   auto scores = [&](int stage) {
     const uint32_t kb = smem_base + stage * C::kStageBytes + tok_first * C::kRowBytes;
@@ -553,9 +553,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
 #pragma unroll
     for (int a = 0; a < MT; ++a)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int h = 0; h < 2; ++h) {
+        const float ref = m[a][h] == -INFINITY ? 0.f : m[a][h];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[a][n][e] *= f[a][e >> 1];
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) s[a][n][2 * h + e] = fmaf(s[a][n][2 * h + e], f[a][h], -ref);
+      }
     const int tok0 = cur.t * kTile + tok_first;
     if (tok0 + kWarpTok > cur.len - p.L + 1) {  // some row does not see all of them
 #pragma unroll
@@ -578,10 +582,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
     for (int a = 0; a < MT; ++a)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float ref = m[a][h] == -INFINITY ? 0.f : m[a][h];
         float e[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[i] = ex2(s[a][i >> 1][2 * h + (i & 1)] - ref);
+        for (int i = 0; i < 4; ++i) e[i] = ex2(s[a][i >> 1][2 * h + (i & 1)]);
         sum[a][h] = (e[0] + e[1]) + (e[2] + e[3]);
         const uint32_t at = p_base + (a * 16 + li + 8 * h) * kPPitch + (tok_first + 2 * lc) * 2;
         asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(pack_bf16(e[0], e[1])) : "memory");
@@ -986,7 +989,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         grow |= fmaxf(fmaxf(s[a][0][2 * h], s[a][0][2 * h + 1]), fmaxf(s[a][1][2 * h], s[a][1][2 * h + 1])) >
-                m[a][h] + kGrow;
+                (m[a][h] == -INFINITY ? -INFINITY : kGrow);
     float add[MT][2];
     put_p(add);
     if (__syncthreads_or(grow)) {
@@ -1005,10 +1008,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int r = a * 16 + li + 8 * h;
-          const float nm = fmaxf(fmaxf(fmaxf(s_mx[r], s_mx[C::kRows + r]),
-                                       fmaxf(s_mx[2 * C::kRows + r], s_mx[3 * C::kRows + r])), m[a][h]);
-          const float c = m[a][h] == nm ? 1.f : ex2(m[a][h] - nm);
+          // by how much the maximum grows (from 0 where there was none)
+          const float up = fmaxf(fmaxf(s_mx[r], s_mx[C::kRows + r]), fmaxf(s_mx[2 * C::kRows + r], s_mx[3 * C::kRows + r]));
+          const float old = m[a][h], ref = old == -INFINITY ? 0.f : old;
+          const float nm = fmaxf(up + ref, old);
+          const float c = old == nm ? 1.f : ex2(old - nm);
+          const float less = nm == -INFINITY ? 0.f : nm - ref;
           m[a][h] = nm;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) s[a][n][2 * h + e] -= less;
           l[a][h] *= c;
 #pragma unroll
           for (int n = 0; n < kNT; ++n) {
