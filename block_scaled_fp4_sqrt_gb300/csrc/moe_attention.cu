@@ -191,11 +191,11 @@ struct Cfg {
   // p may take q's place once the fragments are in registers
   static constexpr int kQPBytes = kQRegs ? (kQBytes > kPBytes ? kQBytes : kPBytes) : kQBytes + kPBytes;
   static constexpr int kStatBytes = (2 * kWarps + 2) * kRows * 4;
-  // Blocks an SM holds: three, or two where the registers leave no room for more: 64 rows, and 32 rows of a quantised
-  // cache (64 requests x 8 rows: 161 us with three blocks, 143 us with two).  A bf16 cache of 128 columns keeps only two
-  // stages beside three blocks and is still faster (64 x 8 rows 117 against 128 us, 64 x 1 rows 80 against 88 us with
-  // two blocks of three stages).
-  static constexpr int kBlocks = MT == 4 || (MT == 2 && MX) ? 2 : 3;
+  // Blocks an SM holds: three, or two where 168 registers do not hold a row tile's fragments and accumulators: 64 rows,
+  // and 32 rows of a quantised cache, of 128 columns; 64 rows of a quantised cache of 64.  64 requests, three blocks
+  // against two: 128 columns, 8 rows a head MXFP8 138 us against 108 and bf16 (with two stages left) 117 against 128; 64
+  // columns, 8 rows MXFP8 69 against 78, 16 rows MXFP8 153 against 107 and bf16 88 against 99.
+  static constexpr int kBlocks = (D == 128 ? MT == 4 || (MT == 2 && MX) : MT == 4 && MX) ? 2 : 3;
   static constexpr int kBudget = (kBlocks == 2 ? 113 : 75) * 1024 - kQPBytes - kStatBytes - 256;
   static constexpr int kFit = kBudget / kStageBytes;
   static constexpr int kStages = kFit < 2 ? 2 : kFit > 6 ? 6 : kFit;
