@@ -187,16 +187,19 @@ struct Cfg {
   static constexpr int kQPitch = 2 * D + 16;
   static constexpr int kQBytes = kRows * kQPitch;
   static constexpr int kPBytes = kRows * kPPitch;
-  static constexpr bool kQRegs = MT <= 2;                    // q fragments stay in registers
+// q fragments stay in registers, or are read from shared memory for every tile where that makes room for a block more
+  static constexpr bool kQRegs = MX ? MT == 2 && D == 64 : MT <= 2;
   // p may take q's place once the fragments are in registers
   static constexpr int kQPBytes = kQRegs ? (kQBytes > kPBytes ? kQBytes : kPBytes) : kQBytes + kPBytes;
   static constexpr int kStatBytes = (2 * kWarps + 2) * kRows * 4;
-  // Blocks an SM holds: three, or two where 168 registers do not hold a row tile's fragments and accumulators: 64 rows,
-  // and 32 rows of a quantised cache, of 128 columns; 64 rows of a quantised cache of 64.  64 requests, three blocks
-  // against two: 128 columns, 8 rows a head MXFP8 138 us against 108 and bf16 (with two stages left) 117 against 128; 64
-  // columns, 8 rows MXFP8 69 against 78, 16 rows MXFP8 153 against 107 and bf16 88 against 99.
-  static constexpr int kBlocks = (D == 128 ? MT == 4 || (MT == 2 && MX) : MT == 4 && MX) ? 2 : 3;
-  static constexpr int kBudget = (kBlocks == 2 ? 113 : 75) * 1024 - kQPBytes - kStatBytes - 256;
+  // Blocks an SM holds (registers: 255 for two, 168 for three, 128 for four).  Instruction latencies bound a quantised
+  // cache, so it takes as many as its row tile's fragments and accumulators leave.  64 requests, us: 128 columns, MXFP8,
+  // 1 row a head 77 (three, q in registers) 73 (four); 8 rows 108 (two, q in registers) 138 (three, spilling) 97 (three, q
+  // from shared memory); 64 columns, MXFP8, 8 rows 78 (two) 68 (three) 67 (four, but 200 short requests 14.7 -> 15.8), 16
+  // rows 107 (two) 153 (three); bf16 of 128 columns, 8 rows 128 (two) 117 (three, with two stages left); of 64 columns,
+  // 16 rows 99 (two) 88 (three).
+  static constexpr int kBlocks = MX && MT == 1 ? 4 : MT == 4 && (MX || D == 128) ? 2 : 3;
+  static constexpr int kBudget = (kBlocks == 2 ? 113 : kBlocks == 3 ? 75 : 56) * 1024 - kQPBytes - kStatBytes - 256;
   static constexpr int kFit = kBudget / kStageBytes;
   static constexpr int kStages = kFit < 2 ? 2 : kFit > 6 ? 6 : kFit;
   static constexpr int kSmem = kStages * kStageBytes + kQPBytes + kStatBytes + 256;
@@ -1086,7 +1089,7 @@ moe_status_t plan(const moe_kv_cache_t& c, int n_q_heads, int L, int num_sms, co
   z->row_tiles = (int)((z->rows + tr - 1) / tr);
   const int64_t units = (int64_t)c.n_seqs * c.n_kv_heads * z->row_tiles;
   if (units > (1ll << 30)) return decode_fail(MOE_ERR_UNSUPPORTED, "%s: too many row tiles", call);
-  z->blocks = num_sms * 3;  // the most blocks an SM holds
+  z->blocks = num_sms * 4;  // the most blocks an SM holds
   z->groups = z->blocks / kJoin + 1;
   z->units = (size_t)units;
   z->counters = ((z->units + 2 * z->groups) * 4 + 255) / 256 * 256;
