@@ -5,8 +5,8 @@
 // The cache is read once, so a step's few rows a key-value head (heads of the group x L) leave it memory-bound where the
 // cache is bf16: three requests of up to 131,071 tokens 147 us (6.2 TB/s, 93 % of the copy rate), 64 requests x 8 rows
 // 93 us (5.3 TB/s).  An MXFP8 cache is half the bytes, and then the instructions bound it (unpacking, softmax and their
-// latencies at eight warps an SM): 64 x 8 rows 107 us, 64 x 1 rows 77 us, where memory alone would take 38.  One request
-// of 333 tokens takes 8.1 us, of which the join of its six parts is about half.
+// latencies at 12 to 16 warps an SM): 64 x 8 rows 96 us, 64 x 1 rows 72 us, where memory alone would take 38.  One request
+// of 333 tokens takes 8.4 us, of which the join of its six parts is about half.
 // Layout of the work:
 //  * A unit is (request, kv head, row tile): the rows r = l * group + j of the query heads that share the kv head,
 //    16 MT of them at a time.  Every unit is cut into tiles of 64 tokens; the tiles of all units, in order and with
@@ -22,12 +22,12 @@
 //  * A unit that several blocks share is joined, in block order, by the last of them to arrive (a counter per unit,
 //    zero between calls); more than 16 parts in two steps, of which the first runs in many blocks at once.
 //
-// Products run on mma.sync, at a measured 605 TFLOP/s for the 16-bit forms (m16n8k16): 26 % (MXFP8) and 31 % (bf16) of
+// Products run on mma.sync, at a measured 605 TFLOP/s for the 16-bit forms (m16n8k16): 29 % (MXFP8) and 31 % (bf16) of
 // its cycles at 32 rows a kv head.  The form for tensor memory was built and measured for MXFP8 caches: both products
 // transposed, so that the 128-row side is the cache's (K as it lies, block-scaled, times q in two MXFP8 parts; V unpacked
 // to bf16 as an MN-major operand), warps of their own for fetching and unpacking, issuing and softmax.  A 128 x 16 x 32
 // product takes 80 cycles there whatever its 16 columns hold, and the roles' code together misses the instruction cache;
-// 64 requests x 8 rows took 116 us against 107 us here, 64 x 1 rows 93 against 77 us.
+// 64 requests x 8 rows took 116 us against 96 us here, 64 x 1 rows 93 against 72 us.
 //  * bf16 cache: both products in bf16 with fp32 accumulation.  p is rounded to bf16 (8 bits, as the output is);
 //    its sum is taken before that rounding.
 //  * MXFP8 cache, scores: E4M3 codes become fp16 (exact, one conversion a pair) and meet q in fp16, its row scaled by
