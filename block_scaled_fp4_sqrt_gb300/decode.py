@@ -24,6 +24,8 @@ def _rows(t: torch.Tensor, name: str, shape, dtype=torch.bfloat16) -> tuple[int,
     row, col = t.stride()
     if col != 1 and shape[1] > 1:
         raise ValueError(f"the columns of {name} must be contiguous")
+    if row == 0 and shape[0] > 1:  # the library reads stride 0 as contiguous rows
+        raise ValueError(f"{name} is broadcast: its rows must lie in memory of their own")
     return t.data_ptr(), row
 
 
@@ -32,8 +34,9 @@ def moe_add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None, weight: tor
                      y_q: torch.Tensor | None = None, y_s: torch.Tensor | None = None, stream=None) -> None:
     """sum_out = bf16(x + residual); y = bf16((x + residual) * weight / rms); (y_q, y_s) = MXFP8(y).
 
-    x, residual, sum_out, y: bf16 [T, d] (row-strided views allowed); weight: bf16 or fp32 [d]; y_q: uint8
-    [T, d] E4M3 codes and y_s: uint8 [T, d / 32] E8M0 bytes, contiguous, as ``moe_permute`` writes them.
+    x, residual, sum_out, y: bf16 [T, d] (row-strided views allowed, broadcast rows not); weight: bf16 or fp32
+    [d]; y_q: uint8 [T, d] E4M3 codes and y_s: uint8 [T, d / 32] E8M0 bytes, contiguous, as ``moe_permute``
+    writes them.
     residual and each output may be None; sum_out may be x or residual, y may be x."""
     shape = x.shape
     if len(shape) != 2:
@@ -134,7 +137,10 @@ class PagedKVCache:
         sb, sl, sh, sd = t.stride()
         if sd != 1 or (h > 1 and sh != d) or (B > 1 and L > 1 and sb != L * sl):
             raise ValueError(f"{name}: heads must be contiguous and the rows (request, token) at one stride")
-        return L, h, 0 if B * L <= 1 else (sl if L > 1 else sb)
+        row = sl if L > 1 else sb
+        if row == 0 and B * L > 1:  # the library reads stride 0 as contiguous rows
+            raise ValueError(f"{name} is broadcast: its rows must lie in memory of their own")
+        return L, h, 0 if B * L <= 1 else row
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, stream=None) -> None:
         """Write the step's L new tokens: bf16 [n_seqs, L, n_kv_heads, head_dim], token l of request b at

@@ -1,0 +1,111 @@
+"""What the Python calls of the decode step hand to the library: traced on the CPU with stand-ins for tensors on a GPU,
+the library and the stream."""
+import pytest
+import torch
+
+BF = torch.bfloat16
+
+
+class OnGpu:
+    """A CPU tensor that says it lies on GPU `index`: what the binding reads of a tensor before it passes its address."""
+
+    def __init__(self, t: torch.Tensor, index: int = 0):
+        self.t, self.index = t, index
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    is_cuda = True
+
+    @property
+    def device(self):
+        return torch.device("cuda", self.index)
+
+    def get_device(self):
+        return self.index
+
+
+def zeros(*shape, dtype=BF, index=0):
+    return OnGpu(torch.zeros(*shape, dtype=dtype), index)
+
+
+def expand(t: OnGpu, *shape):
+    return OnGpu(t.t.expand(*shape), t.index)
+
+
+class Library:
+    """Records the calls and their arguments; every call succeeds."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 0
+        return call
+
+
+@pytest.fixture
+def m(monkeypatch):
+    import block_scaled_fp4_sqrt_gb300 as mod
+    from block_scaled_fp4_sqrt_gb300 import decode
+    library = Library()
+    for at in (mod, decode):
+        monkeypatch.setattr(at, "lib", lambda: library)
+        monkeypatch.setattr(at, "_raw_stream", lambda stream: 0 if stream is None else int(stream))
+    mod.library = library
+    yield mod
+    del mod.library
+
+
+def cache(m, n_seqs=3, heads=2, head_dim=64):
+    c = object.__new__(m.PagedKVCache)
+    c.n_seqs, c.n_kv_heads, c.head_dim = n_seqs, heads, head_dim
+    c.device, c._index, c._ref, c._workspaces = torch.device("cuda", 0), 0, None, {}
+    return c
+
+
+# ---------------------------------------------------------------------------------------------- broadcast rows
+def test_norm_passes_row_strides_and_refuses_broadcast_rows(m):
+    """The library reads stride 0 as contiguous rows: a broadcast tensor would be read and written past its end."""
+    w, wide, lone = zeros(64), zeros(4, 200), zeros(1, 64)
+    x = OnGpu(wide.t[:, 72:136])
+    m.moe_add_rms_norm(x, None, w, y=zeros(4, 64))
+    args = m.library.calls[-1][1][0]
+    assert (args.T, args.d, args.x_stride, args.y_stride) == (4, 64, 200, 64)
+    m.moe_add_rms_norm(lone, expand(lone, 1, 64), w, y=lone)  # one row has no stride
+    rows, calls = expand(lone, 4, 64), len(m.library.calls)
+    full = zeros(4, 64)
+    for kw in (dict(x=rows, residual=None, y=full), dict(x=full, residual=rows, y=full),
+               dict(x=full, residual=None, y=rows), dict(x=full, residual=None, sum_out=rows)):
+        with pytest.raises(ValueError, match="row"):
+            m.moe_add_rms_norm(weight=w, **kw)
+    u8 = torch.uint8
+    with pytest.raises(ValueError):
+        m.moe_add_rms_norm(full, None, w, y_q=expand(zeros(1, 64, dtype=u8), 4, 64), y_s=zeros(4, 2, dtype=u8))
+    with pytest.raises(ValueError):
+        m.moe_add_rms_norm(full, None, w, y_q=zeros(4, 64, dtype=u8), y_s=expand(zeros(1, 2, dtype=u8), 4, 2))
+    assert len(m.library.calls) == calls
+
+
+@pytest.mark.parametrize("L", [1, 2])
+def test_append_and_attend_refuse_broadcast_rows(m, L):
+    c = cache(m)
+    full, fq = zeros(3, L, 2, 64), zeros(3, L, 4, 64)
+    c.append(full, full)
+    assert m.library.calls[-1][1][2] == 2 * 64
+    calls = len(m.library.calls)
+    for t in (expand(zeros(1, 1, 2, 64), 3, L, 2, 64), expand(zeros(1, L, 2, 64), 3, L, 2, 64)):
+        for args in ((t, full), (full, t)):
+            with pytest.raises(ValueError):
+                c.append(*args)
+    for q in (expand(zeros(1, 1, 4, 64), 3, L, 4, 64), expand(zeros(1, L, 4, 64), 3, L, 4, 64)):
+        for args in ((q, fq), (fq, q)):
+            with pytest.raises(ValueError):
+                c.attend(*args)
+    one = cache(m, n_seqs=1)
+    if L > 1:
+        with pytest.raises(ValueError):
+            one.append(expand(zeros(1, 1, 2, 64), 1, L, 2, 64), zeros(1, L, 2, 64))
+    assert len(m.library.calls) == calls
