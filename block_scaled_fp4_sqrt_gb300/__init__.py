@@ -162,6 +162,13 @@ def _input(x: torch.Tensor, token_ids: torch.Tensor | None = None) -> moe_input_
                        None if token_ids is None else ctypes.c_void_p(token_ids.data_ptr()))
 
 
+def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> None:
+    """A kernel reads or writes t as dense rows of this type and shape."""
+    if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}, strides {t.stride()}")
+
+
 def make_config(d_model: int, d_ff: int, n_experts: int, top_k: int, route_scale: float = 1.5,
                 swiglu_limit: float = 10.0) -> moe_config_t:
     return moe_config_t(d_model, d_ff, n_experts, top_k, route_scale, swiglu_limit)
@@ -215,8 +222,17 @@ def moe_forward(x, router_w, router_bias, experts, shared, out, token_ids=None, 
 
 def moe_forward_few(x, router_w, router_bias, experts, shared, out, topk_ids=None, topk_w=None, token_ids=None,
                     stream=None) -> None:
-    """moe_forward for at most MOE_FEW_MAX_T rows in one kernel; topk_ids int32 and topk_w fp32 [T, top_k]
-    receive the routing."""
+    """moe_forward for at most MOE_FEW_MAX_T rows in one kernel: x and out bf16 [T, d], token_ids int32 [T or more];
+    topk_ids int32 and topk_w fp32 [T, top_k] receive the routing."""
+    T = x.shape[0]
+    _dense(x, "x", torch.bfloat16, (T, *x.shape[1:2]))
+    _dense(out, "out", torch.bfloat16, x.shape)
+    if token_ids is not None:
+        _dense(token_ids, "token_ids", torch.int32, (max(T, token_ids.shape[0]),))
+    if topk_ids is not None:
+        _dense(topk_ids, "topk_ids", torch.int32, (T, *topk_ids.shape[1:2]))
+    if topk_w is not None:
+        _dense(topk_w, "topk_w", torch.float32, (T, *topk_w.shape[1:2]))
     _ok("moe_forward_few", lib().moe_forward_few(ctypes.byref(_input(x, token_ids)), _p(router_w), _p(router_bias),
                                                  experts, shared, _p(out), _p(topk_ids), _p(topk_w), _stream(stream)))
 
@@ -433,7 +449,12 @@ class MoELayer:
     def forward_few(self, x: torch.Tensor, token_ids: torch.Tensor | None = None, out: torch.Tensor | None = None,
                     topk_ids: torch.Tensor | None = None, topk_w: torch.Tensor | None = None,
                     stream=None) -> torch.Tensor:
-        """``forward`` for at most MOE_FEW_MAX_T rows, in one kernel (MXFP8 activations)."""
+        """``forward`` for at most MOE_FEW_MAX_T rows, in one kernel (MXFP8 activations); topk_ids int32 and topk_w
+        fp32 [T, top_k], if given, receive the routing."""
+        T = x.shape[0]
+        for t, name, cols in ((x, "x", self.d), (topk_ids, "topk_ids", self.k), (topk_w, "topk_w", self.k)):
+            if t is not None and tuple(t.shape) != (T, cols):
+                raise ValueError(f"{name} must have the shape {(T, cols)}, got {tuple(t.shape)}")
         if token_ids is None and self.hash_table is not None:
             token_ids = self.token_ids
         if out is None:

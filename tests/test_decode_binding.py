@@ -34,12 +34,15 @@ def expand(t: OnGpu, *shape):
 
 
 class Library:
-    """Records the calls and their arguments; every call succeeds."""
+    """Records the calls and their arguments; every call succeeds.  (Handles of earlier tests may be collected meanwhile:
+    their destruction goes to the library.)"""
 
-    def __init__(self):
-        self.calls = []
+    def __init__(self, real):
+        self.calls, self.real = [], real
 
     def __getattr__(self, name):
+        if name.endswith("_destroy"):
+            return getattr(self.real(), name)
         def call(*args):
             self.calls.append((name, args))
             return 0
@@ -50,7 +53,7 @@ class Library:
 def m(monkeypatch):
     import block_scaled_fp4_sqrt_gb300 as mod
     from block_scaled_fp4_sqrt_gb300 import decode
-    library = Library()
+    library = Library(mod.lib)
     for at in (mod, decode):
         monkeypatch.setattr(at, "lib", lambda: library)
         monkeypatch.setattr(at, "_raw_stream", lambda stream: 0 if stream is None else int(stream))
@@ -108,4 +111,36 @@ def test_append_and_attend_refuse_broadcast_rows(m, L):
     if L > 1:
         with pytest.raises(ValueError):
             one.append(expand(zeros(1, 1, 2, 64), 1, L, 2, 64), zeros(1, L, 2, 64))
+    assert len(m.library.calls) == calls
+
+
+# ---------------------------------------------------------------------------------------------- the few-token layer
+def layer(m, d=256, k=2, hash_table=None):
+    lay = object.__new__(m.MoELayer)
+    lay.d, lay.k, lay.device, lay.hash_table, lay._handles = d, k, torch.device("cuda", 0), hash_table, []
+    lay.h = lay.h_shared = None
+    lay.router_w = lay.router_bias = None
+    lay.resident_router = True
+    return lay
+
+
+def test_forward_few_passes_what_fits_and_refuses_the_rest(m):
+    """The kernel writes dense rows of the batch's size into out, topk_ids and topk_w, whatever they are."""
+    lay, x, i32, f32 = layer(m), zeros(3, 256), torch.int32, torch.float32
+    good = dict(out=zeros(3, 256), topk_ids=zeros(3, 2, dtype=i32), topk_w=zeros(3, 2, dtype=f32))
+    assert lay.forward_few(x, **good) is good["out"]
+    assert [c[0] for c in m.library.calls] == ["moe_forward_few"]
+    lay.forward_few(x, token_ids=zeros(5, dtype=i32), **good)  # the first T of a longer list
+    lay.forward_few(zeros(0, 256), out=zeros(0, 256))
+    calls = len(m.library.calls)
+    for kw in (dict(x=zeros(3, 128)), dict(x=zeros(3, 256, dtype=f32)), dict(x=OnGpu(torch.zeros(3, 512, dtype=BF)[:, ::2])),
+               dict(x=x.t), dict(out=zeros(2, 256)), dict(out=zeros(3, 256, dtype=f32)), dict(out=zeros(3, 264)),
+               dict(out=expand(zeros(1, 256), 3, 256)), dict(topk_ids=zeros(3, 2, dtype=torch.int64)),
+               dict(topk_ids=zeros(2, 2, dtype=i32)), dict(topk_ids=zeros(3, 1, dtype=i32)), dict(topk_ids=zeros(6, dtype=i32)),
+               dict(topk_ids=OnGpu(torch.zeros(2, 3, dtype=i32).t())), dict(topk_w=zeros(3, 2, dtype=BF)),
+               dict(topk_w=zeros(3, 2, dtype=f32).t), dict(topk_w=zeros(1, 2, dtype=f32)),
+               dict(token_ids=zeros(3, dtype=torch.int64)), dict(token_ids=zeros(2, dtype=i32)),
+               dict(token_ids=OnGpu(torch.zeros(6, dtype=i32)[::2]))):
+        with pytest.raises(ValueError):
+            lay.forward_few(**{"x": x, **good, **kw})
     assert len(m.library.calls) == calls
