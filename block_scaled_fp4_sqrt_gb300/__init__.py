@@ -37,6 +37,7 @@ ACT_FORMATS = {"mxfp8": MOE_ACT_MXFP8, "mxfp4": MOE_ACT_MXFP4}
 
 MOE_N_STAGES = 5
 MOE_FEW_MAX_T = 8
+MOE_ATTENTION_COUNTER_BYTES = 4096  # the part of an attention workspace that must be zero before its first use
 STAGE_NAMES = ("route", "dispatch", "gemm_gate_up", "gemm_down", "combine")
 
 

@@ -19,8 +19,10 @@
 //    instead of four times that, quantised values are unpacked once a block, and a unit's end needs no exchange.
 //  * The running maximum of a row moves only when a score exceeds it by more than 2^8 (a vote in the barrier that
 //    publishes p): p stays below 256, which costs no precision, and accumulators are rescaled rarely.
-//  * A unit that several blocks share is joined, in block order, by the last of them to arrive (a counter per unit,
-//    zero between calls); more than 16 parts in two steps, of which the first runs in many blocks at once.
+//  * A unit that several blocks share is joined, in block order, by the last of them to arrive (a counter, zero between
+//    calls); more than 16 parts in two steps, of which the first runs in many blocks at once.  The counters stand at the
+//    front of the workspace, one for every block that a shared unit can begin in, whatever the call's shape: no call's
+//    parts ever lie where another call counts.
 //
 // Products run on mma.sync, at a measured 605 TFLOP/s for the 16-bit forms (m16n8k16): 29 % (MXFP8) and 31 % (bf16) of
 // its cycles at 32 rows a kv head.  The form for tensor memory was built and measured for MXFP8 caches: both products
@@ -72,7 +74,7 @@ struct AttnParams {
   uint32_t page_units, row_units, head_units;  // the cache's strides in 16-byte units
   float scale_log2;                   // scale * log2(e)
   PageDiv pd;
-  int* counters;    // [n_seqs * kv heads * row_tiles], zero between calls
+  int* counters;    // [grid] of the shared unit that begins in a block (at most one does), zero between calls
   float* partial;   // [grid][2][rows of a tile][head_dim + 2]
   int* group_counters;   // [grid / kJoin + 1][2], zero between calls
   float* group_partial;  // [grid / kJoin + 1][2][rows of a tile][head_dim + 2]
@@ -955,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
       return p.partial + ((size_t)b * 2 + (unit_first > b * per ? 1 : 0)) * kSlot;
     };
     put_part(block_slot(blockIdx.x));
-    int* counter = p.counters + ((int64_t)cur.b * H + cur.head) * p.row_tiles + cur.rt;
+    int* counter = p.counters + b0;
     if (parts <= kJoin) {
       if (!last_of(counter, parts)) return;
       join(parts, [&](int i) { return block_slot(b0 + i); });
@@ -1074,7 +1076,7 @@ cudaError_t launch_rows(const AttnParams& p, int num_sms, cudaStream_t s) {
 struct Sizes {
   int64_t rows;
   int row_tiles;
-  size_t blocks, groups, units, counters, slot, bytes;
+  size_t blocks, groups, slot, bytes;
 };
 
 moe_status_t plan(const moe_kv_cache_t& c, int n_q_heads, int L, int num_sms, const char* call, Sizes* z) {
@@ -1091,10 +1093,10 @@ moe_status_t plan(const moe_kv_cache_t& c, int n_q_heads, int L, int num_sms, co
   if (units > (1ll << 30)) return decode_fail(MOE_ERR_UNSUPPORTED, "%s: too many row tiles", call);
   z->blocks = num_sms * 4;  // the most blocks an SM holds
   z->groups = z->blocks / kJoin + 1;
-  z->units = (size_t)units;
-  z->counters = ((z->units + 2 * z->groups) * 4 + 255) / 256 * 256;
+  if ((z->blocks + 2 * z->groups) * 4 > MOE_ATTENTION_COUNTER_BYTES)
+    return decode_fail(MOE_ERR_UNSUPPORTED, "%s: %d SMs", call, num_sms);
   z->slot = (size_t)tr * (c.head_dim + 2) * 4;
-  z->bytes = z->counters + 2 * (z->blocks + z->groups) * z->slot;
+  z->bytes = MOE_ATTENTION_COUNTER_BYTES + 2 * (z->blocks + z->groups) * z->slot;
   return MOE_OK;
 }
 
@@ -1167,8 +1169,8 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   p.row_units = (uint32_t)(c.row_stride / unit);
   p.head_units = (uint32_t)(c.head_stride / unit);
   p.counters = static_cast<int*>(a->workspace);
-  p.group_counters = p.counters + z.units;
-  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + z.counters);
+  p.group_counters = p.counters + z.blocks;
+  p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + MOE_ATTENTION_COUNTER_BYTES);
   p.group_partial = p.partial + 2 * z.blocks * (z.slot / 4);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool mx = c.format == MOE_KV_MXFP8;

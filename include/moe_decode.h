@@ -105,11 +105,14 @@ MOE_API moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const void* k_ne
  *            0 = contiguous), 16-byte aligned.
  *   lse      fp32 [n_seqs, L, n_q_heads] or NULL.
  *   n_q_heads a multiple of n_kv_heads; L >= 0; scale finite; k and v span less than 64 GB each.
- *   workspace  moe_paged_attention_workspace(cache, n_q_heads, L) bytes, 256-byte aligned, ZERO-FILLED before
- *            its first use (calls leave it ready for the next); calls that may overlap need one each.
+ *   workspace  at least moe_paged_attention_workspace(cache, n_q_heads, L) bytes, 256-byte aligned.  Its first
+ *            MOE_ATTENTION_COUNTER_BYTES bytes must be ZERO before its first use; every call leaves them zero, and what
+ *            else it holds does not matter.  So one buffer serves any calls, of any caches and shapes, that run one
+ *            after another; calls that may overlap need one each.
  * The result does not depend on timing: the work is split over the length by a rule on the lengths alone and
  * joined in a fixed order.
  */
+#define MOE_ATTENTION_COUNTER_BYTES 4096
 typedef struct {
   const void* q;
   void* out;

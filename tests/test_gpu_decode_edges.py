@@ -1,0 +1,51 @@
+"""The decode-step operators at the edges of their contracts: workspaces that many calls share, rows that hold NaN,
+scales at the ends of E8M0, prompts of many row tiles."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+from test_gpu_decode import BF, DEV, HALF_ULP, attend_ref, check_attend, fill, gen, make_cache, moe, randn  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------------------------- workspaces
+def attend_c(moe, cache, q, ws):
+    """moe_paged_attention through the C call, in a workspace of the caller's."""
+    B, L, H, D = q.shape
+    out, lse = torch.full_like(q, float("nan")), torch.full((B, L, H), float("nan"), device=DEV)
+    a = moe.moe_attention_t(q.data_ptr(), out.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), 0, 0, H, L, D ** -0.5)
+    assert moe.lib().moe_paged_attention(cache._ref, ctypes.byref(a), torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    cache.check()
+    return out, lse
+
+
+def test_one_workspace_serves_calls_of_any_shape(moe):  # noqa: F811
+    """Parts of one call must not lie where another one counts: requests, heads, row tiles and widths that differ."""
+    shapes = [  # lens, kv, group, L, D, format
+        ([20000], 8, 4, 1, 128, "bf16"),
+        ([300 + 17 * i for i in range(64)], 8, 4, 8, 128, "mxfp8"),
+        ([4000, 9000], 2, 16, 4, 64, "bf16"),
+        ([700] * 40, 1, 16, 5, 64, "mxfp8"),
+        ([20000], 8, 4, 1, 128, "bf16"),
+        ([50] * 150, 1, 4, 1, 64, "bf16"),
+        ([30000], 1, 8, 1, 128, "mxfp8"),
+    ]
+    calls, size = [], 0
+    for i, (lens, kv, group, L, D, fmt) in enumerate(shapes):
+        cache, g = make_cache(moe, lens, kv, D, 64, fmt, seed=200 + i)
+        fill(cache, g, lens)
+        q = (1.5 * randn(g, len(lens), L, kv * group, D)).to(BF)
+        size = max(size, moe.lib().moe_paged_attention_workspace(cache._ref, kv * group, L))
+        calls.append((cache, q))
+    ws = torch.full((size,), 0xA5, dtype=torch.uint8, device=DEV)  # what is not a counter may hold anything
+    ws[:moe.MOE_ATTENTION_COUNTER_BYTES] = 0
+    for cache, q in calls + calls[::-1]:
+        fresh = torch.zeros(size, dtype=torch.uint8, device=DEV)
+        want, got = attend_c(moe, cache, q, fresh), attend_c(moe, cache, q, ws)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert not torch.isnan(got[0]).any() and not torch.isnan(got[1]).any()
+        assert torch.all(ws[:moe.MOE_ATTENTION_COUNTER_BYTES] == 0)
