@@ -47,6 +47,10 @@ struct moe_experts_s {
   int32_t ws_max_T = 0;
   Workspace ws{};
   int* status = nullptr;  // owned: device status word
+  // Owned: counters that every call finds at zero and leaves at zero.  The workspace is no place for them: layers of
+  // other shapes may share it and lay other buffers there.
+  int32_t* route_done = nullptr;    // [1] CTA count of the small-batch router
+  int32_t* few_counters = nullptr;  // of the one-kernel layer for a few tokens (moe_few.h)
   uint64_t budget_ns = 2000000000ull;
   int num_sms = 0;
   int device = 0;
@@ -281,9 +285,7 @@ size_t workspace_layout(int max_T, int d, int f, int E, int k, Workspace* ws, vo
   w.h_sf = (uint8_t*)take((size_t)dm.max_tiles * (f / 128) * kSfAtomBytes);
   w.y_rows.val = (__half*)take((size_t)dm.rows * d * 2);
   w.y_rows.exp = (uint8_t*)take((size_t)dm.rows * (d / 32));
-  w.route_done = (int32_t*)take(4);
   const size_t few_T = std::min(max_T, kFewMaxT);
-  w.few_counters = (int32_t*)take((size_t)few_counters(d) * 4);
   w.few_h = (uint8_t*)take(few_T * (k + 1) * f);
   w.few_h_s = (uint8_t*)take(few_T * (k + 1) * (f / 32));
   w.few_rows = (float*)take(few_T * (k + 1) * d * 4);
@@ -353,6 +355,10 @@ moe_status_t moe_experts_create(const moe_config_t* cfg, int32_t n, const uint8_
   if (e == cudaSuccess) e = cudaMalloc(&h->sf2, sf2_bytes);
   if (e == cudaSuccess) e = cudaMalloc(&h->status, sizeof(int));
   if (e == cudaSuccess) e = cudaMemsetAsync(h->status, 0, sizeof(int), s);
+  if (e == cudaSuccess) e = cudaMalloc(&h->route_done, sizeof(int32_t));
+  if (e == cudaSuccess) e = cudaMemsetAsync(h->route_done, 0, sizeof(int32_t), s);
+  if (e == cudaSuccess) e = cudaMalloc(&h->few_counters, (size_t)few_counters(d) * 4);
+  if (e == cudaSuccess) e = cudaMemsetAsync(h->few_counters, 0, (size_t)few_counters(d) * 4, s);
   if (e == cudaSuccess) e = launch_pack_weights(w13_fp4, n, 2 * f, d, 0, h->w13, s);
   if (e == cudaSuccess) e = launch_pack_weights(w2_fp4, n, d, f, 1, h->w2, s);
   if (e == cudaSuccess) e = launch_pack_weight_sf(w13_e8m0, n, 2 * f, d, 0, h->sf13, s);
@@ -386,6 +392,8 @@ void moe_experts_destroy(moe_experts_t h) {
   if (h->sf13) cudaFree(h->sf13);
   if (h->sf2) cudaFree(h->sf2);
   if (h->status) cudaFree(h->status);
+  if (h->route_done) cudaFree(h->route_done);
+  if (h->few_counters) cudaFree(h->few_counters);
   if (h->router_split) cudaFree(h->router_split);
   if (h->router_w32) cudaFree(h->router_w32);
   if (h->router_bias) cudaFree(h->router_bias);
@@ -460,10 +468,9 @@ moe_status_t moe_set_workspace(moe_experts_t h, void* ws, size_t bytes, int32_t 
                                        nullptr);
   if (bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed for max_T %d", bytes, need, max_T);
   workspace_layout(max_T, h->cfg.d_model, h->cfg.d_ff, h->cfg.n_experts, h->cfg.top_k, &h->ws, ws);
-  // the small-batch router's CTA count starts at zero (and every call leaves it there)
-  MOE_CUDA(cudaMemset(h->ws.route_done, 0, sizeof(int32_t)), "router counter");
-  // as do those of the one-kernel layer
-  MOE_CUDA(cudaMemset(h->ws.few_counters, 0, (size_t)few_counters(h->cfg.d_model) * 4), "few-token counters");
+  // every call leaves the counters at zero; a new workspace starts them over all the same
+  MOE_CUDA(cudaMemset(h->route_done, 0, sizeof(int32_t)), "router counter");
+  MOE_CUDA(cudaMemset(h->few_counters, 0, (size_t)few_counters(h->cfg.d_model) * 4), "few-token counters");
   h->ws_base = ws;
   h->ws_bytes = bytes;
   h->ws_max_T = max_T;
@@ -508,7 +515,7 @@ static moe_status_t route_into(moe_experts_s* h, const moe_input_t* x, const flo
     if (!x->token_ids) return fail(MOE_ERR_INVALID_ARG, "hash layer: token_ids is NULL");
     if (T == 0) return MOE_OK;
     MOE_CUDA(launch_hash_route(x->token_ids, h->hash_table, h->hash_V, T, E, k, h->cfg.route_scale, ids, wts, h->status,
-                               s, h->ws.route_done, dout),
+                               s, h->route_done, dout),
              "hash route");
     return MOE_OK;
   }
@@ -523,7 +530,7 @@ static moe_status_t route_into(moe_experts_s* h, const moe_input_t* x, const flo
   if (T <= kRouterSmallMaxT) {  // small batches: fp32 logits over the whole GPU and top-k, one kernel
     MOE_CUDA(launch_router_small(static_cast<const __nv_bfloat16*>(x->x_bf16), resident ? h->router_w32 : router_w,
                                  resident ? h->router_bias : router_bias, T, d, E, k, h->cfg.route_scale, h->ws.logits,
-                                 h->ws.route_done, ids, wts, resident ? 1 : 0, disp, s),
+                                 h->route_done, ids, wts, resident ? 1 : 0, disp, s),
              "router");
     return MOE_OK;
   }
@@ -542,7 +549,7 @@ static moe_status_t route_into(moe_experts_s* h, const moe_input_t* x, const flo
   }
   if (E <= 256) {  // logits, split-K reduction and top-k in one cluster kernel
     MOE_CUDA(launch_router_fused(tm_x, tm_w, router_bias, T, E, d, k, h->cfg.route_scale, router_fused_split(T, d), ids,
-                                 wts, h->status, h->budget_ns, s, h->ws.route_done, dout),
+                                 wts, h->status, h->budget_ns, s, h->route_done, dout),
              "router");
     return MOE_OK;
   }
@@ -840,7 +847,7 @@ moe_status_t moe_forward_few(const moe_input_t* x, const float* router_w, const 
   a.h = h->ws.few_h;
   a.h_s = h->ws.few_h_s;
   a.rows = h->ws.few_rows;
-  a.counters = h->ws.few_counters;
+  a.counters = h->few_counters;
   a.ws_ids = h->ws.topk_ids;
   a.ws_w = h->ws.topk_w;
   a.out_ids = topk_ids;

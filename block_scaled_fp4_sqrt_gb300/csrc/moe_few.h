@@ -8,7 +8,7 @@ namespace moe {
 constexpr int kFewMaxT = 8;
 constexpr int kFewMaxSlots = kFewMaxT * 16 + 1;  // touched experts: at most T * top_k, and the shared one
 
-// Counters in the workspace, all zero between calls.
+// Counters of a handle, all zero between calls.
 constexpr int kFewScoresDone = 0;                          // blocks whose router scores are written
 constexpr int kFewBlocksDone = 1;                          // blocks that have ended
 constexpr int kFewSlotDone = 2;                            // [slot] h blocks written

@@ -78,8 +78,6 @@ struct Workspace {
   uint8_t* h_q;         // [rows, f]
   uint8_t* h_sf;        // [max_tiles, f/128, 512]
   ExpertRows y_rows;     // [rows, d] weighted expert outputs (scaled fp16) and [rows, d / 32] scales
-  int32_t* route_done;   // [1] CTA count of the small-batch router (zero between calls)
-  int32_t* few_counters; // counters of the one-kernel layer for a few tokens (zero between calls)
   uint8_t* few_h;        // [few_T, k + 1, f] its h codes, few_T = min(max_T, 8)
   uint8_t* few_h_s;      // [few_T, k + 1, f / 32]
   float* few_rows;       // [few_T, k + 1, d] its weighted expert rows

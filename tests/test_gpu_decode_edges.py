@@ -49,3 +49,36 @@ def test_one_workspace_serves_calls_of_any_shape(moe):  # noqa: F811
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         assert not torch.isnan(got[0]).any() and not torch.isnan(got[1]).any()
         assert torch.all(ws[:moe.MOE_ATTENTION_COUNTER_BYTES] == 0)
+
+
+def layer_of(moe, d, f, E, k, seed, max_T=8, **kw):  # noqa: F811
+    """A layer of random weights (any codes; scales near 1 / sqrt(columns))."""
+    g = gen(seed)
+
+    def codes(n, rows, cols):
+        e = 127 - 2 - cols.bit_length() // 2
+        return (torch.randint(0, 256, (n, rows, cols // 2), dtype=torch.uint8, device=DEV, generator=g),
+                torch.randint(e - 1, e + 1, (n, rows, cols // 32), dtype=torch.uint8, device=DEV, generator=g))
+
+    ex, sh = (moe.DeviceExperts(*codes(n, 2 * f, d), *codes(n, d, f)) for n in (E, 1))
+    return moe.MoELayer(d, f, E, k, ex, sh, randn(g, E, d) * d ** -0.5, 0.05 * randn(g, E), max_T=max_T, device=DEV, **kw)
+
+
+def test_layers_of_other_shapes_may_share_a_workspace(moe):  # noqa: F811
+    """What one layer leaves in the workspace is no counter of another's: one-kernel calls and ordinary ones in turn."""
+    d = 512
+    layers = [layer_of(moe, d, f, E, k, 300 + f) for f, E, k in ((256, 16, 4), (1024, 8, 2), (128, 64, 6))]
+    xs = [randn(gen(310 + T), T, d).to(BF) for T in (1, 3, 8)]
+    want = [[(ly.forward_few(x), ly.forward(x)) for x in xs] for ly in layers]
+    shared = torch.full((max(moe.moe_workspace_size(ly.cfg, 8) for ly in layers),), 0xA5, dtype=torch.uint8, device=DEV)
+    for ly in layers:
+        moe.moe_set_workspace(ly.h, shared, 8)
+    for _ in range(2):
+        for i, x in enumerate(xs):
+            for ly, w in zip(layers, want):
+                assert torch.equal(ly.forward_few(x), w[i][0])
+            for ly, w in zip(layers, want):
+                assert torch.equal(ly.forward(x), w[i][1])
+                assert torch.equal(ly.forward_few(x), w[i][0])
+    for ly in layers:
+        ly.check()
