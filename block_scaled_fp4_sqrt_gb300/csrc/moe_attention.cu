@@ -843,8 +843,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
               *reinterpret_cast<uint32_t*>(dst + n * 8 + 2 * lc) =
                   pack_bf16(o[a][n][2 * h] * inv, o[a][n][2 * h + 1] * inv);
           }
-          if (p.lse && warp == 0 && lc == 0)
-            p.lse[token * p.Hq + head] = m[a][h] == -INFINITY ? -INFINITY : (m[a][h] + log2f(z)) * kLn2;
+          // (m is -inf where no score was above it: z = 0 then gives -inf, a NaN among the scores NaN)
+          if (p.lse && warp == 0 && lc == 0) p.lse[token * p.Hq + head] = (m[a][h] + log2f(z)) * kLn2;
         }
     };
     if (first_tile >= t0 && unit_end <= t1) {  // the whole unit was this block's

@@ -82,3 +82,35 @@ def test_layers_of_other_shapes_may_share_a_workspace(moe):  # noqa: F811
                 assert torch.equal(ly.forward_few(x), w[i][0])
     for ly in layers:
         ly.check()
+
+
+# ---------------------------------------------------------------------------------------------- rows that hold NaN
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("lens", [[90, 6], [30000, 500]])  # units of one block; units that many blocks share
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_lse_of_a_row_that_holds_nan_is_nan(moe, fmt, lens, bad):  # noqa: F811
+    """-inf is for rows that see nothing: who joins parts by lse would drop such a row's NaN."""
+    kv, group, L, D = 2, 4, 2, 64
+    cache, g = make_cache(moe, lens, kv, D, 16, fmt, seed=400)
+    fill(cache, g, lens)
+    q = randn(g, 2, L, kv * group, D).to(BF)
+
+    def attend():
+        lse = torch.full(q.shape[:3], 7.0, device=DEV)
+        return cache.attend(q, lse=lse), lse
+
+    want, want_lse = attend()
+    q[0, 1, 2, 5] = bad
+    got, lse = attend()
+    assert torch.isnan(got[0, 1, 2]).all() and torch.isnan(lse[0, 1, 2])
+    hit = torch.zeros_like(lse, dtype=torch.bool)
+    hit[0, 1, 2] = True
+    assert torch.equal(got[~hit], want[~hit]) and torch.equal(lse[~hit], want_lse[~hit])
+    q[0, 1, 2, 5] = 0.5
+    n = lens[1]  # every key of request 1 and head 0
+    pos = torch.arange(n)
+    at = (cache.tab[1, pos // 16].long().to(DEV), (pos % 16).to(DEV))
+    cache.k[(*at, torch.zeros(n, dtype=torch.long, device=DEV))] = math.nan if fmt == "bf16" else 0x7F
+    got, lse = attend()
+    assert torch.isnan(got[1, :, :group]).all() and torch.isnan(lse[1, :, :group]).all()
+    assert torch.isfinite(lse[1, :, group:]).all() and torch.isfinite(lse[0]).all()
