@@ -696,8 +696,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
           }
     }
   };
-  // Token by token, leaving out the tokens with p = 0.
+  // Token by token, leaving out for each row the tokens that it does not see (not those with p = 0: a NaN or an infinity
+  // that a row sees counts whatever its weight, as in the products).
   auto values_one_by_one = [&](uint32_t vb, uint32_t sb) {
+    int lim[MT][2];
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) lim[a][h] = s_lim[a * 16 + li + 8 * h] - cur.t * kTile;
     for (int tk = 0; tk < kTile; ++tk) {
       float v[kNT][2];
 #pragma unroll
@@ -724,10 +730,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
       for (int a = 0; a < MT; ++a)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+          if (tk >= lim[a][h]) continue;
           uint16_t bits;
           asm volatile("ld.shared.u16 %0, [%1];" : "=h"(bits) : "r"(p_base + (a * 16 + li + 8 * h) * kPPitch + tk * 2));
           const float pr = __uint_as_float((uint32_t)bits << 16);
-          if (pr == 0.f) continue;
 #pragma unroll
           for (int n = 0; n < kNT; ++n)
 #pragma unroll

@@ -99,9 +99,9 @@ MOE_API moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const void* k_ne
  * Attention of the L newest tokens of every request over the request's cache.  Row (b, l) sees positions
  * t < seq_lens[b] - L + 1 + l (causal among the new tokens); with h' = h / (n_q_heads / n_kv_heads):
  *   s_t = scale * q[b, l, h] . k[t, h'];  out = sum_t softmax(s)_t v[t, h'];  lse = log sum_t exp(s_t).
- * A row that sees nothing gets out = 0 and lse = -inf; a NaN in q or among the keys that a row sees makes both NaN.
- * Positions that a row does not see never change its
- * result, whatever they hold (NaN and infinities included).
+ * A row that sees nothing gets out = 0 and lse = -inf; a NaN in q or among the keys that a row sees makes both NaN,
+ * one among the values their column of out.  Positions that a row does not see never change its result, whatever they
+ * hold (NaN and infinities included).
  *   q, out   bf16 rows (b * L + l) of n_q_heads * head_dim elements at q_stride / out_stride (multiples of 8;
  *            0 = contiguous), 16-byte aligned.
  *   lse      fp32 [n_seqs, L, n_q_heads] or NULL.

@@ -114,3 +114,24 @@ def test_lse_of_a_row_that_holds_nan_is_nan(moe, fmt, lens, bad):  # noqa: F811
     got, lse = attend()
     assert torch.isnan(got[1, :, :group]).all() and torch.isnan(lse[1, :, :group]).all()
     assert torch.isfinite(lse[1, :, group:]).all() and torch.isfinite(lse[0]).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("L", [1, 2, 3])
+def test_a_nan_value_of_negligible_weight_reaches_the_rows_that_see_it(moe, fmt, L):  # noqa: F811
+    """A row's own newest token, with a weight that fp32 cannot hold: its NaN counts as it does at every other place."""
+    lens, D = [100, 41], 64
+    cache, g = make_cache(moe, lens, 1, D, 16, fmt, seed=430)
+    fill(cache, g, lens)
+    q = (4 + randn(g, 2, L, 4, D).abs()).to(BF)
+    for b, n in enumerate(lens):
+        page, row = int(cache.tab[b, (n - 1) // 16]), (n - 1) % 16
+        if fmt == "bf16":
+            cache.k[page, row], cache.v[page, row, 0, 9] = -300, math.nan
+        else:
+            cache.k[page, row], cache.k_scales[page, row] = 0xFE, 127  # -448
+            cache.v[page, row, 0, 9] = 0x7F
+    out = cache.attend(q)
+    assert torch.isnan(out[:, -1, :, 9]).all()
+    out[:, -1, :, 9] = 0
+    assert torch.isfinite(out).all()
