@@ -135,3 +135,19 @@ def test_a_nan_value_of_negligible_weight_reaches_the_rows_that_see_it(moe, fmt,
     assert torch.isnan(out[:, -1, :, 9]).all()
     out[:, -1, :, 9] = 0
     assert torch.isfinite(out).all()
+
+
+# ---------------------------------------------------------------------------------------------- the ends of E8M0
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("L", [1, 12])
+def test_attend_keys_of_the_smallest_scale(moe, D, L):  # noqa: F811
+    """Byte 0 is 2^-127, not 0: keys near 2^-125 against queries near 2^120."""
+    lens = [100, 700]
+    cache, g = make_cache(moe, lens, 1, D, 16, "mxfp8", seed=420)
+    k = (randn(g, 2, 700, 1, D) * 2.0 ** -125).to(BF)
+    v = randn(g, 2, 700, 1, D).to(BF)
+    cache.append(k, v)
+    assert int(cache.k_scales[cache.tab[0, 0], 0].max()) == 0
+    q = (randn(g, 2, L, 4, D) * 2.0 ** 120).to(BF)
+    out, _ = check_attend(cache, q, lens, scale=8.0)
+    assert not torch.allclose(out[0, 0, 0].float(), out[0, 0, 1].float(), rtol=0.1, atol=0.1)  # the scores matter
