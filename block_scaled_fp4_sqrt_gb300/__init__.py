@@ -163,11 +163,14 @@ def _input(x: torch.Tensor, token_ids: torch.Tensor | None = None) -> moe_input_
                        None if token_ids is None else ctypes.c_void_p(token_ids.data_ptr()))
 
 
-def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape) -> None:
-    """A kernel reads or writes t as dense rows of this type and shape."""
-    if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}, strides {t.stride()}")
+def _dense(t: torch.Tensor, dtype: torch.dtype, shape) -> bool:
+    """Whether t is dense rows of this type and shape on a GPU, as a kernel reads or writes them."""
+    return t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous()
+
+
+def _refuse(t: torch.Tensor, name: str, what: str):
+    raise ValueError(f"{name} must be a contiguous CUDA tensor, {what}, got {t.dtype} {tuple(t.shape)} on {t.device}, "
+                     f"strides {t.stride()}")
 
 
 def make_config(d_model: int, d_ff: int, n_experts: int, top_k: int, route_scale: float = 1.5,
@@ -225,17 +228,25 @@ def moe_forward_few(x, router_w, router_bias, experts, shared, out, topk_ids=Non
                     stream=None) -> None:
     """moe_forward for at most MOE_FEW_MAX_T rows in one kernel: x and out bf16 [T, d], token_ids int32 [T or more];
     topk_ids int32 and topk_w fp32 [T, top_k] receive the routing."""
-    T = x.shape[0]
-    _dense(x, "x", torch.bfloat16, (T, *x.shape[1:2]))
-    _dense(out, "out", torch.bfloat16, x.shape)
-    if token_ids is not None:
-        _dense(token_ids, "token_ids", torch.int32, (max(T, token_ids.shape[0]),))
-    if topk_ids is not None:
-        _dense(topk_ids, "topk_ids", torch.int32, (T, *topk_ids.shape[1:2]))
-    if topk_w is not None:
-        _dense(topk_w, "topk_w", torch.float32, (T, *topk_w.shape[1:2]))
-    _ok("moe_forward_few", lib().moe_forward_few(ctypes.byref(_input(x, token_ids)), _p(router_w), _p(router_bias),
-                                                 experts, shared, _p(out), _p(topk_ids), _p(topk_w), _stream(stream)))
+    shape = x.shape
+    if len(shape) != 2 or not _dense(x, torch.bfloat16, shape):
+        _refuse(x, "x", "bf16 [T, d]")
+    T = shape[0]
+    if not _dense(out, torch.bfloat16, shape):
+        _refuse(out, "out", f"bf16 {tuple(shape)}")
+    if token_ids is not None and not (_dense(token_ids, torch.int32, (token_ids.numel(),)) and token_ids.numel() >= T):
+        _refuse(token_ids, "token_ids", f"int32 [{T}] or longer")
+    if topk_ids is not None and not _dense(topk_ids, torch.int32, (T, topk_ids.shape[-1])):
+        _refuse(topk_ids, "topk_ids", f"int32 [{T}, top_k]")
+    if topk_w is not None and not _dense(topk_w, torch.float32, (T, topk_w.shape[-1])):
+        _refuse(topk_w, "topk_w", f"fp32 [{T}, top_k]")
+    a = moe_input_t(x.data_ptr() or None, T, None if token_ids is None else token_ids.data_ptr())
+    status = lib().moe_forward_few(ctypes.byref(a), None if router_w is None else router_w.data_ptr(),
+                                   None if router_bias is None else router_bias.data_ptr(), experts, shared,
+                                   out.data_ptr(), None if topk_ids is None else topk_ids.data_ptr(),
+                                   None if topk_w is None else topk_w.data_ptr(), _raw_stream(stream))
+    if status:
+        _ok("moe_forward_few", status)
 
 
 def moe_get_routing(h):
@@ -452,10 +463,12 @@ class MoELayer:
                     stream=None) -> torch.Tensor:
         """``forward`` for at most MOE_FEW_MAX_T rows, in one kernel (MXFP8 activations); topk_ids int32 and topk_w
         fp32 [T, top_k], if given, receive the routing."""
-        T = x.shape[0]
-        for t, name, cols in ((x, "x", self.d), (topk_ids, "topk_ids", self.k), (topk_w, "topk_w", self.k)):
-            if t is not None and tuple(t.shape) != (T, cols):
-                raise ValueError(f"{name} must have the shape {(T, cols)}, got {tuple(t.shape)}")
+        if x.shape[-1] != self.d:
+            _refuse(x, "x", f"bf16 [T, {self.d}]")
+        if topk_ids is not None and topk_ids.shape[-1] != self.k:
+            _refuse(topk_ids, "topk_ids", f"int32 [T, {self.k}]")
+        if topk_w is not None and topk_w.shape[-1] != self.k:
+            _refuse(topk_w, "topk_w", f"fp32 [T, {self.k}]")
         if token_ids is None and self.hash_table is not None:
             token_ids = self.token_ids
         if out is None:
