@@ -169,12 +169,6 @@ __device__ __forceinline__ void e4m3_bf16(uint32_t r, uint32_t& even, uint32_t& 
   top = __vimax3_u16x2(top, e, o);
 }
 
-// Twice the value of E8M0 byte j of w, less 2^-23 of it at most: with all mantissa bits set, byte 0 (2^-127, a subnormal
-// number) needs no instruction of its own.  (The exact value by a maximum with 2^-127: 64 x 8 rows 97.9 -> 99.2 us.)
-__device__ __forceinline__ float e8m0_twice(uint32_t w, int j) {
-  return __uint_as_float(((j == 3 ? w >> 1 : w << (23 - 8 * j)) & 0x7F800000u) | 0x007FFFFFu);
-}
-
 // Position in the sequence of all tiles: request b (length len, nt tiles a unit), kv head, row tile rt, tile t.
 struct Cursor {
   int b, head, rt, t, nt, len;
@@ -433,9 +427,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
         const int be = (int)(top >> 7);
         const int up = be ? min(141 - be, 126) : 126;
         const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
-        // (half of it: e8m0_twice)
-        factor = be == 255 ? __uint_as_float(0x7FC00000u)
-                           : 0.5f * p.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
+        factor = be == 255 ? __uint_as_float(0x7FC00000u) : p.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
         float v[8];
         bf16x8_to_f32(raw[it], v);
         uint32_t h[4];
@@ -537,8 +529,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
         float k0[2], k1[2];
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          k0[n] = e8m0_twice(kw[n][0], k / 2);
-          k1[n] = e8m0_twice(kw[n][1], k / 2);
+          k0[n] = e8m0_float(kw[n][0], k / 2);
+          k1[n] = e8m0_float(kw[n][1], k / 2);
         }
 #pragma unroll
         for (int a = 0; a < MT; ++a) {

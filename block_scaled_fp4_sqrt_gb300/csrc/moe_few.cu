@@ -115,11 +115,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// E8M0 byte j of w as a float (byte 0, 2^-127, reads as 0).
-__device__ __forceinline__ float e8m0_float(uint32_t w, int j) {
-  return __uint_as_float(j == 3 ? (w >> 1) & 0x7F800000u : (w << (23 - 8 * j)) & 0x7F800000u);
-}
-
 __device__ __forceinline__ uint32_t lds32(uint32_t at) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");

@@ -6,6 +6,9 @@ import math
 import pytest
 import torch
 
+import oracle
+import synth
+from gpu_support import assert_close, bf16_to_f64, x_to_device
 from test_gpu_decode import BF, DEV, HALF_ULP, attend_ref, check_attend, fill, gen, make_cache, moe, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -151,3 +154,26 @@ def test_attend_keys_of_the_smallest_scale(moe, D, L):  # noqa: F811
     q = (randn(g, 2, L, 4, D) * 2.0 ** 120).to(BF)
     out, _ = check_attend(cache, q, lens, scale=8.0)
     assert not torch.allclose(out[0, 0, 0].float(), out[0, 0, 1].float(), rtol=0.1, atol=0.1)  # the scores matter
+
+
+@pytest.mark.parametrize("which", ["s13", "s2"])
+def test_few_weights_of_the_smallest_scale(moe, which):  # noqa: F811
+    """Byte 0 of the experts' scales is 2^-127, as moe_forward reads it: large x against W13, the layer's limit against
+    W2."""
+    wl = synth.WORKLOADS["tiny"].with_T(4)
+    inp, ids, wts, _ = oracle.margin_filtered_layer(wl, 7)
+    for e in (inp.experts, inp.shared):
+        getattr(e, which)[...] = 0
+    # h of order 1 to 100: x 2^117 against the scales 2^-127 of W13, x 2^4 against its own
+    bits = (torch.from_numpy(inp.x.view("int16")).view(BF).float() * 2.0 ** (117 if which == "s13" else 4)).to(BF)
+    inp.x = bits.view(torch.int16).numpy().view("uint16")
+    ids, wts, margin = oracle.route(inp.x, inp.router_w, inp.router_bias, wl.k, wl.route_scale)
+    assert (margin >= oracle.MARGIN_MIN).all()
+    layer = moe.MoELayer.from_host(inp, device=DEV, max_T=4)
+    x = x_to_device(inp.x)
+    y_ref = oracle.layer(inp.x, ids, wts, inp.experts, inp.shared, wl.swiglu_limit)
+    assert abs(y_ref).max() > 2.0 ** -118
+    out = layer.forward_few(x)
+    layer.check()
+    assert_close(bf16_to_f64(layer.forward(x)), y_ref, f"{which} = 0, moe_forward")
+    assert_close(bf16_to_f64(out), y_ref, f"{which} = 0")
