@@ -158,6 +158,23 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(_raw_stream(stream))
 
 
+def _on_stream(stream, device):
+    """A context in which torch allocates and launches on `stream` (None: the current one, or an integer handle)."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        raw = _raw_stream(stream)
+        stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype: torch.dtype, device, stream=None) -> torch.Tensor:
+    """Memory for a result that is written on `stream`, from that stream's share of the allocator: a block that pending
+    work of another stream still uses is not handed out."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on_stream(stream, device):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _input(x: torch.Tensor, token_ids: torch.Tensor | None = None) -> moe_input_t:
     return moe_input_t(ctypes.c_void_p(x.data_ptr()) if x.numel() else None, int(x.shape[0]),
                        None if token_ids is None else ctypes.c_void_p(token_ids.data_ptr()))
@@ -288,8 +305,8 @@ def moe_testing_read_h(h, f: int, act: str, stream=None):
     n = ctypes.c_int32(0)
     _ok("moe_testing_read_h", lib().moe_testing_read_h(h, None, None, ctypes.byref(n), _stream(stream)))
     dev = torch.device("cuda", torch.cuda.current_device())
-    hq = torch.empty((n.value, f // 2 if act == "mxfp4" else f), dtype=torch.uint8, device=dev)
-    hs = torch.empty((n.value, f // 32), dtype=torch.uint8, device=dev)
+    hq = _empty((n.value, f // 2 if act == "mxfp4" else f), torch.uint8, dev, stream)
+    hs = _empty((n.value, f // 32), torch.uint8, dev, stream)
     if n.value:
         _ok("moe_testing_read_h", lib().moe_testing_read_h(h, _p(hq), _p(hs), ctypes.byref(n), _stream(stream)))
     return hq, hs
@@ -305,7 +322,7 @@ def moe_testing_read_y32(h, d: int, stream=None) -> torch.Tensor:
     n = ctypes.c_int32(0)
     _ok("moe_testing_read_y32", lib().moe_testing_read_y32(h, None, ctypes.byref(n), _stream(stream)))
     dev = torch.device("cuda", torch.cuda.current_device())
-    y = torch.empty((n.value, d), dtype=torch.float32, device=dev)
+    y = _empty((n.value, d), torch.float32, dev, stream)
     if n.value:
         _ok("moe_testing_read_y32", lib().moe_testing_read_y32(h, _p(y), ctypes.byref(n), _stream(stream)))
     return y
@@ -361,8 +378,8 @@ def moe_stack_destroy(stack) -> None:
 def moe_mx_blocks_unpack(blocks: torch.Tensor, nibble_order: int, stream=None):
     """17-byte MXFP4 blocks (uint8, 17 * n bytes) -> (codes uint8 [n, 16], scales uint8 [n])."""
     n = blocks.numel() // 17
-    codes = torch.empty((n, 16), dtype=torch.uint8, device=blocks.device)
-    scales = torch.empty((n,), dtype=torch.uint8, device=blocks.device)
+    codes = _empty((n, 16), torch.uint8, blocks.device, stream)
+    scales = _empty((n,), torch.uint8, blocks.device, stream)
     _ok("moe_mx_blocks_unpack", lib().moe_mx_blocks_unpack(_p(blocks), n, int(nibble_order), _p(codes), _p(scales),
                                                            _stream(stream)))
     return codes, scales
@@ -453,7 +470,7 @@ class MoELayer:
         if token_ids is None and self.hash_table is not None:
             token_ids = self.token_ids
         if out is None:
-            out = torch.empty((x.shape[0], self.d), dtype=torch.bfloat16, device=self.device)
+            out = _empty((x.shape[0], self.d), torch.bfloat16, self.device, stream)
         rw, rb = (None, None) if self.resident_router else (self.router_w, self.router_bias)
         moe_forward(x, rw, rb, self.h, self.h_shared, out, token_ids, stream)
         return out
@@ -472,7 +489,7 @@ class MoELayer:
         if token_ids is None and self.hash_table is not None:
             token_ids = self.token_ids
         if out is None:
-            out = torch.empty((x.shape[0], self.d), dtype=torch.bfloat16, device=self.device)
+            out = _empty((x.shape[0], self.d), torch.bfloat16, self.device, stream)
         rw, rb = (None, None) if self.resident_router else (self.router_w, self.router_bias)
         moe_forward_few(x, rw, rb, self.h, self.h_shared, out, topk_ids, topk_w, token_ids, stream)
         return out
@@ -577,7 +594,7 @@ class MoEStack:
     def forward(self, x: torch.Tensor, token_ids: torch.Tensor | None = None, out: torch.Tensor | None = None,
                 stream=None) -> torch.Tensor:
         if out is None:
-            out = torch.empty((x.shape[0], self.d), dtype=torch.bfloat16, device=self.device)
+            out = _empty((x.shape[0], self.d), torch.bfloat16, self.device, stream)
         moe_stack_forward(self.stack, x, out, self.scratch[: x.shape[0]], token_ids, stream)
         return out
 

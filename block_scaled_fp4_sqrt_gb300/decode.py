@@ -10,7 +10,7 @@ import ctypes
 
 import torch
 
-from . import MOE_OK, MoEError, _ok, _raw_stream, lib, moe_attention_t, moe_kv_cache_t, moe_norm_t
+from . import MOE_OK, MoEError, _empty, _ok, _on_stream, _raw_stream, lib, moe_attention_t, moe_kv_cache_t, moe_norm_t
 
 MOE_KV_BF16, MOE_KV_MXFP8 = 0, 1
 KV_STATUS = {1: "a sequence length outside the block table", 2: "a page index outside the cache"}
@@ -161,9 +161,7 @@ class PagedKVCache:
             n = int(lib().moe_paged_attention_workspace(self._ref, n_q_heads, L))
             if n == 0:
                 raise MoEError("moe_paged_attention_workspace", 1, lib().moe_last_error().decode())
-            if stream is not None and not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-            with torch.cuda.stream(stream):  # None: the current stream
+            with _on_stream(stream, self.device):
                 ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
                 capturing = torch.cuda.is_current_stream_capturing()
             if not capturing:  # a captured fill has not run yet: such a workspace serves its graph alone
@@ -174,10 +172,11 @@ class PagedKVCache:
                scale: float | None = None, stream=None) -> torch.Tensor:
         """Attention of the L newest tokens of every request: q, out bf16 [n_seqs, L, n_q_heads, head_dim]; lse
         fp32 [n_seqs, L, n_q_heads] or None; scale defaults to head_dim ** -0.5.  Row l sees the positions below
-        seq_lens[b] - L + 1 + l; a row that sees nothing gives 0 (lse -inf)."""
+        seq_lens[b] - L + 1 + l; a row that sees nothing gives 0 (lse -inf).  An out that is not given is allocated on
+        `stream`."""
         L, heads, qs = self._step_rows(q, "q")
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = _empty(q.shape, q.dtype, self.device, stream)
         Lo, _, os_ = self._step_rows(out, "out", heads)
         if Lo != L:
             raise ValueError("q and out hold different numbers of tokens")

@@ -144,3 +144,38 @@ def test_forward_few_passes_what_fits_and_refuses_the_rest(m):
         with pytest.raises(ValueError):
             lay.forward_few(**{"x": x, **good, **kw})
     assert len(m.library.calls) == calls
+
+
+# ---------------------------------------------------------------------------------------------- streams
+def test_results_are_allocated_on_the_stream_that_writes_them(m, monkeypatch):
+    """Memory of the current stream's pool may still be in use there when a kernel on another stream writes it."""
+    active, made = [], []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            active.append(self.stream)
+
+        def __exit__(self, *_):
+            active.pop()
+
+    def empty(*args, device=None, _real=torch.empty, **kw):
+        made.append(active[-1] if active else None)
+        return OnGpu(_real(*args, **kw))
+
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: handle)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
+    monkeypatch.setattr(torch, "empty", empty)
+    c, lay, x, q = cache(m), layer(m), zeros(3, 256), zeros(3, 1, 4, 64)
+    monkeypatch.setattr(m.PagedKVCache, "_workspace", lambda *a: zeros(8, dtype=torch.uint8))
+    for stream, want in ((None, None), (77, 77), (0, "default")):
+        for call in (lambda: c.attend(q, stream=stream), lambda: lay.forward_few(x, stream=stream),
+                     lambda: lay.forward(x, stream=stream)):
+            made.clear()
+            call()
+            assert made == [want]
+            raw = m.library.calls[-1][1][-1]
+            assert (getattr(raw, "value", raw) or 0) == (stream or 0)

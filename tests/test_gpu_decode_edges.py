@@ -177,3 +177,24 @@ def test_few_weights_of_the_smallest_scale(moe, which):  # noqa: F811
     layer.check()
     assert_close(bf16_to_f64(layer.forward(x)), y_ref, f"{which} = 0, moe_forward")
     assert_close(bf16_to_f64(out), y_ref, f"{which} = 0")
+
+
+# ---------------------------------------------------------------------------------------------- streams
+def test_results_on_another_stream_do_not_take_the_current_streams_memory(moe):  # noqa: F811
+    """A block just freed on the current stream may have work pending there: a call on another stream leaves it alone."""
+    cache, g = make_cache(moe, [70, 500], 2, 128, 16, "bf16", seed=460)
+    fill(cache, g, [70, 500])
+    q = randn(g, 2, 2, 8, 128).to(BF)
+    ly = layer_of(moe, 512, 256, 8, 2, 461)
+    x = randn(g, 3, 512).to(BF)
+    side = torch.cuda.Stream()
+    for call in (lambda **kw: cache.attend(q, **kw), lambda **kw: ly.forward_few(x, **kw), lambda **kw: ly.forward(x, **kw)):
+        want = call()
+        freed = [torch.empty_like(want) for _ in range(8)]
+        at = {t.data_ptr() for t in freed}
+        del freed
+        side.wait_stream(torch.cuda.current_stream())
+        for stream in (side, side.cuda_stream):
+            got = call(stream=stream)
+            side.synchronize()
+            assert got.data_ptr() not in at and torch.equal(got, want)
