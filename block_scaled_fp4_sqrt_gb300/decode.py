@@ -10,9 +10,13 @@ import ctypes
 
 import torch
 
-from . import MOE_OK, MoEError, _empty, _ok, _on_stream, _raw_stream, lib, moe_attention_t, moe_kv_cache_t, moe_norm_t
+from . import MOE_ATTENTION_COUNTER_BYTES, MOE_OK, MoEError, _empty, _ok, _on_stream, _raw_stream, lib, moe_attention_t, moe_kv_cache_t, moe_norm_t
 
 MOE_KV_BF16, MOE_KV_MXFP8 = 0, 1
+# The attention workspaces of calls outside captures, one for each GPU and stream, as large as the largest call so far: the
+# calls of a stream run one after another, whatever their caches and shapes.
+_WORKSPACES: dict[tuple[int, int], torch.Tensor] = {}
+
 KV_STATUS = {1: "a sequence length outside the block table", 2: "a page index outside the cache"}
 
 
@@ -110,7 +114,7 @@ class PagedKVCache:
                                  self.status.data_ptr(), *st, MOE_KV_MXFP8 if mx else MOE_KV_BF16, n_pages, page,
                                  heads, d, self.n_seqs, block_table.shape[1])
         self._ref = ctypes.byref(self._c)
-        self._workspaces = {}
+        self._workspace_bytes = {}
         self._index = k.get_device()
 
     @classmethod
@@ -153,27 +157,46 @@ class PagedKVCache:
         if status:
             _ok("moe_kv_append", status)
 
-    def _workspace(self, n_q_heads: int, L: int, stream) -> torch.Tensor:
-        """The attention's workspace for calls on this stream, made (and zeroed there) at first use."""
-        key = (n_q_heads, L, _raw_stream(stream))
-        ws = self._workspaces.get(key)
-        if ws is None:
+    def _bytes(self, n_q_heads: int, L: int) -> int:
+        n = self._workspace_bytes.get((n_q_heads, L))
+        if n is None:
             n = int(lib().moe_paged_attention_workspace(self._ref, n_q_heads, L))
             if n == 0:
                 raise MoEError("moe_paged_attention_workspace", 1, lib().moe_last_error().decode())
+            self._workspace_bytes[n_q_heads, L] = n
+        return n
+
+    def attention_workspace(self, n_q_heads: int, L: int, stream=None) -> torch.Tensor:
+        """A workspace for ``attend`` of up to L new tokens, ready for calls on `stream`: for a program that captures its
+        calls into graphs, or runs them on several streams.  It serves any calls that run one after another."""
+        ws = _empty((self._bytes(n_q_heads, L),), torch.uint8, self.device, stream)
+        with _on_stream(stream, self.device):
+            ws[:MOE_ATTENTION_COUNTER_BYTES].zero_()
+        return ws
+
+    def _workspace(self, n_q_heads: int, L: int, stream, raw: int) -> torch.Tensor:
+        if stream is None:
+            capturing = torch._C._cuda_isCurrentStreamCapturing()
+        else:
             with _on_stream(stream, self.device):
-                ws = torch.zeros(n, dtype=torch.uint8, device=self.device)
-                capturing = torch.cuda.is_current_stream_capturing()
-            if not capturing:  # a captured fill has not run yet: such a workspace serves its graph alone
-                self._workspaces[key] = ws
+                capturing = torch._C._cuda_isCurrentStreamCapturing()
+        if capturing:  # a graph may be replayed on any stream: it has a workspace of its own, cleared at every replay
+            return self.attention_workspace(n_q_heads, L, stream)
+        ws = _WORKSPACES.get((self._index, raw))
+        if ws is None or ws.numel() < self._bytes(n_q_heads, L):
+            _WORKSPACES[self._index, raw] = ws = self.attention_workspace(n_q_heads, L, stream)
         return ws
 
     def attend(self, q: torch.Tensor, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
-               scale: float | None = None, stream=None) -> torch.Tensor:
+               scale: float | None = None, stream=None, workspace: torch.Tensor | None = None) -> torch.Tensor:
         """Attention of the L newest tokens of every request: q, out bf16 [n_seqs, L, n_q_heads, head_dim]; lse
         fp32 [n_seqs, L, n_q_heads] or None; scale defaults to head_dim ** -0.5.  Row l sees the positions below
         seq_lens[b] - L + 1 + l; a row that sees nothing gives 0 (lse -inf).  An out that is not given is allocated on
-        `stream`."""
+        `stream`.
+
+        workspace: one of ``attention_workspace`` (or uint8 memory whose first MOE_ATTENTION_COUNTER_BYTES bytes are
+        zero); calls in it must not overlap, replays of graphs that captured them included.  Without it the calls of
+        a stream share one of their own, and a captured call gets one that its graph clears before every run."""
         L, heads, qs = self._step_rows(q, "q")
         if out is None:
             out = _empty(q.shape, q.dtype, self.device, stream)
@@ -185,11 +208,14 @@ class PagedKVCache:
             raise ValueError(f"lse must be a contiguous fp32 tensor of shape {tuple(q.shape[:3])}")
         if q.numel() == 0:
             return out
-        ws = self._workspace(heads, L, stream)
+        raw = _raw_stream(stream)
+        ws = self._workspace(heads, L, stream, raw) if workspace is None else workspace
+        if workspace is not None and (ws.dtype != torch.uint8 or ws.get_device() != self._index or not ws.is_contiguous()):
+            raise ValueError(f"workspace must be contiguous uint8 memory on {self.device}")
         a = moe_attention_t(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), ws.data_ptr(),
                             ws.numel(), qs, os_, heads, L,
                             self.head_dim ** -0.5 if scale is None else scale)
-        status = lib().moe_paged_attention(self._ref, ctypes.byref(a), _raw_stream(stream))
+        status = lib().moe_paged_attention(self._ref, ctypes.byref(a), raw)
         if status:
             _ok("moe_paged_attention", status)
         return out

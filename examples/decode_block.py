@@ -28,11 +28,13 @@ FEW_ROWS = 4
 
 class DecoderBlock:
     def __init__(self, layer: moe.MoELayer, cache: moe.PagedKVCache, n_q_heads: int, norm_attn, norm_moe, w_qkv, w_o,
-                 eps: float = 1e-6):
-        """norm_*: [d]; w_qkv: bf16 [(n_q + 2 n_kv) head_dim, d]; w_o: bf16 [d, n_q head_dim]."""
+                 eps: float = 1e-6, max_new: int = 1):
+        """norm_*: [d]; w_qkv: bf16 [(n_q + 2 n_kv) head_dim, d]; w_o: bf16 [d, n_q head_dim].  max_new: the most new
+        tokens of a step whose attention runs in the block's workspace (the blocks of a model may share one)."""
         self.layer, self.cache, self.n_q, self.eps = layer, cache, n_q_heads, eps
         self.norm_attn, self.norm_moe, self.w_qkv, self.w_o = norm_attn, norm_moe, w_qkv, w_o
-        self.n_kv, self.hd = cache.n_kv_heads, cache.head_dim
+        self.n_kv, self.hd, self.max_new = cache.n_kv_heads, cache.head_dim, max_new
+        self.workspace = cache.attention_workspace(n_q_heads, max_new)  # a captured step need not clear one
 
     def step(self, x: torch.Tensor, residual: torch.Tensor | None, L: int):
         """x: bf16 [n_seqs * L, d], the block before's MoE output (or the embedding), residual: the stream beside it
@@ -44,7 +46,7 @@ class DecoderBlock:
         q, k, v = qkv.split((self.n_q, self.n_kv, self.n_kv), dim=2)  # views: the calls take the rows' stride
         self.cache.append(k, v)
         o = torch.empty((B, L, self.n_q, self.hd), dtype=x.dtype, device=x.device)
-        self.cache.attend(q, out=o)
+        self.cache.attend(q, out=o, workspace=self.workspace if L <= self.max_new else None)
         a = o.view(T, -1) @ self.w_o.t()
         moe.moe_add_rms_norm(a, stream, self.norm_moe, self.eps, sum_out=stream, y=y)
         return (self.layer.forward_few(y) if T <= FEW_ROWS else self.layer.forward(y)), stream
@@ -75,7 +77,7 @@ def random_block(d: int, f: int, E: int, k: int, n_q: int, n_kv: int, hd: int, n
     bf = torch.bfloat16
     return DecoderBlock(layer, cache, n_q, (1 + rand(d, std=0.1)).to(bf), (1 + rand(d, std=0.1)).to(bf),
                         rand((n_q + 2 * n_kv) * hd, d, std=d ** -0.5).to(bf),
-                        rand(d, n_q * hd, std=(n_q * hd) ** -0.5).to(bf))
+                        rand(d, n_q * hd, std=(n_q * hd) ** -0.5).to(bf), max_new=L)
 
 
 def main() -> None:

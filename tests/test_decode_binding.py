@@ -65,7 +65,7 @@ def m(monkeypatch):
 def cache(m, n_seqs=3, heads=2, head_dim=64):
     c = object.__new__(m.PagedKVCache)
     c.n_seqs, c.n_kv_heads, c.head_dim = n_seqs, heads, head_dim
-    c.device, c._index, c._ref, c._workspaces = torch.device("cuda", 0), 0, None, {}
+    c.device, c._index, c._ref, c._workspace_bytes = torch.device("cuda", 0), 0, None, {}
     return c
 
 
@@ -179,3 +179,74 @@ def test_results_are_allocated_on_the_stream_that_writes_them(m, monkeypatch):
             assert made == [want]
             raw = m.library.calls[-1][1][-1]
             assert (getattr(raw, "value", raw) or 0) == (stream or 0)
+
+
+# ---------------------------------------------------------------------------------------------- attention workspaces
+def test_attention_workspaces(m, monkeypatch):
+    """One a stream for every cache and shape, a private one in a capture, the caller's where it is given; the counters are
+    cleared, the rest is not."""
+    from block_scaled_fp4_sqrt_gb300 import decode
+    sizes, state, made = {(4, 1): 6000, (4, 2): 9000, (8, 1): 7000}, dict(stream=1, capturing=False), []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            self.before = state["stream"]
+            state["stream"] = self.stream or self.before
+
+        def __exit__(self, *_):
+            state["stream"] = self.before
+
+    def empty(shape, dtype=None, device=None, _real=torch.empty):
+        t = torch.full(shape, 7, dtype=dtype) if dtype is torch.uint8 else _real(shape, dtype=dtype)
+        made.append((state["stream"], t))
+        return Memory(t)
+
+    class Memory(OnGpu):
+        def __getitem__(self, at):
+            return self.t[at]
+
+    def size(ref, heads, L):
+        return sizes[heads, L]
+
+    m.library.moe_paged_attention_workspace = size
+    m.library.moe_paged_attention = lambda ref, a, stream: used.append((a._obj.workspace, a._obj.workspace_bytes, stream)) or 0
+    used = []
+    monkeypatch.setattr(decode, "_WORKSPACES", {})
+    monkeypatch.setattr(decode, "_raw_stream", lambda stream: state["stream"] if stream is None else stream)
+    monkeypatch.setattr(m, "_raw_stream", lambda stream: state["stream"] if stream is None else stream)
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: handle)
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: state["capturing"], raising=False)
+    monkeypatch.setattr(torch, "empty", empty)
+    one, two = cache(m), cache(m)
+    q1, q2, q8 = zeros(3, 1, 4, 64), zeros(3, 2, 4, 64), zeros(3, 1, 8, 64)
+
+    def attend(c, q, **kw):
+        made.clear()
+        c.attend(q, out=q, **kw)
+        return used[-1], list(made)
+
+    (ws, n, stream), new = attend(one, q1)
+    assert stream == 1 and n == 6000 and len(new) == 1 and new[0][0] == 1
+    t, zero = new[0][1], m.MOE_ATTENTION_COUNTER_BYTES
+    assert t.data_ptr() == ws and not t[:zero].any() and (t[zero:] == 7).all()
+    assert attend(two, q1) == ((ws, 6000, 1), [])          # another cache: the same
+    (ws2, n, _), new = attend(one, q2)                     # a larger call: a larger one
+    assert n == 9000 and len(new) == 1
+    assert attend(two, q8) == ((ws2, 9000, 1), []) and attend(one, q1) == ((ws2, 9000, 1), [])
+    (ws3, n, stream), new = attend(one, q1, stream=5)      # another stream: its own, made there
+    assert stream == 5 and n == 6000 and ws3 != ws2 and [s for s, _ in new] == [5]
+    state["capturing"] = True
+    (ws4, n, _), new = attend(one, q1)                     # in a capture: one that no other call uses
+    assert n == 6000 and ws4 not in (ws2, ws3) and len(new) == 1
+    assert len(attend(one, q1, stream=5)[1]) == 1
+    mine = zeros(9000, dtype=torch.uint8)
+    assert attend(one, q2, workspace=mine) == ((mine.data_ptr(), 9000, 1), [])
+    state["capturing"] = False
+    assert attend(one, q1) == ((ws2, 9000, 1), [])
+    for bad in (zeros(9000, dtype=BF), OnGpu(torch.zeros(9000, dtype=torch.uint8)[::2]), zeros(9000, dtype=torch.uint8, index=1)):
+        with pytest.raises(ValueError):
+            one.attend(q1, out=q1, workspace=bad)

@@ -198,3 +198,52 @@ def test_results_on_another_stream_do_not_take_the_current_streams_memory(moe): 
             got = call(stream=stream)
             side.synchronize()
             assert got.data_ptr() not in at and torch.equal(got, want)
+
+
+def test_graphs_and_eager_calls_of_one_cache_may_overlap(moe):  # noqa: F811
+    """Captured calls count in workspaces of their own: two graphs captured on a stream, and eager calls there, all at
+    once."""
+    lens = [20000, 300, 9000]
+    cache, g = make_cache(moe, lens, 2, 128, 64, "bf16", seed=470)
+    fill(cache, g, lens)
+    q = [randn(g, 3, 1, 8, 128).to(BF) for _ in range(3)]
+    want = [cache.attend(t) for t in q]
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs, outs = [], [torch.empty_like(t) for t in q]
+    with torch.cuda.stream(side):
+        cache.attend(q[0], outs[0])  # the stream's own workspace exists before the captures
+        for i in (0, 1):
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                cache.attend(q[i], outs[i])
+            graphs.append(graph)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for t in outs:
+            t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(other):
+            graphs[0].replay()
+        graphs[1].replay()
+        with torch.cuda.stream(side):
+            cache.attend(q[2], outs[2])
+        torch.cuda.synchronize()
+        for t, w in zip(outs, want):
+            assert torch.equal(t, w)
+    cache.check()
+
+
+def test_attend_in_a_workspace_of_the_callers(moe):  # noqa: F811
+    lens = [20000, 300]
+    cache, g = make_cache(moe, lens, 2, 128, 64, "mxfp8", seed=480)
+    fill(cache, g, lens)
+    q1, q4 = (randn(g, 2, L, 8, 128).to(BF) for L in (1, 4))
+    want = [cache.attend(q) for q in (q1, q4)]
+    ws = cache.attention_workspace(8, 4)
+    for _ in range(2):
+        for q, w in zip((q1, q4), want):
+            assert torch.equal(cache.attend(q, workspace=ws), w)
+    with pytest.raises(moe.MoEError) as err:
+        cache.attend(randn(g, 2, 16, 8, 128).to(BF), workspace=ws)  # larger row tiles
+    assert err.value.status == 3
