@@ -1074,6 +1074,20 @@ cudaError_t launch_rows(const AttnParams& p, int num_sms, cudaStream_t s) {
   }
 }
 
+// Blocks of the grid for row tiles of tr rows.
+int grid_blocks(const moe_kv_cache_t& c, int tr, int num_sms) {
+  auto of = [&](auto mx, auto d) {
+    constexpr bool MX = decltype(mx)::value;
+    constexpr int D = decltype(d)::value;
+    return tr == 16 ? Cfg<D, MX, 1>::kBlocks : tr == 32 ? Cfg<D, MX, 2>::kBlocks : Cfg<D, MX, 4>::kBlocks;
+  };
+  const std::integral_constant<int, 64> d64;
+  const std::integral_constant<int, 128> d128;
+  const bool mx = c.format == MOE_KV_MXFP8;
+  return num_sms * (c.head_dim == 128 ? (mx ? of(std::true_type{}, d128) : of(std::false_type{}, d128))
+                                      : (mx ? of(std::true_type{}, d64) : of(std::false_type{}, d64)));
+}
+
 struct Sizes {
   int64_t rows;
   int row_tiles;
@@ -1092,7 +1106,7 @@ moe_status_t plan(const moe_kv_cache_t& c, int n_q_heads, int L, int num_sms, co
   z->row_tiles = (int)((z->rows + tr - 1) / tr);
   const int64_t units = (int64_t)c.n_seqs * c.n_kv_heads * z->row_tiles;
   if (units > (1ll << 30)) return decode_fail(MOE_ERR_UNSUPPORTED, "%s: too many row tiles", call);
-  z->blocks = num_sms * 4;  // the most blocks an SM holds
+  z->blocks = grid_blocks(c, tr, num_sms);
   z->groups = z->blocks / kJoin + 1;
   if ((z->blocks + 2 * z->groups) * 4 > MOE_ATTENTION_COUNTER_BYTES)
     return decode_fail(MOE_ERR_UNSUPPORTED, "%s: %d SMs", call, num_sms);

@@ -247,3 +247,20 @@ def test_attend_in_a_workspace_of_the_callers(moe):  # noqa: F811
     with pytest.raises(moe.MoEError) as err:
         cache.attend(randn(g, 2, 16, 8, 128).to(BF), workspace=ws)  # larger row tiles
     assert err.value.status == 3
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("L,limit", [(4, 11e6), (8, 17e6), (16, 33e6)])  # row tiles of 16, 32 and 64
+def test_a_workspace_holds_two_parts_a_block(moe, fmt, D, L, limit):  # noqa: F811
+    """No more than the blocks of the form need, and nothing is written past it: long requests split over all blocks."""
+    lens = [40000, 25000, 31000]
+    cache, g = make_cache(moe, lens, 2, D, 64, fmt, seed=490)
+    fill(cache, g, lens)
+    q = randn(g, 3, L, 8, D).to(BF)
+    n = moe.lib().moe_paged_attention_workspace(cache._ref, 8, L)
+    assert 0 < n < limit * D / 128
+    guarded = torch.full((n + (1 << 20),), 0xA5, dtype=torch.uint8, device=DEV)
+    guarded[:moe.MOE_ATTENTION_COUNTER_BYTES] = 0
+    out, _ = attend_c(moe, cache, q, guarded[:n])
+    assert torch.equal(out, cache.attend(q)) and torch.all(guarded[n:] == 0xA5)
