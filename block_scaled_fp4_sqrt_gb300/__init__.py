@@ -180,9 +180,16 @@ def _input(x: torch.Tensor, token_ids: torch.Tensor | None = None) -> moe_input_
                        None if token_ids is None else ctypes.c_void_p(token_ids.data_ptr()))
 
 
+def _on_current_gpu(name: str, index: int) -> None:
+    """The library launches on the current device."""
+    current = torch._C._cuda_getDevice()
+    if index != current:
+        raise ValueError(f"{name} lies on cuda:{index}, but the current device is cuda:{current}")
+
+
 def _dense(t: torch.Tensor, dtype: torch.dtype, shape) -> bool:
     """Whether t is dense rows of this type and shape on a GPU, as a kernel reads or writes them."""
-    return t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous()
+    return t.is_cuda and t.shape == shape and t.dtype is dtype and t.is_contiguous()
 
 
 def _refuse(t: torch.Tensor, name: str, what: str):
@@ -248,7 +255,11 @@ def moe_forward_few(x, router_w, router_bias, experts, shared, out, topk_ids=Non
     shape = x.shape
     if len(shape) != 2 or not _dense(x, torch.bfloat16, shape):
         _refuse(x, "x", "bf16 [T, d]")
-    T = shape[0]
+    T, gpu = shape[0], x.get_device()
+    _on_current_gpu("x", gpu)
+    for t in (out, token_ids, topk_ids, topk_w):
+        if t is not None and t.get_device() != gpu:
+            raise ValueError(f"x lies on cuda:{gpu}, another tensor of the call on {t.device}")
     if not _dense(out, torch.bfloat16, shape):
         _refuse(out, "out", f"bf16 {tuple(shape)}")
     if token_ids is not None and not (_dense(token_ids, torch.int32, (token_ids.numel(),)) and token_ids.numel() >= T):

@@ -10,7 +10,7 @@ import ctypes
 
 import torch
 
-from . import MOE_ATTENTION_COUNTER_BYTES, MOE_OK, MoEError, _empty, _ok, _on_stream, _raw_stream, lib, moe_attention_t, moe_kv_cache_t, moe_norm_t
+from . import MOE_ATTENTION_COUNTER_BYTES, MOE_OK, MoEError, _empty, _ok, _on_current_gpu, _on_stream, _raw_stream, lib, moe_attention_t, moe_kv_cache_t, moe_norm_t
 
 MOE_KV_BF16, MOE_KV_MXFP8 = 0, 1
 # The attention workspaces of calls outside captures, one for each GPU and stream, as large as the largest call so far: the
@@ -20,10 +20,10 @@ _WORKSPACES: dict[tuple[int, int], torch.Tensor] = {}
 KV_STATUS = {1: "a sequence length outside the block table", 2: "a page index outside the cache"}
 
 
-def _rows(t: torch.Tensor, name: str, shape, dtype=torch.bfloat16) -> tuple[int, int]:
-    """Address and row stride of a row-strided 2-D CUDA tensor with contiguous columns."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+def _rows(t: torch.Tensor, name: str, shape, gpu: int, dtype=torch.bfloat16) -> tuple[int, int]:
+    """Address and row stride of a row-strided 2-D tensor on cuda:gpu with contiguous columns."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != gpu:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on cuda:{gpu}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     row, col = t.stride()
     if col != 1 and shape[1] > 1:
@@ -46,21 +46,25 @@ def moe_add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None, weight: tor
     if len(shape) != 2:
         raise ValueError(f"x must be [T, d], got {tuple(shape)}")
     T, d = shape
+    gpu = x.get_device()
+    if gpu < 0:
+        raise ValueError(f"x must be a CUDA tensor, got one on {x.device}")
+    _on_current_gpu("x", gpu)
     w32 = weight.dtype is torch.float32
     if not (w32 or weight.dtype is torch.bfloat16) or weight.shape != (d,) or not weight.is_contiguous() or \
-            not weight.is_cuda:
-        raise ValueError(f"weight must be a contiguous bf16 or fp32 CUDA tensor of {d} columns")
-    xp, xs = _rows(x, "x", shape)
-    rp, rs = (None, 0) if residual is None else _rows(residual, "residual", shape)
-    up, us = (None, 0) if sum_out is None else _rows(sum_out, "sum_out", shape)
-    yp, ys = (None, 0) if y is None else _rows(y, "y", shape)
+            weight.get_device() != gpu:
+        raise ValueError(f"weight must be a contiguous bf16 or fp32 tensor of {d} columns on cuda:{gpu}")
+    xp, xs = _rows(x, "x", shape, gpu)
+    rp, rs = (None, 0) if residual is None else _rows(residual, "residual", shape, gpu)
+    up, us = (None, 0) if sum_out is None else _rows(sum_out, "sum_out", shape, gpu)
+    yp, ys = (None, 0) if y is None else _rows(y, "y", shape, gpu)
     qp = sp = None
     if y_q is not None:
-        qp, row = _rows(y_q, "y_q", shape, torch.uint8)
+        qp, row = _rows(y_q, "y_q", shape, gpu, torch.uint8)
         if row != d and T > 1:
             raise ValueError("y_q must be contiguous")
     if y_s is not None:
-        sp, row = _rows(y_s, "y_s", (T, d // 32), torch.uint8)
+        sp, row = _rows(y_s, "y_s", (T, d // 32), gpu, torch.uint8)
         if row != d // 32 and T > 1:
             raise ValueError("y_s must be contiguous")
     if T <= 1:  # the stride of a lone row means nothing
@@ -149,6 +153,7 @@ class PagedKVCache:
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, stream=None) -> None:
         """Write the step's L new tokens: bf16 [n_seqs, L, n_kv_heads, head_dim], token l of request b at
         position seq_lens[b] - L + l (negative positions are skipped)."""
+        _on_current_gpu("the cache", self._index)
         L, _, ks = self._step_rows(k_new, "k_new", self.n_kv_heads)
         Lv, _, vs = self._step_rows(v_new, "v_new", self.n_kv_heads)
         if L != Lv:
@@ -197,6 +202,7 @@ class PagedKVCache:
         workspace: one of ``attention_workspace`` (or uint8 memory whose first MOE_ATTENTION_COUNTER_BYTES bytes are
         zero); calls in it must not overlap, replays of graphs that captured them included.  Without it the calls of
         a stream share one of their own, and a captured call gets one that its graph clears before every run."""
+        _on_current_gpu("the cache", self._index)
         L, heads, qs = self._step_rows(q, "q")
         if out is None:
             out = _empty(q.shape, q.dtype, self.device, stream)

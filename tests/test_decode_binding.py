@@ -57,6 +57,7 @@ def m(monkeypatch):
     for at in (mod, decode):
         monkeypatch.setattr(at, "lib", lambda: library)
         monkeypatch.setattr(at, "_raw_stream", lambda stream: 0 if stream is None else int(stream))
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     mod.library = library
     yield mod
     del mod.library
@@ -250,3 +251,41 @@ def test_attention_workspaces(m, monkeypatch):
     for bad in (zeros(9000, dtype=BF), OnGpu(torch.zeros(9000, dtype=torch.uint8)[::2]), zeros(9000, dtype=torch.uint8, index=1)):
         with pytest.raises(ValueError):
             one.attend(q1, out=q1, workspace=bad)
+
+
+# ---------------------------------------------------------------------------------------------- devices
+def test_calls_refuse_tensors_of_another_device(m, monkeypatch):
+    """A call runs on the current device: neither another device's tensors nor a mixture reach the library."""
+    def there(*shape, dtype=BF):
+        return zeros(*shape, dtype=dtype, index=1)
+
+    x, w, q, lay, c = zeros(4, 64), zeros(64), zeros(3, 1, 4, 64), layer(m), cache(m)
+    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+    mixed = [lambda: m.moe_add_rms_norm(x, None, there(64), y=x), lambda: m.moe_add_rms_norm(x, there(4, 64), w, y=x),
+             lambda: m.moe_add_rms_norm(x, None, w, y=there(4, 64)), lambda: m.moe_add_rms_norm(x, None, w, sum_out=there(4, 64)),
+             lambda: m.moe_add_rms_norm(x, None, w, y_q=there(4, 64, dtype=u8), y_s=zeros(4, 2, dtype=u8)),
+             lambda: m.moe_add_rms_norm(x, None, w, y_q=zeros(4, 64, dtype=u8), y_s=there(4, 2, dtype=u8)),
+             lambda: c.append(there(3, 1, 2, 64), zeros(3, 1, 2, 64)), lambda: c.attend(there(3, 1, 4, 64)),
+             lambda: c.attend(q, out=there(3, 1, 4, 64)), lambda: c.attend(q, out=q, lse=there(3, 1, 4, dtype=f32)),
+             lambda: lay.forward_few(zeros(3, 256), out=there(3, 256)),
+             lambda: lay.forward_few(zeros(3, 256), out=zeros(3, 256), topk_ids=there(3, 2, dtype=i32)),
+             lambda: lay.forward_few(zeros(3, 256), out=zeros(3, 256), topk_w=there(3, 2, dtype=f32)),
+             lambda: lay.forward_few(zeros(3, 256), out=zeros(3, 256), token_ids=there(3, dtype=i32))]
+    all_there = [lambda: m.moe_add_rms_norm(there(4, 64), None, there(64), y=there(4, 64)),
+                 lambda: lay.forward_few(there(3, 256), out=there(3, 256))]
+    new = zeros(3, 1, 2, 64)
+    here = [lambda: m.moe_add_rms_norm(x, None, w, y=x), lambda: c.append(new, new),
+            lambda: lay.forward_few(zeros(3, 256), out=zeros(3, 256))]
+    for call in mixed + all_there:
+        with pytest.raises(ValueError):
+            call()
+    assert not m.library.calls
+    for call in here:
+        call()
+    assert len(m.library.calls) == 3
+    m.library.calls.clear()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)  # the tensors' device is not the current one
+    for call in here + [lambda: c.attend(q, out=q)]:
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    assert not m.library.calls
