@@ -99,6 +99,7 @@ def main() -> None:
         return block.step(x0, None, L)
 
     side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())  # where the weights, lengths and x0 are still being written
     with torch.cuda.stream(side):
         for _ in range(3):
             step()

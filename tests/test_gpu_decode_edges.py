@@ -2,6 +2,8 @@
 scales at the ends of E8M0, prompts of many row tiles."""
 import ctypes
 import math
+import os
+import sys
 
 import pytest
 import torch
@@ -12,6 +14,8 @@ from gpu_support import assert_close, bf16_to_f64, x_to_device
 from test_gpu_decode import BF, DEV, HALF_ULP, attend_ref, check_attend, fill, gen, make_cache, moe, randn  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
 
 
 # ---------------------------------------------------------------------------------------------- workspaces
@@ -264,3 +268,21 @@ def test_a_workspace_holds_two_parts_a_block(moe, fmt, D, L, limit):  # noqa: F8
     guarded[:moe.MOE_ATTENTION_COUNTER_BYTES] = 0
     out, _ = attend_c(moe, cache, q, guarded[:n])
     assert torch.equal(out, cache.attend(q)) and torch.all(guarded[n:] == 0xA5)
+
+
+def test_the_example_waits_for_its_set_up(moe, monkeypatch, capsys):  # noqa: F811
+    """Its steps run on a stream of their own; the lengths and inputs are written on the current one, here after a pause."""
+    import decode_block
+    blocks = []
+
+    def built_late(*args, _build=decode_block.random_block, **kw):
+        blocks.append(_build(*args, **kw))
+        torch.cuda._sleep(200_000_000)  # 0.1 s of the current stream, in front of what main() still writes there
+        return blocks[-1]
+
+    monkeypatch.setattr(decode_block, "random_block", built_late)
+    monkeypatch.setattr(sys, "argv", ["decode_block.py", "--requests", "2", "--tokens", "2", "--context", "100", "--steps", "4"])
+    decode_block.main()
+    torch.cuda.synchronize()
+    assert blocks[0].cache.seq_lens.tolist() == [100 + 2 * (3 + 4)] * 2
+    assert "us a step" in capsys.readouterr().out
