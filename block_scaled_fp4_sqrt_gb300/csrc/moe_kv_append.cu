@@ -99,8 +99,9 @@ extern "C" moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const void* k
                        (long long)k_stride, (long long)v_stride);
   if (!aligned_to(k_new, 16) || !aligned_to(v_new, 16))
     return decode_fail(MOE_ERR_INVALID_ARG, "moe_kv_append: k_new and v_new must be 16-byte aligned");
-  if (L == 0 || c.n_seqs == 0 || c.max_pages == 0) return MOE_OK;
+  if (L == 0 || c.n_seqs == 0) return MOE_OK;
   if (!k_new || !v_new) return decode_fail(MOE_ERR_INVALID_ARG, "moe_kv_append: k_new or v_new is NULL");
+  if (!c.seq_lens) return decode_fail(MOE_ERR_INVALID_ARG, "moe_kv_append: seq_lens is NULL");
   st = check_device(nullptr);
   if (st != MOE_OK) return st;
   if (L > (1 << 30)) return decode_fail(MOE_ERR_UNSUPPORTED, "moe_kv_append: more than 2^30 new tokens a request");

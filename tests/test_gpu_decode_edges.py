@@ -286,3 +286,18 @@ def test_the_example_waits_for_its_set_up(moe, monkeypatch, capsys):  # noqa: F8
     torch.cuda.synchronize()
     assert blocks[0].cache.seq_lens.tolist() == [100 + 2 * (3 + 4)] * 2
     assert "us a step" in capsys.readouterr().out
+
+
+def test_append_to_a_table_without_pages_reports_the_lengths(moe):  # noqa: F811
+    """No page can hold the new tokens: the length is above the bound, as in any other table."""
+    pages = torch.zeros(4, 16, 1, 64, dtype=BF, device=DEV)
+    lens = torch.tensor([0, 3], dtype=torch.int32, device=DEV)
+    cache = moe.PagedKVCache(pages, pages.clone(), torch.empty(2, 0, dtype=torch.int32, device=DEV), lens)
+    new = torch.ones(2, 1, 1, 64, dtype=BF, device=DEV)
+    cache.append(new, new)
+    with pytest.raises(moe.MoEError, match="sequence length"):
+        cache.check()
+    assert torch.all(pages == 0)
+    lens.zero_()
+    cache.append(new, new)
+    cache.check()
