@@ -28,7 +28,8 @@ extern "C" {
  *   y   = bf16(t * w / sqrt(mean(t^2) + eps))
  *   y_q, y_s = the MXFP8 form of the bf16 rows y: E4M3 codes and one E8M0 byte per 32 columns, exactly what
  *         moe_permute writes for y (rows contiguous: [T, d] and [T, d / 32]); a valid input of moe_expert_ffn.
- * The mean and the norm use the unrounded fp32 t; every bf16 output is rounded once.
+ * The mean and the norm use the unrounded fp32 t; every bf16 output is rounded once.  The squares are summed in fp32: a
+ * row's root of the sum of squares is to lie below 1.8e19, and values below 1e-22 count as 0 in it.
  *   x, residual, sum, y   bf16, 16-byte aligned, row strides a multiple of 8 and at least d (0 = d).
  *   weight                [d], bf16 or fp32 (weight_f32 != 0), 16-byte aligned.
  *   d                     a multiple of 8 up to 65536, of 32 where y_q is asked for; T >= 0; eps >= 0.
@@ -133,8 +134,13 @@ MOE_API moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_
 /*
  * moe_forward for a batch of at most MOE_FEW_MAX_T rows, in one kernel: the same routing, MXFP8 activations,
  * experts and combine (see moe.h), with the weighted expert rows summed in fp32 as they are; a token's row has the
- * same bits alone and in any company.  The faster call for one or two rows; above four moe_forward is.  Arguments and
- * errors are moe_forward's; the expert sets must use MOE_ACT_MXFP8, and n_experts <= 512 for the learned router.
+ * same bits alone and in any company.  The faster call for one or two rows; above four moe_forward is.  The codes of a row
+ * of x or h are held in fp16 with the block scales relative to the row's largest: exact where a block's scale is at most
+ * 2^22 below that, with fewer bits further down, and possibly 0 where it is more than 2^31 below.
+ * Arguments and errors are moe_forward's, and three limits more, each MOE_ERR_UNSUPPORTED: the expert sets must use
+ * MOE_ACT_MXFP8; n_experts <= 512 for the learned router; and the rows must leave room in shared memory for the weights:
+ *   rows          1      2      3      4      5      6      7     8
+ *   d_model  <= any  39680  26112  19200  15104  12544  10496  8960
  * topk_ids int32 [T, top_k] and topk_w fp32 [T, top_k] receive the routing (each may be NULL).  Uses the
  * workspace of `experts`.  The kernel's blocks wait on one another: it is launched cooperatively, one block per
  * SM, and every wait is bounded by the handle's wait budget (moe_check reports MOE_ERR_TIMEOUT).

@@ -301,3 +301,20 @@ def test_append_to_a_table_without_pages_reports_the_lengths(moe):  # noqa: F811
     lens.zero_()
     cache.append(new, new)
     cache.check()
+
+
+# ---------------------------------------------------------------------------------------------- the few-token layer's limits
+@pytest.mark.parametrize("T,d", [(2, 39680), (4, 19200), (7, 10496), (8, 8960)])
+def test_few_takes_rows_up_to_the_stated_width(moe, T, d):  # noqa: F811
+    """include/moe_decode.h gives the widest d_model for every number of rows: that one runs, the next is refused."""
+    ly = layer_of(moe, d, 128, 4, 2, 510 + T)
+    x = randn(gen(520 + T), T, d).to(BF)
+    want = ly.forward(x)
+    got = ly.forward_few(x)
+    ly.check()
+    # the same arithmetic but for the fp16 rounding of moe_forward's rows and the order of fp32 sums
+    assert_close(bf16_to_f64(got), bf16_to_f64(want), f"{T} rows of {d}")
+    wider = layer_of(moe, d + 256, 128, 4, 2, 530 + T)
+    with pytest.raises(moe.MoEError) as err:
+        wider.forward_few(randn(gen(540 + T), T, d + 256).to(BF))
+    assert err.value.status == 2
