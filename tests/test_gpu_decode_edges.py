@@ -318,3 +318,58 @@ def test_few_takes_rows_up_to_the_stated_width(moe, T, d):  # noqa: F811
     with pytest.raises(moe.MoEError) as err:
         wider.forward_few(randn(gen(540 + T), T, d + 256).to(BF))
     assert err.value.status == 2
+
+
+# ---------------------------------------------------------------------------------------------- prompts
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("lens,kv,group,L,D,page", [
+    ([300, 777], 2, 4, 300, 128, 16),      # a prompt on an empty and on a filled cache: 19 row tiles of 64
+    ([2000], 1, 4, 2000, 64, 48),          # 125 row tiles
+    ([100, 0, 333, 64], 1, 16, 100, 64, 64),  # prompts shorter than the longest of them
+    ([1023], 2, 1, 257, 128, 128),         # one row over
+])
+def test_attend_prompts(moe, fmt, lens, kv, group, L, D, page):  # noqa: F811
+    cache, g = make_cache(moe, lens, kv, D, page, fmt, seed=450 + L)
+    fill(cache, g, lens)
+    q = (1.5 * randn(g, len(lens), L, kv * group, D)).to(BF)
+    out, lse = check_attend(cache, q, lens)
+    assert torch.equal(cache.attend(q), out)
+    if L > 2:  # the last rows alone: the same attention in another form of the kernel, to the same bounds
+        check_attend(cache, q[:, -2:].contiguous(), lens)
+
+
+@pytest.mark.parametrize("B,L", [(1, 1), (2, 2), (3, 4)])  # 1 and 4 rows: forward_few; 12: forward
+def test_the_blocks_moe_half_against_the_layer_in_64_bits(moe, B, L):  # noqa: F811
+    """Every row: the rows that the block's second norm makes, with their own routing, through the oracle's layer."""
+    import decode_block
+    d, f, E, k = 512, 256, 8, 2
+    block = decode_block.random_block(d, f, E, k, 8, 2, 64, B, 64, L, page=16, fmt="bf16", seed=11 * B)
+    ly = block.layer
+    host = [synth.ExpertWeights(*(getattr(e, n).cpu().numpy() for n in ("w13", "s13", "w2", "s2")))
+            for e in (ly.experts, ly.shared_w)]
+    g, seen = gen(500 + B), 0
+    for _ in range(3):
+        x, res = randn(g, B * L, d).to(BF), randn(g, B * L, d).to(BF)
+        rows = []
+        for name in ("forward", "forward_few"):  # what the block hands to its layer
+            def spy(y, call=getattr(moe.MoELayer, name).__get__(ly)):
+                rows.append(y.clone())
+                return call(y)
+            setattr(ly, name, spy)
+        block.cache.seq_lens.add_(L)
+        out, stream = block.step(x, res, L)
+        ly.check()
+        assert len(rows) == 1
+        t = stream.double()
+        y2 = t / torch.sqrt((t * t).mean(-1, keepdim=True) + block.eps) * block.norm_moe.double()
+        # the norm is of the unrounded sum: its rounding to the stream (2^-9 a value) moves a row's rms by less, and y2 is
+        # rounded once more
+        assert torch.all((rows[0].double() - y2).abs() <= 2 * (HALF_ULP + 2.0 ** -17) * y2.abs() + 2.0 ** -9 * y2.abs())
+        bits = rows[0].cpu().view(torch.int16).numpy().view("uint16")
+        ids, wts, margin = oracle.route(bits, ly.router_w.cpu().numpy(), ly.router_bias.cpu().numpy(), k, 1.5)
+        sure = margin >= oracle.MARGIN_MIN
+        ref = oracle.layer(bits, ids, wts, *host, 10.0)
+        seen += int(sure.sum())
+        if sure.any():
+            assert_close(bf16_to_f64(out)[sure], ref[sure], f"{B} x {L}")
+    assert seen >= 2 * B * L  # of three steps' rows
