@@ -3,10 +3,11 @@
 //   s_t = scale * q . k_t  for t < limit(row),  m = max s,  p_t = exp(s_t - m),  z = sum p,  out = sum p_t v_t / z
 //
 // The cache is read once, so a step's few rows a key-value head (heads of the group x L) leave it memory-bound where the
-// cache is bf16: three requests of up to 131,071 tokens 147 us (6.2 TB/s, 93 % of the copy rate), 64 requests x 8 rows
-// 93 us (5.3 TB/s).  An MXFP8 cache is half the bytes, and then the instructions bound it (unpacking, softmax and their
-// latencies at 12 to 16 warps an SM): 64 x 8 rows 96 us, 64 x 1 rows 72 us, where memory alone would take 38.  One request
-// of 333 tokens takes 8.4 us, of which the join of its six parts is about half.
+// cache is bf16: three requests of up to 131,071 tokens 148 us (6.2 TB/s, 92 % of the copy rate), 64 requests x 8 rows
+// 94 us (5.2 TB/s).  An MXFP8 cache is half the bytes, and then the instructions bound it (unpacking, softmax and their
+// latencies at 12 to 16 warps an SM): 64 x 8 rows 98 us, 64 x 1 rows 73 us, where memory alone would take 38.  One request
+// of 333 tokens takes 8.7 us, of which the join of its six parts is about half.  A prompt is bound by the products: 8191
+// new tokens, 8 x 4 heads of 128, 4.4 ms (every row tile walks all key tiles: 125 TFLOP/s of what lies below the diagonal).
 // Layout of the work:
 //  * A unit is (request, kv head, row tile): the rows r = l * group + j of the query heads that share the kv head,
 //    16 MT of them at a time.  Every unit is cut into tiles of 64 tokens; the tiles of all units, in order and with
@@ -29,9 +30,10 @@
 // transposed, so that the 128-row side is the cache's (K as it lies, block-scaled, times q in two MXFP8 parts; V unpacked
 // to bf16 as an MN-major operand), warps of their own for fetching and unpacking, issuing and softmax.  A 128 x 16 x 32
 // product takes 80 cycles there whatever its 16 columns hold, and the roles' code together misses the instruction cache;
-// 64 requests x 8 rows took 116 us against 96 us here, 64 x 1 rows 93 against 72 us.
+// 64 requests x 8 rows took 116 us against 96 us here, 64 x 1 rows 93 against 72 us (one set of inputs, repeated).
 //  * bf16 cache: both products in bf16 with fp32 accumulation.  p is rounded to bf16 (8 bits, as the output is);
-//    its sum is taken before that rounding.
+//    its sum is taken before that rounding.  The error against 64 bits is 0.0019 to 0.0022 of the output's rms, where the
+//    output's own rounding makes 0.0017: p in more bits would be a second product.
 //  * MXFP8 cache, scores: E4M3 codes become fp16 (exact, one conversion a pair) and meet q in fp16, its row scaled by
 //    a power of two to a maximum in [2^14, 2^15): bf16's 8 bits are kept down to 2^-28 of the maximum.  A block's
 //    E8M0 scale multiplies the fp32 product of its 32 columns.  (mma.sync on E4M3 operands runs the same fp16

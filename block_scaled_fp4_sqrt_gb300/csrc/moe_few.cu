@@ -5,12 +5,12 @@
 // token, about 0.6 GB for eight), so a step should take their time at HBM rate.  What moe_forward loses against that at
 // these sizes are the gaps between its five kernels; here one persistent block per SM keeps a ring of weight
 // tiles in flight from the routing to the end.
-// Measured (d = 4096, f = 2048, 256 experts, graph replays; moe_forward beside it): one token 31.2 us against 42.5
-// (14.6 at HBM rate: a cooperative launch takes about 5, the routing 5.7, the weights then arrive at 5.7 TB/s), two 45
-// against 61, three 63 against 62, four 80 against 79, five 96 against 97, eight 132 against 116 (90.8 at HBM rate).
-// From three tokens on the two are level, and at eight moe_forward leads: x, the partial products and the h slices of
-// eight tokens leave shared memory for four stages, and the instructions (60 % of the issue slots) get in each other's
-// way.  What it keeps is that a token's row has the same bits alone and in any company.
+// Measured (d = 4096, f = 2048, 256 experts, graph replays with other rows at every call; moe_forward beside it): one
+// token 33 to 35 us over boxes against 44.5 (14.6 at HBM rate: a cooperative launch takes about 5, the routing 6, the
+// weights then arrive at 5.7 TB/s), two 46 against 63, three 67 against 64, four 82 against 81, five 98 against 95, eight
+// 134 to 140 against 119 (90.8 at HBM rate).  Below three tokens it leads; at eight moe_forward does: x, the partial
+// products and the h slices of eight tokens leave shared memory for four stages, and the instructions (60 % of the issue
+// slots) get in each other's way.  What it keeps is that a token's row has the same bits alone and in any company.
 //
 //  1. Router.  Block b computes the fp32 logits of experts b, b + grid, .. for all tokens (its warps split d);
 //     the same pass loads x and quantises it to MXFP8.  A grid-wide count, then every block selects the top-k of

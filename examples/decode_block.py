@@ -22,7 +22,8 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import block_scaled_fp4_sqrt_gb300 as moe  # noqa: E402
 
 # The most rows for forward_few: its one kernel leads while launches and routing weigh most (one row of the full-size
-# layer 31 us against 42), is level at three and four rows and behind MoELayer.forward's tensor-memory GEMMs above.
+# layer 34 us against 44), is near MoELayer.forward at three and four rows (67 and 82 against 64 and 81; ahead on smaller
+# layers) and behind its tensor-memory GEMMs above.
 FEW_ROWS = 4
 
 
