@@ -39,7 +39,7 @@
 //    E8M0 scale multiplies the fp32 product of its 32 columns.  (mma.sync on E4M3 operands runs the same fp16
 //    instructions here, after conversions of both operands: 690 instead of 200 instructions a tile and warp.)
 //  * MXFP8 cache, values: E4M3 codes become bf16 by moving bits (value times 2^-120) and one packed multiplication
-//    by the block's scale times 2^120; every product of a code and a power of two is exact in bf16.
+//    by the block's scale times 2^120; a product of a code and a power of two is exact in bf16 (down to its smallest 2^-133).
 #include <float.h>
 
 #include <algorithm>
@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
             asm volatile("ld.shared.u8 %0, [%1];" : "=h"(code) : "r"(at));
             asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(sb + tk * C::kScale + col / 32));
             asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(code));
-            v[n][y] = __low2float(*reinterpret_cast<const __half2*>(&h2)) * __uint_as_float(e << 23);
+            v[n][y] = __low2float(*reinterpret_cast<const __half2*>(&h2)) * e8m0_float(e, 0);
           } else {
             uint16_t bits;
             asm volatile("ld.shared.u16 %0, [%1];" : "=h"(bits) : "r"(at));

@@ -373,3 +373,21 @@ def test_the_blocks_moe_half_against_the_layer_in_64_bits(moe, B, L):  # noqa: F
         if sure.any():
             assert_close(bf16_to_f64(out)[sure], ref[sure], f"{B} x {L}")
     assert seen >= 2 * B * L  # of three steps' rows
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_values_of_the_smallest_scale_beside_a_hidden_nan(moe, D):  # noqa: F811
+    """Values near 2^-123 in blocks of byte 0, with a NaN that the first rows do not see: taken one by one they are the same
+    values."""
+    cache, g = make_cache(moe, [50], 1, D, 16, "mxfp8", seed=560)
+    k = randn(g, 1, 50, 1, D).to(BF)
+    cache.append(k, (randn(g, 1, 50, 1, D).clamp(-3, 3) * 2.0 ** -123).to(BF))
+    page = cache.tab[0].tolist()
+    assert max(int(cache.v_scales[p].where(cache.v_scales[p] < 200, 0).max()) for p in page[:3]) == 0
+    q = randn(g, 1, 3, 2, D).to(BF)
+    want = cache.attend(q).float()[0, :2] * 2.0 ** 123
+    assert want.abs().max() > 2.0 ** -3
+    cache.v[page[49 // 16], 49 % 16] = 0x7F  # the last row's own token
+    got = cache.attend(q).float()[0, :2] * 2.0 ** 123
+    # two forms of the same products, each rounded to bf16 (below 2^-126 to a fixed step of 2^-133)
+    assert torch.all((got - want).abs() <= 2 * HALF_ULP * want.abs() + 2.0 ** -9)
