@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(const NormParams p, 
 // that two vectors a thread need (d = 4096: 256), and four or eight vectors a thread above 16384 / 32768 columns.
 static cudaError_t launch_add_rms_norm(const NormParams& p, int w_f32, cudaStream_t s) {
   const int nvec = p.d / 8;
-  if (nvec <= 64) return launch_pdl(add_rms_norm_kernel<2, true>, dim3((p.T + 7) / 8), dim3(256), 0, s, p, w_f32);
+  if (nvec <= 64) return launch_pdl(add_rms_norm_kernel<2, true>, dim3((p.T - 1) / 8 + 1), dim3(256), 0, s, p, w_f32);
   const int nv = nvec <= 2048 ? 2 : nvec <= 4096 ? 4 : 8;
   const dim3 block(((nvec + nv - 1) / nv + 31) / 32 * 32), grid(p.T);
   switch (nv) {

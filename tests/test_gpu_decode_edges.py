@@ -391,3 +391,27 @@ def test_attend_values_of_the_smallest_scale_beside_a_hidden_nan(moe, D):  # noq
     got = cache.attend(q).float()[0, :2] * 2.0 ** 123
     # two forms of the same products, each rounded to bf16 (below 2^-126 to a fixed step of 2^-133)
     assert torch.all((got - want).abs() <= 2 * HALF_ULP * want.abs() + 2.0 ** -9)
+
+
+# ---------------------------------------------------------------------------------------------- far rows
+def test_norm_rows_beyond_32_bit_offsets(moe):  # noqa: F811
+    """2.5 G elements; and the most rows that a call takes."""
+    T, d = 600_011, 4096
+    g = gen(570)
+    base = randn(g, 4096, d).to(BF)
+    x = torch.empty(T, d, dtype=BF, device=DEV)
+    for i in range(0, T, 4096):
+        x[i:i + 4096] = base[:min(4096, T - i)]
+    w = (1 + 0.1 * randn(g, d)).to(BF)
+    y, yq = torch.empty_like(x), torch.empty(T, d, dtype=torch.uint8, device=DEV)
+    ys = torch.empty(T, d // 32, dtype=torch.uint8, device=DEV)
+    moe.moe_add_rms_norm(x, None, w, 1e-6, None, y, yq, ys)
+    n = T % 4096
+    for t in (y.view(torch.int16), yq, ys):
+        assert torch.equal(t[-n:], t[:n]) and torch.equal(t[4096 * 100:4096 * 101], t[:4096])
+    del x, y, yq, ys
+    T = 2 ** 31 - 1
+    x = torch.ones(T, 8, dtype=BF, device=DEV)
+    x[-1] = 2
+    moe.moe_add_rms_norm(x, None, torch.ones(8, device=DEV), 0.0, None, x)
+    assert torch.all(x[:: 2 ** 16] == 1) and torch.all(x[-9:] == 1)  # every row has one value: the norm is 1
