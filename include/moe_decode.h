@@ -106,7 +106,8 @@ MOE_API moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const void* k_ne
  *   q, out   bf16 rows (b * L + l) of n_q_heads * head_dim elements at q_stride / out_stride (multiples of 8;
  *            0 = contiguous), 16-byte aligned.
  *   lse      fp32 [n_seqs, L, n_q_heads] or NULL.
- *   n_q_heads a multiple of n_kv_heads; L >= 0; scale finite; k and v span less than 64 GB each.
+ *   n_q_heads a multiple of n_kv_heads; L >= 0; scale finite; k and v span less than 64 GB each; the keys of an MXFP8
+ *            cache lie below 2^100 (their block sums are held in fp32 before q's own scale).
  *   workspace  at least moe_paged_attention_workspace(cache, n_q_heads, L) bytes, 256-byte aligned.  Its first
  *            MOE_ATTENTION_COUNTER_BYTES bytes must be ZERO before its first use; every call leaves them zero, and what
  *            else it holds does not matter.  So one buffer serves any calls, of any caches and shapes, that run one
@@ -136,7 +137,7 @@ MOE_API moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_
  * experts and combine (see moe.h), with the weighted expert rows summed in fp32 as they are; a token's row has the
  * same bits alone and in any company.  The faster call for one or two rows; above four moe_forward is.  The codes of a row
  * of x or h are held in fp16 with the block scales relative to the row's largest: exact where a block's scale is at most
- * 2^22 below that, with fewer bits further down, and possibly 0 where it is more than 2^31 below.
+ * 2^22 below that, with fewer bits further down, and possibly 0 where it is more than 2^31 below.  The experts' scales lie below 2^96.
  * Arguments and errors are moe_forward's, and three limits more, each MOE_ERR_UNSUPPORTED: the expert sets must use
  * MOE_ACT_MXFP8; n_experts <= 512 for the learned router; and the rows must leave room in shared memory for the weights:
  *   rows          1      2      3      4      5      6      7     8
