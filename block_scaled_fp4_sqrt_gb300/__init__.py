@@ -187,9 +187,9 @@ def _on_current_gpu(name: str, index: int) -> None:
         raise ValueError(f"{name} lies on cuda:{index}, but the current device is cuda:{current}")
 
 
-def _dense(t: torch.Tensor, dtype: torch.dtype, shape) -> bool:
-    """Whether t is dense rows of this type and shape on a GPU, as a kernel reads or writes them."""
-    return t.is_cuda and t.shape == shape and t.dtype is dtype and t.is_contiguous()
+def _dense(t: torch.Tensor, dtype: torch.dtype, n: int) -> bool:
+    """Whether t is n dense elements of this type on a GPU, as a kernel reads or writes them (in any shape)."""
+    return t.is_cuda and t.dtype is dtype and t.numel() == n and t.is_contiguous()
 
 
 def _refuse(t: torch.Tensor, name: str, what: str):
@@ -252,21 +252,20 @@ def moe_forward_few(x, router_w, router_bias, experts, shared, out, topk_ids=Non
                     stream=None) -> None:
     """moe_forward for at most MOE_FEW_MAX_T rows in one kernel: x and out bf16 [T, d], token_ids int32 [T or more];
     topk_ids int32 and topk_w fp32 [T, top_k] receive the routing."""
-    shape = x.shape
-    if len(shape) != 2 or not _dense(x, torch.bfloat16, shape):
+    if x.dim() != 2 or not _dense(x, torch.bfloat16, x.numel()):
         _refuse(x, "x", "bf16 [T, d]")
-    T, gpu = shape[0], x.get_device()
+    (T, d), gpu = x.shape, x.get_device()
     _on_current_gpu("x", gpu)
     for t in (out, token_ids, topk_ids, topk_w):
         if t is not None and t.get_device() != gpu:
             raise ValueError(f"x lies on cuda:{gpu}, another tensor of the call on {t.device}")
-    if not _dense(out, torch.bfloat16, shape):
-        _refuse(out, "out", f"bf16 {tuple(shape)}")
-    if token_ids is not None and not (_dense(token_ids, torch.int32, (token_ids.numel(),)) and token_ids.numel() >= T):
+    if not _dense(out, torch.bfloat16, T * d):
+        _refuse(out, "out", f"bf16 {(T, d)}")
+    if token_ids is not None and not (_dense(token_ids, torch.int32, token_ids.numel()) and token_ids.numel() >= T):
         _refuse(token_ids, "token_ids", f"int32 [{T}] or longer")
-    if topk_ids is not None and not _dense(topk_ids, torch.int32, (T, topk_ids.shape[-1])):
+    if topk_ids is not None and not _dense(topk_ids, torch.int32, T * topk_ids.shape[-1]):
         _refuse(topk_ids, "topk_ids", f"int32 [{T}, top_k]")
-    if topk_w is not None and not _dense(topk_w, torch.float32, (T, topk_w.shape[-1])):
+    if topk_w is not None and not _dense(topk_w, torch.float32, T * topk_w.shape[-1]):
         _refuse(topk_w, "topk_w", f"fp32 [{T}, top_k]")
     a = moe_input_t(x.data_ptr() or None, T, None if token_ids is None else token_ids.data_ptr())
     status = lib().moe_forward_few(ctypes.byref(a), None if router_w is None else router_w.data_ptr(),

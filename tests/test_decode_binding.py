@@ -133,6 +133,8 @@ def test_forward_few_passes_what_fits_and_refuses_the_rest(m):
     assert [c[0] for c in m.library.calls] == ["moe_forward_few"]
     lay.forward_few(x, token_ids=zeros(5, dtype=i32), **good)  # the first T of a longer list
     lay.forward_few(zeros(0, 256), out=zeros(0, 256))
+    six = zeros(6, 256)  # dense memory of the right size, kept in another shape: two requests of three rows
+    lay.forward_few(six, zeros(2, 3, dtype=i32), zeros(2, 3, 256), zeros(2, 3, 2, dtype=i32), zeros(2, 3, 2, dtype=f32))
     calls = len(m.library.calls)
     for kw in (dict(x=zeros(3, 128)), dict(x=zeros(3, 256, dtype=f32)), dict(x=OnGpu(torch.zeros(3, 512, dtype=BF)[:, ::2])),
                dict(x=x.t), dict(out=zeros(2, 256)), dict(out=zeros(3, 256, dtype=f32)), dict(out=zeros(3, 264)),
