@@ -46,111 +46,20 @@
 #include <cmath>
 #include <type_traits>
 
-#include "moe_decode_device.cuh"
+#include "moe_attention_fp4.h"
 
 namespace moe {
 
 namespace {
 
-constexpr int kTile = 64;      // tokens of a tile
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kWarpTok = kTile / kWarps;  // tokens of a tile that a warp fetches and scores
 constexpr int kPPitch = kTile * 2 + 16;   // bytes of a row of p: eight rows fall on distinct banks
-constexpr int kJoin = 16;                 // parts that are joined in one step
-// What beginning and ending a unit costs, in tiles, when the work is dealt.  64 requests of 100 to 8000 tokens, us at a
-// cost of 0 / 2 / 4 / 7: 8 rows MXFP8 145 / 107 / 105 / 114, 8 rows bf16 117 / 93 / 93 / 95; 200 requests of up to 1500
-// tokens 17.8 / 13.9 / 14.6 / 16.0; long requests do not depend on it.
-constexpr int kUnitCost = 3;
 constexpr float kGrow = 8.f;              // log2 units by which a score may exceed the running maximum
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
-struct AttnParams {
-  moe_kv_cache_t c;
-  const __nv_bfloat16* q;
-  __nv_bfloat16* out;
-  float* lse;
-  int64_t q_stride, out_stride;
-  int L, group, rows, row_tiles, Hq;  // rows = L * group
-  uint32_t page_units, row_units, head_units;  // the cache's strides in 16-byte units
-  float scale_log2;                   // scale * log2(e)
-  PageDiv pd;
-  int* counters;    // [grid] of the shared unit that begins in a block (at most one does), zero between calls
-  float* partial;   // [grid][2][rows of a tile][head_dim + 2]
-  int* group_counters;   // [grid / kJoin + 1][2], zero between calls
-  float* group_partial;  // [grid / kJoin + 1][2][rows of a tile][head_dim + 2]
-};
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? 16 : 0;
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? 4 : 0;
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-
-__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// d = a b (no accumulator to clear first)
-__device__ __forceinline__ void mma_f16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
-}
 
 // Two E4M3 codes (the low or high half of r) as an fp16 pair, exact.
 __device__ __forceinline__ uint32_t e4m3_f16(uint32_t r, bool high) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(high ? r >> 16 : r)));
   return h;
-}
-
-// (c0, c1) += (a0, a1) * (b0, b1)
-__device__ __forceinline__ void fma2(float& c0, float& c1, float a0, float a1, float b0, float b1) {
-  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%0, %1};\n"
-      " fma.rn.f32x2 c, a, b, c;\n mov.b64 {%0, %1}, c;\n}"
-      : "+f"(c0), "+f"(c1)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -170,11 +79,6 @@ __device__ __forceinline__ void e4m3_bf16(uint32_t r, uint32_t& even, uint32_t& 
   odd = (r & 0x80008000u) | o;
   top = __vimax3_u16x2(top, e, o);
 }
-
-// Position in the sequence of all tiles: request b (length len, nt tiles a unit), kv head, row tile rt, tile t.
-struct Cursor {
-  int b, head, rt, t, nt, len;
-};
 
 template <int D, bool MX, int MT>
 struct Cfg {
@@ -221,8 +125,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
   float* s_l = s_mx + kWarps * C::kRows;                      // [warp][row]
   float* s_f = s_l + kWarps * C::kRows;                       // [row] score factor
   int* s_lim = reinterpret_cast<int*>(s_f + C::kRows);        // [row] first position the row does not see
-  __shared__ int s_b, s_last;
-  __shared__ int64_t s_part[kWarps], s_first;
+  __shared__ int s_last;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int li = lane >> 2, lc = lane & 3;
@@ -230,80 +133,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
   pdl_trigger();
   pdl_wait();
 
-  // ---- this block's run of places
-  const int B = p.c.n_seqs, H = p.c.n_kv_heads, HR = H * p.row_tiles;
-  auto tiles_of = [](int len) { return len > 0 ? (len + kTile - 1) / kTile : 1; };
-  int64_t sum = 0;
-  for (int b = tid; b < B; b += kThreads) sum += tiles_of(seq_len_of(p.c, b)) + kUnitCost;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
-  if (lane == 0) s_part[warp] = sum;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) total += s_part[i];
-  total *= HR;
-  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t t0 = per * blockIdx.x, t1 = t0 + per < total ? t0 + per : total;
-  if (t0 >= t1) return;
-  Cursor cur;
-  {
-    const int64_t want = t0 / HR;  // in places of one unit per request
-    int64_t carry = 0;
-    for (int b0 = 0; b0 < B; b0 += kThreads) {
-      const int b = b0 + tid;
-      const int n = b < B ? tiles_of(seq_len_of(p.c, b)) + kUnitCost : 0;
-      int64_t incl = n;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
-        if (lane >= off) incl += o;
-      }
-      __syncthreads();
-      if (lane == 31) s_part[warp] = incl;
-      __syncthreads();
-      int64_t before = carry;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) before += s_part[i];
-        carry += s_part[i];
-      }
-      if (n > 0 && before + incl - n <= want && want < before + incl) {
-        s_b = b;
-        s_first = before + incl - n;
-      }
-      __syncthreads();
-      if (want < carry) break;
-    }
-    cur.b = s_b;
-    cur.len = seq_len_of(p.c, cur.b);
-    cur.nt = tiles_of(cur.len);
-    const int64_t off = t0 - s_first * HR;
-    const int w = (int)(off / (cur.nt + kUnitCost));
-    cur.t = (int)(off - (int64_t)w * (cur.nt + kUnitCost)) - kUnitCost;
-    cur.head = w / p.row_tiles;
-    cur.rt = w - cur.head * p.row_tiles;
-  }
-  int64_t pos = t0;  // place of the tile cur
-  if (cur.t < 0) {   // the run begins in front of a unit's first tile
-    pos -= cur.t;
-    cur.t = 0;
-  }
-  if (pos >= t1) return;
-  // to the next tile; returns how many places further it lies
-  auto advance = [&](Cursor& c) -> int {
-    if (++c.t < c.nt) return 1;
-    c.t = 0;
-    if (++c.rt < p.row_tiles) return 1 + kUnitCost;
-    c.rt = 0;
-    if (++c.head < H) return 1 + kUnitCost;
-    c.head = 0;
-    if (++c.b < B) {
-      c.len = seq_len_of(p.c, c.b);
-      c.nt = tiles_of(c.len);
-    }
-    return 1 + kUnitCost;
-  };
+  Run run;
+  if (!deal_run(p, tid, run)) return;
+  Cursor cur = run.cur;
+  const int64_t t0 = run.t0, t1 = run.t1, per = run.per;
+  int64_t pos = run.pos;  // place of the tile cur
 
   // ---- loading: a warp fetches 16 tokens of a tile
   const uint32_t smem_base = smem_addr(smem);
@@ -375,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
           late_dst = dst;
         }
       }
-      ld_pos += advance(ld);
+      ld_pos += advance_tile(p, ld);
       lookup();
     }
     cp_async_commit();
@@ -1048,7 +882,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, MX, MT>::kBlocks) paged_atten
       end_unit(pos - cur.t - kUnitCost);
       fresh = true;
     }
-    pos += advance(cur);
+    pos += advance_tile(p, cur);
   }
   cp_async_wait<0>();
 }
@@ -1078,6 +912,7 @@ cudaError_t launch_rows(const AttnParams& p, int num_sms, cudaStream_t s) {
 
 // Blocks of the grid for row tiles of tr rows.
 int grid_blocks(const moe_kv_cache_t& c, int tr, int num_sms) {
+  if (c.format == MOE_KV_MXFP4) return num_sms * attention_fp4_blocks(c.head_dim, tr);
   auto of = [&](auto mx, auto d) {
     constexpr bool MX = decltype(mx)::value;
     constexpr int D = decltype(d)::value;
@@ -1104,7 +939,7 @@ moe_status_t plan(const moe_kv_cache_t& c, int n_q_heads, int L, int num_sms, co
   z->rows = (int64_t)(n_q_heads / c.n_kv_heads) * L;
   if (z->rows > (1 << 20) || (int64_t)n_q_heads * c.head_dim > (1ll << 31))
     return decode_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^20 rows a kv head", call);
-  const int tr = tile_rows(z->rows);
+  const int tr = c.format == MOE_KV_MXFP4 ? attention_fp4_tile_rows(z->rows) : tile_rows(z->rows);
   z->row_tiles = (int)((z->rows + tr - 1) / tr);
   const int64_t units = (int64_t)c.n_seqs * c.n_kv_heads * z->row_tiles;
   if (units > (1ll << 30)) return decode_fail(MOE_ERR_UNSUPPORTED, "%s: too many row tiles", call);
@@ -1144,7 +979,8 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   // rows are addressed by 32-bit counts of 16-byte units
   const __int128 last = (__int128)(c.n_pages > 0 ? c.n_pages - 1 : 0) * c.page_stride +
                         (__int128)(c.page_size - 1) * c.row_stride + (__int128)(c.n_kv_heads - 1) * c.head_stride;
-  if (last / (c.format == MOE_KV_MXFP8 ? 16 : 8) >= 0xFFFFFFFFll)
+  const int64_t unit = c.format == MOE_KV_BF16 ? 8 : c.format == MOE_KV_MXFP8 ? 16 : 32;
+  if (last / unit >= 0xFFFFFFFFll)
     return decode_fail(MOE_ERR_UNSUPPORTED, "moe_paged_attention: k or v spans 64 GB or more");
   if (!std::isfinite(a->scale)) return decode_fail(MOE_ERR_INVALID_ARG, "moe_paged_attention: scale is not finite");
   const int64_t width = (int64_t)a->n_q_heads * c.head_dim;
@@ -1181,7 +1017,6 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   p.Hq = a->n_q_heads;
   p.scale_log2 = a->scale * kLog2e;
   p.pd = page_div((uint32_t)c.page_size);
-  const int64_t unit = c.format == MOE_KV_MXFP8 ? 16 : 8;
   p.page_units = (uint32_t)(c.page_stride / unit);
   p.row_units = (uint32_t)(c.row_stride / unit);
   p.head_units = (uint32_t)(c.head_stride / unit);
@@ -1191,7 +1026,8 @@ extern "C" moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const m
   p.group_partial = p.partial + 2 * z.blocks * (z.slot / 4);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool mx = c.format == MOE_KV_MXFP8;
-  cudaError_t e = c.head_dim == 128 ? (mx ? launch_rows<128, true>(p, sms, s) : launch_rows<128, false>(p, sms, s))
+  cudaError_t e = c.format == MOE_KV_MXFP4 ? launch_attention_fp4(p, sms, s)
+                  : c.head_dim == 128      ? (mx ? launch_rows<128, true>(p, sms, s) : launch_rows<128, false>(p, sms, s))
                                     : (mx ? launch_rows<64, true>(p, sms, s) : launch_rows<64, false>(p, sms, s));
   if (e != cudaSuccess) return decode_fail(MOE_ERR_CUDA, "moe_paged_attention: %s", cudaGetErrorString(e));
   return MOE_OK;

@@ -39,9 +39,9 @@ moe_status_t check_device(int* num_sms) {
 
 moe_status_t check_cache(const moe_kv_cache_t* c, const char* call) {
   if (!c) return decode_fail(MOE_ERR_INVALID_ARG, "%s: cache is NULL", call);
-  if (c->format != MOE_KV_BF16 && c->format != MOE_KV_MXFP8)
+  if (c->format != MOE_KV_BF16 && c->format != MOE_KV_MXFP8 && c->format != MOE_KV_MXFP4)
     return decode_fail(MOE_ERR_INVALID_ARG, "%s: unknown cache format %d", call, c->format);
-  const bool mx = c->format == MOE_KV_MXFP8;
+  const bool mx = c->format != MOE_KV_BF16;
   if (c->head_dim != 64 && c->head_dim != 128)
     return decode_fail(MOE_ERR_UNSUPPORTED, "%s: head_dim (%d) must be 64 or 128", call, c->head_dim);
   if (c->n_pages < 0 || c->page_size < 1 || c->n_kv_heads < 1 || c->n_seqs < 0 || c->max_pages < 0)

@@ -31,6 +31,26 @@ __device__ __forceinline__ uint4 f32_to_bf16x8(const float (&v)[8]) {
   return u;
 }
 
+// The largest magnitude of eight values as fp32 bits: above every finite value for infinities, and above those for NaN.
+__device__ __forceinline__ uint32_t abs_max_bits(const float (&v)[8]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  return top;
+}
+
+// Eight values of an MXFP4 block whose largest magnitude is top (abs_max_bits over the block): their codes, value i in bits
+// 4 i .., and the block's scale byte.  E2M1 has neither infinities nor NaN: a block that holds one gets the byte 255, which
+// reads as NaN, and codes 0.
+__device__ __forceinline__ uint8_t mxfp4_quad(const float (&v)[8], uint32_t top, uint32_t& codes) {
+  const bool finite = top < 0x7F800000u;
+  const int e = finite ? mxfp4_block_exp(__uint_as_float(top)) : 0;
+  const float mul = exp2_neg_int(e);
+  codes = e2m1x8(v[0] * mul, v[1] * mul, v[2] * mul, v[3] * mul, v[4] * mul, v[5] * mul, v[6] * mul, v[7] * mul);
+  if (!finite) codes = 0;
+  return finite ? (uint8_t)(e + 127) : (uint8_t)255;
+}
+
 // E8M0 byte j of w as a float, exact: two bytes at a time become bf16, which holds 2^-127 (byte 0) as a subnormal number.
 // (Shifts and masks read byte 0 as 0, and one instruction more to mend that costs the few-token layer 9 % at one token and
 // 3 % at eight, the attention 1 %: the conversion costs neither.)

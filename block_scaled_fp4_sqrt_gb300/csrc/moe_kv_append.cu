@@ -1,7 +1,7 @@
 // The paged cache's writer (moe_kv_append): token l of request b goes to position seq_lens[b] - L + l, in the
 // cache's own format.  A copy with a quantiser in it: each thread takes eight columns of one head of one token, of K and
 // of V (two 16-byte loads; four neighbouring lanes hold one MX block), looks their page up once and stores 16 bytes of
-// bf16 or 8 bytes of E4M3 twice.  The loads of the new values do not wait for the page lookup.
+// bf16, 8 bytes of E4M3 or 4 bytes of E2M1 twice.  The loads of the new values do not wait for the page lookup.
 // Memory-bound for prompts, latency-bound (length -> page -> store) for a step's few rows.  All index arithmetic is 32-bit
 // with divisions by multiplication: with 64-bit divisions, and K and V in threads of their own, instructions were the
 // bound (81 % of the issue slots, 15.2 us for a prompt of 8191 tokens, 8 heads of 128 in bf16).  Measured now: that prompt
@@ -25,7 +25,7 @@ struct AppendParams {
   PageDiv page, heads, len;
 };
 
-template <bool MX>
+template <int FMT>
 __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
   pdl_trigger();
   pdl_wait();
@@ -58,20 +58,32 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendParams p) {
     const int64_t at = page * c.page_stride + prow * c.row_stride + head * c.head_stride + col;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      if (!MX) {
+      if (FMT == MOE_KV_BF16) {
         if (page >= 0) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(i ? c.v : c.k) + at) = raw[i];
       } else {
         float v[8];
         bf16x8_to_f32(raw[i], v);
-        float amax = 0.f;
+        if constexpr (FMT == MOE_KV_MXFP8) {
+          float amax = 0.f;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) amax = fmaxf(amax, fabsf(v[x]));
-        amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 2));
-        const int e = mxfp8_block_exp(amax);
-        if (page >= 0) {
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(i ? c.v : c.k) + at) = e4m3_8(v, exp2_neg_int(e));
-          if ((lane & 3) == 0) (i ? c.v_s : c.k_s)[at >> 5] = (uint8_t)(e + 127);
+          for (int x = 0; x < 8; ++x) amax = fmaxf(amax, fabsf(v[x]));
+          amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(quad, amax, 2));
+          const int e = mxfp8_block_exp(amax);
+          if (page >= 0) {
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(i ? c.v : c.k) + at) = e4m3_8(v, exp2_neg_int(e));
+            if ((lane & 3) == 0) (i ? c.v_s : c.k_s)[at >> 5] = (uint8_t)(e + 127);
+          }
+        } else {
+          uint32_t top = abs_max_bits(v);
+          top = max(top, __shfl_xor_sync(quad, top, 1));
+          top = max(top, __shfl_xor_sync(quad, top, 2));
+          uint32_t codes;
+          const uint8_t scale = mxfp4_quad(v, top, codes);
+          if (page >= 0) {
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(i ? c.v : c.k) + (at >> 1)) = codes;
+            if ((lane & 3) == 0) (i ? c.v_s : c.k_s)[at >> 5] = scale;
+          }
         }
       }
     }
@@ -124,8 +136,10 @@ extern "C" moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const void* k
     p.l0 = (int)(row0 % L);
     p.n_units = (uint32_t)(std::min(step, rows - row0) * row_units);
     const dim3 grid((p.n_units + 255) / 256 < 152 * 8 ? (p.n_units + 255) / 256 : 152 * 8);  // what the SMs hold
-    const cudaError_t e = launch_pdl(c.format == MOE_KV_MXFP8 ? kv_append_kernel<true> : kv_append_kernel<false>, grid,
-                                     dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), p);
+    auto* kernel = c.format == MOE_KV_MXFP8   ? kv_append_kernel<MOE_KV_MXFP8>
+                   : c.format == MOE_KV_MXFP4 ? kv_append_kernel<MOE_KV_MXFP4>
+                                              : kv_append_kernel<MOE_KV_BF16>;
+    const cudaError_t e = launch_pdl(kernel, grid, dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), p);
     if (e != cudaSuccess) return decode_fail(MOE_ERR_CUDA, "moe_kv_append: %s", cudaGetErrorString(e));
   }
   return MOE_OK;

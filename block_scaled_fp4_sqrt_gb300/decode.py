@@ -12,7 +12,7 @@ import torch
 
 from . import MOE_ATTENTION_COUNTER_BYTES, MOE_OK, MoEError, _empty, _ok, _on_current_gpu, _on_stream, _raw_stream, lib, moe_attention_t, moe_kv_cache_t, moe_norm_t
 
-MOE_KV_BF16, MOE_KV_MXFP8 = 0, 1
+MOE_KV_BF16, MOE_KV_MXFP8, MOE_KV_MXFP4 = 0, 1, 4
 # The attention workspaces of calls outside captures, one for each GPU and stream, as large as the largest call so far: the
 # calls of a stream run one after another, whatever their caches and shapes.
 _WORKSPACES: dict[tuple[int, int], torch.Tensor] = {}
@@ -79,7 +79,8 @@ class PagedKVCache:
     """One layer's paged key-value cache over the caller's tensors.
 
     k, v: [n_pages, page_size, n_kv_heads, head_dim], bf16, or uint8 E4M3 codes (MXFP8) with k_scales,
-    v_scales uint8 [..., head_dim / 32]; any strides with contiguous columns, the same for k and v.
+    v_scales uint8 [..., head_dim / 32]; or uint8 [..., head_dim / 2] of two E2M1 codes each, the even column in the low
+    half (MXFP4), with the same scales; any strides with contiguous columns, the same for k and v.
     block_table: int32 [n_seqs, max_pages], contiguous; seq_lens: int32 [n_seqs], the tokens of every request
     including the ones of the current step.  Their contents may change between calls (in place).
 
@@ -91,16 +92,19 @@ class PagedKVCache:
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.stride(3) != 1:
             raise ValueError("k and v must be alike: [n_pages, page_size, n_kv_heads, head_dim], columns contiguous")
         if k.dtype != (torch.uint8 if mx else torch.bfloat16) or v.dtype != k.dtype:
-            raise ValueError("k and v must be bf16, or uint8 E4M3 codes with k_scales and v_scales")
+            raise ValueError("k and v must be bf16, or uint8 E4M3 or E2M1 codes with k_scales and v_scales")
         if mx != (v_scales is not None):
             raise ValueError("k_scales and v_scales go together")
         n_pages, page, heads, d = k.shape
+        # codes of head_dim columns with head_dim / 32 scales: a byte a column, or half a byte
+        per_byte = 2 if mx and k_scales.dim() == 4 and 16 * k_scales.shape[3] == d else 1
+        d *= per_byte
         if mx:
             for s in (k_scales, v_scales):
                 if s.dtype != torch.uint8 or s.shape != (n_pages, page, heads, d // 32) or s.stride(3) != 1:
                     raise ValueError("scales must be uint8 [n_pages, page_size, n_kv_heads, head_dim / 32]")
-                if any(n > 1 and 32 * a != b for n, a, b in zip(s.shape[:3], s.stride(), k.stride())):
-                    raise ValueError("the scales' strides must be those of k and v divided by 32")
+                if any(n > 1 and 32 * a != per_byte * b for n, a, b in zip(s.shape[:3], s.stride(), k.stride())):
+                    raise ValueError("the scales' strides must be those of k and v, counted in columns, divided by 32")
         if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
             raise ValueError("block_table must be a contiguous int32 [n_seqs, max_pages]")
         if seq_lens.dtype != torch.int32 or seq_lens.shape != block_table.shape[:1] or not seq_lens.is_contiguous():
@@ -112,10 +116,11 @@ class PagedKVCache:
         self.block_table, self.seq_lens = block_table, seq_lens
         self.device, self.n_seqs, self.n_kv_heads, self.head_dim = k.device, seq_lens.shape[0], heads, d
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
-        st = [s if n > 1 else 0 for n, s in zip(k.shape[:3], k.stride())]  # strides of lone entries mean nothing
+        self.format = (MOE_KV_MXFP4 if per_byte == 2 else MOE_KV_MXFP8) if mx else MOE_KV_BF16
+        st = [s * per_byte if n > 1 else 0 for n, s in zip(k.shape[:3], k.stride())]  # strides of lone entries mean nothing
         self._c = moe_kv_cache_t(k.data_ptr(), v.data_ptr(), k_scales.data_ptr() if mx else None,
                                  v_scales.data_ptr() if mx else None, block_table.data_ptr(), seq_lens.data_ptr(),
-                                 self.status.data_ptr(), *st, MOE_KV_MXFP8 if mx else MOE_KV_BF16, n_pages, page,
+                                 self.status.data_ptr(), *st, self.format, n_pages, page,
                                  heads, d, self.n_seqs, block_table.shape[1])
         self._ref = ctypes.byref(self._c)
         self._workspace_bytes = {}
@@ -124,13 +129,14 @@ class PagedKVCache:
     @classmethod
     def allocate(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, block_table: torch.Tensor,
                  seq_lens: torch.Tensor, fmt: str = "bf16") -> "PagedKVCache":
-        """A cache with zeroed pages of its own on the block table's device; fmt: "bf16" or "mxfp8"."""
-        if fmt not in ("bf16", "mxfp8"):
+        """A cache with zeroed pages of its own on the block table's device; fmt: "bf16", "mxfp8" or "mxfp4"."""
+        if fmt not in ("bf16", "mxfp8", "mxfp4"):
             raise ValueError(f"unknown cache format {fmt!r}")
         shape, dev = (n_pages, page_size, n_kv_heads, head_dim), block_table.device
         if fmt == "bf16":
             return cls(*(torch.zeros(shape, dtype=torch.bfloat16, device=dev) for _ in "kv"), block_table, seq_lens)
-        k, v = (torch.zeros(shape, dtype=torch.uint8, device=dev) for _ in "kv")
+        codes = (*shape[:3], head_dim // 2) if fmt == "mxfp4" else shape
+        k, v = (torch.zeros(codes, dtype=torch.uint8, device=dev) for _ in "kv")
         ks, vs = (torch.zeros((*shape[:3], head_dim // 32), dtype=torch.uint8, device=dev) for _ in "kv")
         return cls(k, v, block_table, seq_lens, ks, vs)
 

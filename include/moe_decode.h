@@ -59,8 +59,10 @@ MOE_API moe_status_t moe_add_rms_norm(const moe_norm_t* args, moe_stream_t strea
  *                page * page_stride + row * row_stride + head * head_stride + i, the same for k and v, so any
  *                order of page rows and heads can be described.  16-byte aligned.
  *   format       MOE_KV_BF16: bf16 elements.  MOE_KV_MXFP8: E4M3 codes with one E8M0 byte per 32 elements of a
- *                row in k_s / v_s, at the same strides divided by 32 (bytes 0..254).
- *   strides      multiples of 8 (bf16) or 32 (MXFP8).
+ *                row in k_s / v_s, at the same strides divided by 32 (bytes 0..254).  MOE_KV_MXFP4: E2M1 codes, element
+ *                2 i in the low half of byte i of a row (the strides count elements, two to a byte), with scales as for
+ *                MXFP8; a block of scale 255 reads as NaN.
+ *   strides      multiples of 8 (bf16) or 32 (MXFP8, MXFP4).
  *   block_table  int32 [n_seqs][max_pages]: page of the request's tokens [j * page_size, (j + 1) * page_size).
  *                Entries past a request's length are never read.
  *   seq_lens     int32 [n_seqs]: tokens of every request, the step's L new ones included; may be 0.
@@ -70,7 +72,7 @@ MOE_API moe_status_t moe_add_rms_norm(const moe_norm_t* args, moe_stream_t strea
  *   head_dim     64 or 128; page_size >= 1; n_kv_heads >= 1.
  * Pages may be shared by requests as long as no call writes to them.
  */
-enum { MOE_KV_BF16 = 0, MOE_KV_MXFP8 = 1 };
+enum { MOE_KV_BF16 = 0, MOE_KV_MXFP8 = 1, MOE_KV_MXFP4 = 4 };
 enum { MOE_KV_BAD_LENGTH = 1, MOE_KV_BAD_PAGE = 2 };
 typedef struct {
   void* k;
@@ -90,7 +92,8 @@ typedef struct {
  * Write the L new tokens of every request into the cache: token l of request b goes to position
  * seq_lens[b] - L + l (a negative position is skipped).  k_new, v_new: bf16 rows (b * L + l) of n_kv_heads *
  * head_dim elements at k_stride / v_stride (multiples of 8; 0 = contiguous), 16-byte aligned: views of a fused
- * projection's output serve.  MXFP8 caches receive the codes and scales of moe.h's MXFP8 rule, exact.
+ * projection's output serve.  MXFP8 caches receive the codes and scales of moe.h's MXFP8 rule, exact;
+ * MXFP4 caches those of its MXFP4 rule, and the scale 255 with codes 0 for a block that holds a NaN or an infinity.
  * L >= 0: one token, a verify step's rows or a whole prompt.
  */
 MOE_API moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const void* k_new, int64_t k_stride,
@@ -107,7 +110,8 @@ MOE_API moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const void* k_ne
  *            0 = contiguous), 16-byte aligned.
  *   lse      fp32 [n_seqs, L, n_q_heads] or NULL.
  *   n_q_heads a multiple of n_kv_heads; L >= 0; scale finite; k and v span less than 64 GB each; the keys of an MXFP8
- *            cache lie below 2^100 (their block sums are held in fp32 before q's own scale).
+ *            or MXFP4 cache lie below 2^100 (their block sums are held in fp32 before q's own scale), and so do the values of
+ *            an MXFP4 cache (their sums are held times 2^19).
  *   workspace  at least moe_paged_attention_workspace(cache, n_q_heads, L) bytes, 256-byte aligned.  Its first
  *            MOE_ATTENTION_COUNTER_BYTES bytes must be ZERO before its first use; every call leaves them zero, and what
  *            else it holds does not matter.  So one buffer serves any calls, of any caches and shapes, that run one
