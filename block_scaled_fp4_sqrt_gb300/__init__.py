@@ -29,7 +29,8 @@ EXPORTED = ("moe_experts_create", "moe_experts_set_hash_table", "moe_workspace_s
             "moe_stack_create", "moe_stack_forward", "moe_stack_destroy", "moe_mx_blocks_unpack",
             "moe_experts_set_activation_format", "moe_measure_mxf4_peak", "moe_testing_read_h",
             "moe_experts_set_router", "moe_testing_read_y32", "moe_testing_set_pair_gemm", "moe_add_rms_norm",
-            "moe_kv_append", "moe_paged_attention", "moe_paged_attention_workspace", "moe_forward_few")
+            "moe_kv_append", "moe_paged_attention", "moe_paged_attention_workspace", "moe_forward_few",
+            "moe_head_norm_rope", "moe_pages_fork", "moe_pages_resize", "moe_pages_compact", "moe_copy_pages")
 
 MOE_MX_NIBBLES_PAIRED, MOE_MX_NIBBLES_SPLIT = 0, 1
 MOE_ACT_MXFP8, MOE_ACT_MXFP4 = 0, 1
@@ -77,6 +78,20 @@ class moe_attention_t(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class moe_head_rope_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "q_out", "k_out", "q_weight", "k_weight", "turns", "axis",
+                                                "positions")] +
+                [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride", "k_out_stride",
+                                               "position_stride")] +
+                [(n, ctypes.c_int32) for n in ("T", "L", "n_q_heads", "n_kv_heads", "head_dim", "rot_dim", "pairs", "n_axes",
+                                               "weight_f32")] + [("eps", ctypes.c_float)])
+
+
+class moe_page_pool_t(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("block_table", "seq_lens", "page_refs", "status")] +
+                [(n, ctypes.c_int32) for n in ("n_seqs", "max_pages", "n_pages", "page_size")])
+
+
 class moe_input_t(ctypes.Structure):
     _fields_ = [("x_bf16", ctypes.c_void_p), ("T", ctypes.c_int32), ("token_ids", ctypes.c_void_p)]
 
@@ -122,6 +137,12 @@ def lib() -> ctypes.CDLL:
         L.moe_paged_attention.argtypes = [cachep, ctypes.POINTER(moe_attention_t), vp]
         L.moe_paged_attention_workspace.argtypes = [cachep, i32, i32]
         L.moe_paged_attention_workspace.restype = ctypes.c_size_t
+        L.moe_head_norm_rope.argtypes = [cachep, ctypes.POINTER(moe_head_rope_t), vp]
+        poolp = ctypes.POINTER(moe_page_pool_t)
+        L.moe_pages_fork.argtypes = [poolp, vp, vp, i32, vp]
+        L.moe_pages_resize.argtypes = [poolp, vp, vp, vp]
+        L.moe_pages_compact.argtypes = [poolp, vp, i32, vp]
+        L.moe_copy_pages.argtypes = [ctypes.POINTER(cachep), i32, vp, i32, vp]
         L.moe_forward_few.argtypes = [inp, vp, vp, vp, vp, vp, vp, vp, vp]
         L.moe_stack_destroy.restype = None
         L.moe_experts_destroy.argtypes = [vp]
@@ -624,4 +645,4 @@ class MoEStack:
             pass
 
 
-from .decode import PagedKVCache, moe_add_rms_norm  # noqa: E402  (needs the names above)
+from .decode import PagedKVCache, PagePool, RotaryPlan, moe_add_rms_norm, moe_copy_pages, moe_head_norm_rope  # noqa: E402  (needs the names above)

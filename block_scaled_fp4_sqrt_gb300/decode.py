@@ -1,5 +1,6 @@
 """The decode-step operators around the MoE layer (``include/moe_decode.h``): the residual addition with its
-root-mean-square norm, and the paged key-value cache with the attention that reads it.
+root-mean-square norm, the norms of the heads with the position rotation, the paged key-value cache with the attention
+that reads it, and the pool of its pages.
 
 Like the rest of the binding these only check and marshal arguments; every step runs in the library's
 kernels, asynchronously on the given stream (default: the current one).
@@ -7,17 +8,22 @@ kernels, asynchronously on the given stream (default: the current one).
 from __future__ import annotations
 
 import ctypes
+from fractions import Fraction
 
 import torch
 
-from . import MOE_ATTENTION_COUNTER_BYTES, MOE_OK, MoEError, _empty, _ok, _on_current_gpu, _on_stream, _raw_stream, lib, moe_attention_t, moe_kv_cache_t, moe_norm_t
+from . import (MOE_ATTENTION_COUNTER_BYTES, MOE_OK, MoEError, _dense, _empty, _ok, _on_current_gpu, _on_stream, _raw_stream,
+               _refuse, lib, moe_attention_t, moe_head_rope_t, moe_kv_cache_t, moe_norm_t, moe_page_pool_t)
 
 MOE_KV_BF16, MOE_KV_MXFP8, MOE_KV_MXFP4 = 0, 1, 4
 # The attention workspaces of calls outside captures, one for each GPU and stream, as large as the largest call so far: the
 # calls of a stream run one after another, whatever their caches and shapes.
 _WORKSPACES: dict[tuple[int, int], torch.Tensor] = {}
 
-KV_STATUS = {1: "a sequence length outside the block table", 2: "a page index outside the cache"}
+KV_STATUS = {1: "a sequence length outside the block table", 2: "a page index outside the cache",
+             4: "a request wanted more pages than are free", 8: "a fork between requests that do not allow it"}
+MOE_POOL_MAX_SEQS = 8192
+PAIRS = {"half": 0, "adjacent": 1}
 
 
 def _rows(t: torch.Tensor, name: str, shape, gpu: int, dtype=torch.bfloat16) -> tuple[int, int]:
@@ -73,6 +79,119 @@ def moe_add_rms_norm(x: torch.Tensor, residual: torch.Tensor | None, weight: tor
                                     _raw_stream(stream))
     if status:
         _ok("moe_add_rms_norm", status)
+
+
+# 2 pi to 40 digits: a frequency becomes a fraction of a turn without losing a bit of its 64
+_TWO_PI = Fraction(6283185307179586476925286766559005768394, 10 ** 39)
+
+
+class RotaryPlan:
+    """The rotation of a model's heads: inv_freq [rot_dim / 2], the angle per position of every pair in radians (numbers or a
+    tensor, read as 64-bit); pairs "half" (columns i and i + rot_dim / 2) or "adjacent" (2 i and 2 i + 1); axis_of
+    [rot_dim / 2], the position axis that a pair turns with (None: one axis).  Kept as exact fractions of a turn, so that
+    far positions lose nothing."""
+
+    def __init__(self, inv_freq, axis_of=None, pairs: str = "half", device="cuda"):
+        if pairs not in PAIRS:
+            raise ValueError(f"unknown pairs {pairs!r}")
+        freq = [float(f) for f in inv_freq]
+        axis = None if axis_of is None else [int(a) for a in axis_of]
+        if any(f != f or abs(f) == float("inf") for f in freq):
+            raise ValueError("inv_freq must be finite")
+        if axis is not None and (len(axis) != len(freq) or any(not 0 <= a < 256 for a in axis)):
+            raise ValueError(f"axis_of must hold {len(freq)} axes in [0, 256)")
+        turns = [round(Fraction(f) / _TWO_PI * 2 ** 64) % 2 ** 64 for f in freq]
+        self.rot_dim, self.n_axes = 2 * len(freq), 1 + max(axis or [0])
+        self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
+        self.axis = None if axis is None else torch.tensor(axis, dtype=torch.uint8, device=device)
+        self.pairs = PAIRS[pairs]
+
+
+def _head_rows(t: torch.Tensor, name: str, gpu: int) -> tuple:
+    """(rows, heads, head_dim, row stride) of a bf16 tensor [..., heads, head_dim] whose rows lie at one stride."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) < 3 or t.dtype is not torch.bfloat16 or t.get_device() != gpu:
+        raise ValueError(f"{name} must be bf16 [..., heads, head_dim] on cuda:{gpu}, got {t.dtype} {tuple(shape)} on {t.device}")
+    h, d = shape[-2:]
+    rows, row = 1, 0
+    for n, s in zip(reversed(shape[:-2]), reversed(stride[:-2])):
+        if n > 1:
+            if rows > 1 and s != rows * row:
+                raise ValueError(f"{name}: the rows must lie at one stride")
+            if rows == 1:
+                row = s
+                if row == 0:  # the library reads stride 0 as contiguous rows
+                    raise ValueError(f"{name} is broadcast: its rows must lie in memory of their own")
+        rows *= n
+    if (d > 1 and stride[-1] != 1) or (h > 1 and stride[-2] != d):
+        raise ValueError(f"{name}: heads must be contiguous")
+    return rows, h, d, row
+
+
+def _rope_args(gpu: int, q, k, v, rope: RotaryPlan, positions, q_weight, k_weight, eps, q_out, k_out) -> moe_head_rope_t:
+    a, rows, dim, shapes = moe_head_rope_t(), None, None, {}
+    for name, t in (("q", q), ("k", k), ("v", v), ("q_out", q_out), ("k_out", k_out)):
+        if t is None:
+            continue
+        n, h, d, row = _head_rows(t, name, gpu)
+        if (rows is not None and rows != n) or (dim is not None and dim != d):
+            raise ValueError(f"{name} holds {n} rows of heads of {d} columns, others {rows} of {dim}")
+        rows, dim, shapes[name] = n, d, h
+        setattr(a, name, t.data_ptr())
+        setattr(a, name + "_stride", row)
+    for x, y in (("q", "q_out"), ("k", "k_out"), ("k", "v")):
+        if x in shapes and y in shapes and shapes[x] != shapes[y]:
+            raise ValueError(f"{x} has {shapes[x]} heads, {y} {shapes[y]}")
+    if rope.turns.get_device() != gpu:
+        raise ValueError(f"the rotation's plan lies on {rope.turns.device}, the tensors on cuda:{gpu}")
+    if positions is not None:
+        if positions.dtype is not torch.int32 or positions.get_device() != gpu or not positions.is_contiguous() or \
+                positions.numel() != rope.n_axes * rows:
+            _refuse(positions, "positions", f"int32 [{rope.n_axes}, {rows}]")
+        a.positions = positions.data_ptr()
+    kinds = {w.dtype for w in (q_weight, k_weight) if w is not None}
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        if len(kinds) != 1 or w.dtype not in (torch.bfloat16, torch.float32) or w.shape != (dim,) or not w.is_contiguous() or \
+                w.get_device() != gpu:
+            raise ValueError(f"{name} must be a contiguous bf16 or fp32 tensor of {dim} columns on cuda:{gpu}, of the other "
+                             "weight's type")
+        setattr(a, name, w.data_ptr())
+    a.turns = rope.turns.data_ptr() if rope.rot_dim else None
+    a.axis = None if rope.axis is None else rope.axis.data_ptr()
+    a.T, a.n_q_heads, a.n_kv_heads = rows, shapes.get("q", 0), shapes.get("k", 0)
+    a.head_dim, a.rot_dim, a.pairs, a.n_axes = dim, rope.rot_dim, rope.pairs, rope.n_axes
+    a.weight_f32, a.eps = int(kinds == {torch.float32}), eps
+    return a
+
+
+def moe_head_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, rope: RotaryPlan, positions: torch.Tensor,
+                       q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                       q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None) -> tuple:
+    """Root-mean-square norm of every head of q and k and its rotation, in one pass; returns (q_out, k_out).
+
+    q, k: bf16 [..., heads, head_dim] with the same rows, or None (views of a fused projection serve); positions: int32
+    [n_axes, rows] contiguous (in any shape of that order); weights: [head_dim] bf16 or fp32, None for no norm.  q_out may be
+    q and k_out k; outputs that are not given are allocated on `stream`."""
+    lead = q if q is not None else k
+    if lead is None:
+        raise ValueError("q or k must be given")
+    gpu = lead.get_device()
+    if gpu < 0:
+        raise ValueError(f"q and k must be CUDA tensors, got one on {lead.device}")
+    _on_current_gpu("q" if q is not None else "k", gpu)
+    if (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError("an output without its input")
+    q_out = _empty(q.shape, q.dtype, q.device, stream) if q is not None and q_out is None else q_out
+    k_out = _empty(k.shape, k.dtype, k.device, stream) if k is not None and k_out is None else k_out
+    a = _rope_args(gpu, q, k, None, rope, positions, q_weight, k_weight, eps, q_out, k_out)
+    if positions is None and a.T and rope.rot_dim:
+        raise ValueError("positions must be given")
+    status = lib().moe_head_norm_rope(None, ctypes.byref(a), _raw_stream(stream))
+    if status:
+        _ok("moe_head_norm_rope", status)
+    return q_out, k_out
 
 
 class PagedKVCache:
@@ -168,6 +287,34 @@ class PagedKVCache:
         if status:
             _ok("moe_kv_append", status)
 
+    def append_rotated(self, q: torch.Tensor | None, k_new: torch.Tensor, v_new: torch.Tensor, rope: RotaryPlan,
+                       positions: torch.Tensor | None = None, q_weight: torch.Tensor | None = None,
+                       k_weight: torch.Tensor | None = None, eps: float = 1e-6, q_out: torch.Tensor | None = None,
+                       k_out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+        """``moe_head_norm_rope`` of the step's L new tokens and ``append`` of the rotated keys and of the values, in one
+        pass: q [n_seqs, L, n_q_heads, head_dim] or None, k_new, v_new [n_seqs, L, n_kv_heads, head_dim]; positions None:
+        the tokens' places in their sequences.  Returns q_out (allocated on `stream` if not given; may be q); k_out, if given,
+        receives the rotated keys as well."""
+        _on_current_gpu("the cache", self._index)
+        if q is None and q_out is not None:
+            raise ValueError("an output without its input")
+        q_out = _empty(q.shape, q.dtype, self.device, stream) if q is not None and q_out is None else q_out
+        L = None
+        for name, t, heads in (("q", q, None), ("q_out", q_out, None), ("k_new", k_new, self.n_kv_heads),
+                               ("v_new", v_new, self.n_kv_heads), ("k_out", k_out, self.n_kv_heads)):
+            if t is None:
+                continue
+            n = self._step_rows(t, name, heads)[0]
+            if L is not None and n != L:
+                raise ValueError(f"{name} holds another number of tokens")
+            L = n
+        a = _rope_args(self._index, q, k_new, v_new, rope, positions, q_weight, k_weight, eps, q_out, k_out)
+        a.L = L
+        status = lib().moe_head_norm_rope(self._ref, ctypes.byref(a), _raw_stream(stream))
+        if status:
+            _ok("moe_head_norm_rope", status)
+        return q_out
+
     def _bytes(self, n_q_heads: int, L: int) -> int:
         n = self._workspace_bytes.get((n_q_heads, L))
         if n is None:
@@ -234,7 +381,107 @@ class PagedKVCache:
 
     def check(self) -> None:
         """Wait for the device, then raise if a call met a bad length or page since the last check."""
-        bits = int(self.status.item())
-        if bits != MOE_OK:
-            self.status.zero_()
-            raise MoEError("PagedKVCache", 5, "; ".join(t for b, t in KV_STATUS.items() if bits & b))
+        _check_status(self.status, "PagedKVCache")
+
+
+def _check_status(status: torch.Tensor, name: str) -> None:
+    bits = int(status.item())
+    if bits != MOE_OK:
+        status.zero_()
+        raise MoEError(name, 5, "; ".join(t for b, t in KV_STATUS.items() if bits & b))
+
+
+class PagePool:
+    """The pages of caches that share one block table, managed on the device without a host synchronisation.
+
+    block_table int32 [n_seqs, max_pages], seq_lens int32 [n_seqs] (those of the caches) and page_refs int32 [n_pages], the
+    number of requests that hold each page: contiguous, changed in place.  ``resize`` grows, truncates and frees, ``fork``
+    branches, ``compact`` moves pages together; ``moe_copy_pages`` then copies the contents that they ask for, in every
+    layer's cache, before the next append."""
+
+    def __init__(self, block_table: torch.Tensor, seq_lens: torch.Tensor, page_refs: torch.Tensor, page_size: int):
+        for name, t, dims in (("block_table", block_table, 2), ("seq_lens", seq_lens, 1), ("page_refs", page_refs, 1)):
+            if t.dtype is not torch.int32 or t.dim() != dims or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {dims} dimensions")
+        if seq_lens.shape[0] != block_table.shape[0]:
+            raise ValueError("seq_lens and block_table hold different numbers of requests")
+        if len({t.device for t in (block_table, seq_lens, page_refs)}) != 1:
+            raise ValueError("the pool's tensors must be on one CUDA device")
+        if seq_lens.shape[0] > MOE_POOL_MAX_SEQS:
+            raise ValueError(f"a pool holds up to {MOE_POOL_MAX_SEQS} requests")
+        self.block_table, self.seq_lens, self.page_refs, self.page_size = block_table, seq_lens, page_refs, page_size
+        self.device, self._index = block_table.device, block_table.get_device()
+        self.n_seqs, self.max_pages, self.n_pages = *block_table.shape, page_refs.shape[0]
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._c = moe_page_pool_t(block_table.data_ptr(), seq_lens.data_ptr(), page_refs.data_ptr(), self.status.data_ptr(),
+                                  self.n_seqs, self.max_pages, self.n_pages, page_size)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def allocate(cls, n_seqs: int, max_pages: int, n_pages: int, page_size: int, device="cuda") -> "PagePool":
+        """A pool of its own tensors: every request empty, every page free."""
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.full((n_seqs, max_pages), -1, **i32), torch.zeros(n_seqs, **i32), torch.zeros(n_pages, **i32), page_size)
+
+    def _ints(self, t: torch.Tensor, name: str, *shape) -> int:
+        if t.shape != shape or not _dense(t, torch.int32, t.numel()) or t.get_device() != self._index:
+            _refuse(t, name, f"int32 {list(shape)} on {self.device}")
+        return t.data_ptr()
+
+    def fork(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+        """Request dst[i], of length 0, becomes a branch of request src[i]: the same pages and length.  int32 [n]."""
+        _on_current_gpu("the pool", self._index)
+        n = src.shape[0] if src.dim() == 1 else -1
+        status = lib().moe_pages_fork(self._ref, self._ints(src, "src", n), self._ints(dst, "dst", n), n, _raw_stream(stream))
+        if status:
+            _ok("moe_pages_fork", status)
+
+    def resize(self, new_lens: torch.Tensor, copies: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Every request gets length new_lens[b] (int32 [n_seqs]): pages behind it go back, missing ones are taken.  Returns
+        copies, int32 [n_seqs, 2] (allocated on `stream` if not given): (old page, new page) of the requests that grow inside a
+        page that others hold too, for ``moe_copy_pages``, and (-1, -1).  A request whose pages are not to be had keeps its
+        length (``check`` reports it)."""
+        _on_current_gpu("the pool", self._index)
+        if copies is None:
+            copies = _empty((self.n_seqs, 2), torch.int32, self.device, stream)
+        status = lib().moe_pages_resize(self._ref, self._ints(new_lens, "new_lens", self.n_seqs),
+                                        self._ints(copies, "copies", self.n_seqs, 2), _raw_stream(stream))
+        if status:
+            _ok("moe_pages_resize", status)
+        return copies
+
+    def compact(self, copies: torch.Tensor, stream=None) -> torch.Tensor:
+        """Move the highest live pages into the lowest free ones, at most copies.shape[0] of them; copies, int32
+        [capacity, 2], receives (from, to) of the moves for ``moe_copy_pages``, and (-1, -1)."""
+        _on_current_gpu("the pool", self._index)
+        n = copies.shape[0]
+        status = lib().moe_pages_compact(self._ref, self._ints(copies, "copies", n, 2), n, _raw_stream(stream))
+        if status:
+            _ok("moe_pages_compact", status)
+        return copies
+
+    def free_pages(self) -> int:
+        """The number of free pages (waits for the device)."""
+        return int((self.page_refs == 0).sum())
+
+    def check(self) -> None:
+        """Wait for the device, then raise if a call met a bad table, or could not do what was asked, since the last check."""
+        _check_status(self.status, "PagePool")
+
+
+def moe_copy_pages(caches, copies: torch.Tensor, stream=None) -> None:
+    """In every cache of the list, page copies[i, 1] receives the contents of page copies[i, 0]; pairs whose first page is
+    negative are skipped.  copies: int32 [n, 2].  No page may be the second of two pairs, or of one and the first of another."""
+    caches = list(caches)
+    if len(copies.shape) != 2 or copies.shape[1] != 2 or not _dense(copies, torch.int32, copies.numel()):
+        _refuse(copies, "copies", "int32 [n, 2]")
+    _on_current_gpu("copies", copies.get_device())
+    for c in caches:
+        if c._index != copies.get_device():
+            raise ValueError(f"a cache lies on {c.device}, copies on {copies.device}")
+    if not caches:
+        return
+    refs = (ctypes.POINTER(moe_kv_cache_t) * len(caches))(*[ctypes.pointer(c._c) for c in caches])
+    status = lib().moe_copy_pages(refs, len(caches), copies.data_ptr(), copies.shape[0], _raw_stream(stream))
+    if status:
+        _ok("moe_copy_pages", status)

@@ -1,11 +1,12 @@
 /*
  * moe_decode.h -- the operators around the MoE layer in a decode or verify step: the residual addition with
- * its root-mean-square norm, the paged key-value cache (its writer and the attention that reads it), and the
- * whole MoE layer for a few tokens in one kernel.
+ * its root-mean-square norm, the norms of the heads with the position rotation, the paged key-value cache (its writer, the
+ * attention that reads it and the management of its pages), and the whole MoE layer for a few tokens in one kernel.
  *
  * A decoder block of one step, T = n_seqs * L rows (L new tokens of every request; L = 8 in the verify batch of
  * 64 requests x 8 rows that moe.h describes):
- *   moe_add_rms_norm -> (q, k, v projections) -> moe_kv_append -> moe_paged_attention -> (output projection)
+ *   moe_add_rms_norm -> (q, k, v projections) -> moe_kv_append, or moe_head_norm_rope with the cache
+ *   -> moe_paged_attention -> (output projection)
  *   -> moe_add_rms_norm -> moe_forward, or moe_forward_few for up to MOE_FEW_MAX_T rows.
  *
  * The conventions of moe.h hold: device pointers, asynchronous on `stream`, no allocation inside a call, the
@@ -135,6 +136,96 @@ typedef struct {
 MOE_API size_t moe_paged_attention_workspace(const moe_kv_cache_t* cache, int32_t n_q_heads, int32_t L);
 MOE_API moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_attention_t* args,
                                          moe_stream_t stream);
+
+/*
+ * Norms of the heads with the position rotation, for the rows of a step: between the fused projection and the attention.
+ * For every head of q and k (and row r, or (b, l) with a cache):
+ *   x' = x * w / sqrt(mean(x^2) + eps)         over the head's D columns, fp32; x' = x where the weight is NULL
+ *   pair (i, j):  y_i = x'_i cos a - x'_j sin a,  y_j = x'_i sin a + x'_j cos a,   a = 2 pi position[axis_i] turns_i / 2^64
+ * for the rot_dim / 2 pairs: MOE_ROPE_HALF (i, i + rot_dim / 2), MOE_ROPE_ADJACENT (2 i, 2 i + 1); columns from rot_dim on
+ * are x'.  Every output is the fp32 value rounded once.
+ *   rope       turns [rot_dim / 2], device, 8-byte aligned: the angle per position as a fraction of a turn, in units of 2^-64
+ *              turns (modulo 2^64): the phase of any position is exact integer arithmetic, so that far positions lose nothing.
+ *              axis [rot_dim / 2] or NULL (all 0): which row of `positions` a pair turns with, below n_axes.
+ *              rot_dim even, 0 to head_dim.
+ *   positions  int32 [n_axes][T] with rows position_stride apart (0 = T), or NULL with a cache: seq_lens[b] - L + l on
+ *              every axis.
+ *   q, k, v    bf16 rows at q_stride / k_stride / v_stride (multiples of 8; 0 = contiguous), 16-byte aligned, heads
+ *              contiguous: views of a fused projection's output serve.  q_out, k_out likewise; they may be q or k themselves
+ *              (same stride); other overlaps are not allowed.  q and q_out go together; k_out may be NULL with a cache.
+ *   weights    [head_dim] bf16 or fp32 (weight_f32 != 0), 16-byte aligned, or NULL: no norm.
+ * Without a cache (NULL): T rows, v is not used, q or k may be NULL.  With one: T = n_seqs * L rows, k and v are given, and
+ * the rotated keys and the values go to the places of moe_kv_append, in the cache's format: its codes are those of the fp32
+ * keys (one rounding; moe_kv_append after a rotation in bf16 rounds twice).  head_dim is 64 or 128; n_kv_heads is the cache's.
+ * Errors: MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_CUDA.
+ */
+enum { MOE_ROPE_HALF = 0, MOE_ROPE_ADJACENT = 1 };
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  void* k_out;
+  const void* q_weight;
+  const void* k_weight;
+  const uint64_t* turns;
+  const uint8_t* axis;
+  const int32_t* positions;
+  int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride, position_stride;
+  int32_t T, L; /* T: rows, without a cache; L: new tokens a request, with one */
+  int32_t n_q_heads, n_kv_heads, head_dim, rot_dim, pairs, n_axes;
+  int32_t weight_f32;
+  float eps;
+} moe_head_rope_t;
+
+MOE_API moe_status_t moe_head_norm_rope(const moe_kv_cache_t* cache, const moe_head_rope_t* args, moe_stream_t stream);
+
+/*
+ * The pages of caches that share one block table (the layers of a model), managed on the device.
+ *   block_table  int32 [n_seqs][max_pages], seq_lens int32 [n_seqs]: as in moe_kv_cache_t.
+ *   page_refs    int32 [n_pages]: how many requests hold a page (0: free).
+ *   status       device int32 or NULL: sticky bits as in moe_kv_cache_t, and MOE_POOL_EXHAUSTED (a growth that the free
+ *                pages do not cover, which is not made) and MOE_POOL_BAD_REQUEST (a fork that is not allowed, not made).
+ * n_seqs up to MOE_POOL_MAX_SEQS.  The calls change the tables in place, asynchronously, by rules on their contents alone:
+ * the same tables give the same pages.  A page index outside [0, n_pages) in a used entry is reported and left alone.
+ *
+ * moe_pages_fork: request dst[i] becomes a branch of request src[i]: it holds the same pages (their counts grow) and has the
+ *   same length, as it stood before the call.  dst[i] must have length 0, and only the first of several pairs with the
+ *   same dst counts.  src, dst: device int32 [n], n <= n_seqs.
+ * moe_pages_resize: every request b gets length new_lens[b] (device int32 [n_seqs]).  Shrinking gives the pages behind the
+ *   new length back (length 0: all); growing takes free pages.  A request that grows inside a partly filled page that
+ *   others hold too takes a page of its own for it: copies[b] (device int32 [n_seqs][2]) is then (old page, new page), and
+ *   (-1, -1) otherwise.  First all requests give pages back; then the pages that are wanted, in the order of the requests
+ *   (the copy's page first), are the free ones in the order of their indexes.  A request that wants pages beyond the last
+ *   free one keeps its length; a new length outside [0, max_pages * page_size] is reported and not taken.  Pages that only
+ *   become free because their last holders took copies are not handed out in the same call.
+ * moe_pages_compact: the live page of the highest index moves to the free page of the lowest, the next highest to the next
+ *   lowest, and so on while that is lower, at most `capacity` pages; copies[i] (device int32 [capacity][2]) is (from, to) of
+ *   move i, (-1, -1) behind the last.
+ * Entries of the block table behind a request's length are -1 where the calls gave their pages back.
+ *
+ * moe_copy_pages: in each of n_caches caches, page copies[i][1] receives the contents of page copies[i][0], for i < n; pairs
+ *   whose first page is negative are skipped.  All pairs are read and written in no order: no page may be the
+ *   second of two pairs, or the second of one and the first of another (the calls above make no such pairs).  An index outside
+ *   the cache is reported in its status and skipped.  Run it before the next append into the pages.
+ */
+enum { MOE_POOL_EXHAUSTED = 4, MOE_POOL_BAD_REQUEST = 8 };
+#define MOE_POOL_MAX_SEQS 8192
+typedef struct {
+  int32_t* block_table;
+  int32_t* seq_lens;
+  int32_t* page_refs;
+  int32_t* status;
+  int32_t n_seqs, max_pages, n_pages, page_size;
+} moe_page_pool_t;
+
+MOE_API moe_status_t moe_pages_fork(const moe_page_pool_t* pool, const int32_t* src, const int32_t* dst, int32_t n,
+                                    moe_stream_t stream);
+MOE_API moe_status_t moe_pages_resize(const moe_page_pool_t* pool, const int32_t* new_lens, int32_t* copies,
+                                      moe_stream_t stream);
+MOE_API moe_status_t moe_pages_compact(const moe_page_pool_t* pool, int32_t* copies, int32_t capacity, moe_stream_t stream);
+MOE_API moe_status_t moe_copy_pages(const moe_kv_cache_t* const* caches, int32_t n_caches, const int32_t* copies, int32_t n,
+                                    moe_stream_t stream);
 
 /*
  * moe_forward for a batch of at most MOE_FEW_MAX_T rows, in one kernel: the same routing, MXFP8 activations,
