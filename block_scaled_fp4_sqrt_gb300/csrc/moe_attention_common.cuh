@@ -1,8 +1,8 @@
 // What the forms of the paged attention share: the call's parameters, the dealing of the work to the blocks, copies into
 // shared memory and the matrix instructions.
 //
-// A unit is (request, kv head, row tile).  Every unit is cut into tiles of 64 tokens; the tiles of all units, in order and
-// with kUnitCost places in front of each unit's first, are dealt to the grid in equal contiguous runs of places, computed by
+// A unit is (request, kv head, row tile).  Every unit is cut into tiles of TILE tokens; the tiles of all units, in order and
+// with COST places in front of each unit's first, are dealt to the grid in equal contiguous runs of places, computed by
 // every block from the lengths alone.
 #pragma once
 
@@ -17,6 +17,7 @@ struct AttnParams {
   float* lse;
   int64_t q_stride, out_stride;
   int L, group, rows, row_tiles, Hq;  // rows = L * group
+  int lanes;  // MXFP4: kv heads that as many blocks read side by side
   uint32_t page_units, row_units, head_units;  // the cache's strides in 16-byte units
   float scale_log2;                   // scale * log2(e)
   PageDiv pd;
@@ -28,15 +29,9 @@ struct AttnParams {
 
 namespace {
 
-constexpr int kTile = 64;      // tokens of a tile
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kWarpTok = kTile / kWarps;  // tokens of a tile that a warp fetches and scores
 constexpr int kJoin = 16;                 // parts that are joined in one step
-// What beginning and ending a unit costs, in tiles, when the work is dealt.  64 requests of 100 to 8000 tokens, us at a
-// cost of 0 / 2 / 4 / 7: 8 rows MXFP8 145 / 107 / 105 / 114, 8 rows bf16 117 / 93 / 93 / 95; 200 requests of up to 1500
-// tokens 17.8 / 13.9 / 14.6 / 16.0; long requests do not depend on it.
-constexpr int kUnitCost = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -117,16 +112,28 @@ struct Run {
   int64_t t0, t1, per, pos;
 };
 
-__device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kTile - 1) / kTile : 1; }
+template <int TILE>
+__device__ __forceinline__ int tiles_of(int len) {
+  return len > 0 ? (len + TILE - 1) / TILE : 1;
+}
 
-// This block's run; false where it has no tile.  All threads of the block call it.
-__device__ __forceinline__ bool deal_run(const AttnParams& p, int tid, Run& run) {
-  __shared__ int s_b;
+// a / b for a >= 0, b > 0 (a 64-bit division takes some hundred cycles).
+__device__ __forceinline__ int64_t places_div(int64_t a, int b) {
+  return a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
+// The run of block `index` of `blocks` over the tiles of `heads` kv heads of every request; false where it has no tile.
+// All threads of the block call it.
+template <int TILE, int COST>
+__device__ __forceinline__ bool deal_run(const AttnParams& p, int heads, int blocks, int index, int tid, Run& run) {
+  __shared__ int s_b, s_len;
   __shared__ int64_t s_part[kWarps], s_first;
   const int warp = tid >> 5, lane = tid & 31;
-  const int B = p.c.n_seqs, H = p.c.n_kv_heads, HR = H * p.row_tiles;
+  const int B = p.c.n_seqs, HR = heads * p.row_tiles;
+  const int len0 = tid < B ? seq_len_of(p.c, tid) : 0;  // of the first kThreads requests: read once
+  auto places = [&](int b) { return tiles_of<TILE>(b == tid ? len0 : seq_len_of(p.c, b)) + COST; };
   int64_t sum = 0;
-  for (int b = tid; b < B; b += kThreads) sum += tiles_of(seq_len_of(p.c, b)) + kUnitCost;
+  for (int b = tid; b < B; b += kThreads) sum += places(b);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
   if (lane == 0) s_part[warp] = sum;
@@ -135,16 +142,16 @@ __device__ __forceinline__ bool deal_run(const AttnParams& p, int tid, Run& run)
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) total += s_part[i];
   total *= HR;
-  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  const int64_t t0 = per * blockIdx.x, t1 = t0 + per < total ? t0 + per : total;
+  const int64_t per = places_div(total + blocks - 1, blocks);
+  const int64_t t0 = per * index, t1 = t0 + per < total ? t0 + per : total;
   if (t0 >= t1) return false;
   Cursor cur;
   {
-    const int64_t want = t0 / HR;  // in places of one unit per request
+    const int64_t want = places_div(t0, HR);  // in places of one unit per request
     int64_t carry = 0;
     for (int b0 = 0; b0 < B; b0 += kThreads) {
       const int b = b0 + tid;
-      const int n = b < B ? tiles_of(seq_len_of(p.c, b)) + kUnitCost : 0;
+      const int n = b < B ? places(b) : 0;
       int64_t incl = n;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -162,17 +169,18 @@ __device__ __forceinline__ bool deal_run(const AttnParams& p, int tid, Run& run)
       }
       if (n > 0 && before + incl - n <= want && want < before + incl) {
         s_b = b;
+        s_len = b == tid ? len0 : seq_len_of(p.c, b);
         s_first = before + incl - n;
       }
       __syncthreads();
       if (want < carry) break;
     }
     cur.b = s_b;
-    cur.len = seq_len_of(p.c, cur.b);
-    cur.nt = tiles_of(cur.len);
+    cur.len = s_len;
+    cur.nt = tiles_of<TILE>(cur.len);
     const int64_t off = t0 - s_first * HR;
-    const int w = (int)(off / (cur.nt + kUnitCost));
-    cur.t = (int)(off - (int64_t)w * (cur.nt + kUnitCost)) - kUnitCost;
+    const int w = (int)places_div(off, cur.nt + COST);
+    cur.t = (int)(off - (int64_t)w * (cur.nt + COST)) - COST;
     cur.head = w / p.row_tiles;
     cur.rt = w - cur.head * p.row_tiles;
   }
@@ -186,18 +194,19 @@ __device__ __forceinline__ bool deal_run(const AttnParams& p, int tid, Run& run)
 }
 
 // To the next tile; returns how many places further it lies.
-__device__ __forceinline__ int advance_tile(const AttnParams& p, Cursor& c) {
+template <int TILE, int COST>
+__device__ __forceinline__ int advance_tile(const AttnParams& p, int heads, Cursor& c) {
   if (++c.t < c.nt) return 1;
   c.t = 0;
-  if (++c.rt < p.row_tiles) return 1 + kUnitCost;
+  if (++c.rt < p.row_tiles) return 1 + COST;
   c.rt = 0;
-  if (++c.head < p.c.n_kv_heads) return 1 + kUnitCost;
+  if (++c.head < heads) return 1 + COST;
   c.head = 0;
   if (++c.b < p.c.n_seqs) {
     c.len = seq_len_of(p.c, c.b);
-    c.nt = tiles_of(c.len);
+    c.nt = tiles_of<TILE>(c.len);
   }
-  return 1 + kUnitCost;
+  return 1 + COST;
 }
 
 }  // namespace

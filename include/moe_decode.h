@@ -69,12 +69,13 @@ MOE_API moe_status_t moe_add_rms_norm(const moe_norm_t* args, moe_stream_t strea
  *   seq_lens     int32 [n_seqs]: tokens of every request, the step's L new ones included; may be 0.
  *   status       device int32 or NULL: sticky error bits (MOE_KV_BAD_LENGTH: a length below 0 or above
  *                max_pages * page_size, used as 0 or as that bound; MOE_KV_BAD_PAGE: a page outside
- *                [0, n_pages), which is not accessed: its request's result is not meaningful).
+ *                [0, n_pages), which is not accessed: its request's result is not meaningful; MOE_KV_TIMEOUT: a wait
+ *                inside a kernel ran out of its two seconds, and the call's results are not meaningful).
  *   head_dim     64 or 128; page_size >= 1; n_kv_heads >= 1.
  * Pages may be shared by requests as long as no call writes to them.
  */
 enum { MOE_KV_BF16 = 0, MOE_KV_MXFP8 = 1, MOE_KV_MXFP4 = 4 };
-enum { MOE_KV_BAD_LENGTH = 1, MOE_KV_BAD_PAGE = 2 };
+enum { MOE_KV_BAD_LENGTH = 1, MOE_KV_BAD_PAGE = 2, MOE_KV_TIMEOUT = 16 };
 typedef struct {
   void* k;
   void* v;
