@@ -37,35 +37,25 @@ constexpr float kGrow4 = 14.f; // and the one at which it moves
 constexpr int kVUp = 5;        // values are held times 2^kVUp
 // scale bytes at which fp16 holds every code times its scale exactly: half of 2^-23 is its smallest number, 6 2^13 below its
 // largest
-constexpr uint32_t kKLow = 127 - 23, kKHigh = 127 + 13, kVLow = kKLow - kVUp, kVHigh = kKHigh - kVUp;
+constexpr uint32_t kVLow = 127 - 23 - kVUp, kVHigh = 127 + 13 - kVUp;
 
 // RT: rows of a row tile, in eights.
 template <int D, int RT>
 struct Cfg4 {
   static constexpr int kRows = 8 * RT;
-  #ifndef V_TOK1
-#define V_TOK1 32
-#define V_STEP1 32
-#define V_BLK1 3
-#define V_TOK2 32
-#define V_STEP2 32
-#define V_BLK2 2
-#define V_TOK4 32
-#define V_MAXS 6
-#endif
-  static constexpr int kTok = RT == 1 ? V_TOK1 : RT == 2 ? V_TOK2 : V_TOK4;  // tokens of a tile that a warp fetches
-  static constexpr int kStep = RT == 1 ? V_STEP1 : RT == 2 ? V_STEP2 : 16;   // .. and works on at once
+    // Tokens of a tile that a warp fetches, and works on at once.  Us for 64 requests, one and eight rows a head: 32 and 32
+  // tokens 44 (16 and 16: 54, with a fourth block 52), 32 and 16 tokens 91 (16 and 16: 104).
+  static constexpr int kTok = 32;
+  static constexpr int kStep = RT <= 2 ? 32 : 16;
   static constexpr int kTile = kWarps * kTok;
   // what beginning and ending a unit costs when the work is dealt, in tiles
   static constexpr int kCost = RT == 1 ? 2 : 3;
   static constexpr int kRowBytes = D / 2;  // one token of one head
   static constexpr int kBlk = D / 32;      // MX blocks of a row
   static constexpr int kPart = kTok * kRowBytes;  // K (or V) of a warp's tokens
-  // a warp's stage: K, V, the scales of K as fp16 pairs [token][block], of V in fp16 times 2^kVUp [block][place], and the
-  // scale bytes of K and of V
+  // a warp's stage: K, V, the scales of K in fp32 [token][block], of V in fp16 times 2^kVUp [block][place], and V's bytes
   static constexpr int kKs = 2 * kPart, kVs = kKs + kTok * kBlk * 4, kVb = kVs + kTok * kBlk * 2;
-  static constexpr int kKb = kVb + kTok * kBlk;
-  static constexpr int kWarpStage = (kKb + kTok * kBlk + 127) / 128 * 128;
+  static constexpr int kWarpStage = (kVb + kTok * kBlk + 127) / 128 * 128;
   static constexpr int kQPitch = 2 * D + 16;
   static constexpr int kQBytes = kRows * kQPitch;
   // the warps' sums at a unit's end, of kORound pairs of columns a warp of eight rows at a time; two buffers, where there is
@@ -75,11 +65,11 @@ struct Cfg4 {
   static constexpr int kOBuffers = RT > 1 ? 2 : 1;
   static constexpr int kOBytes = kOBuffers * kOPart;
   static constexpr int kStatBytes = (3 * kWarps + 1) * kRows * 4;
-  static constexpr int kBlocks = RT == 1 ? V_BLK1 : RT == 2 ? V_BLK2 : 2;
-  static constexpr bool kFarLoader = RT >= 3 && D == 128;  // the accumulators leave no registers for the loader's state
-  static constexpr int kBudget = (kBlocks == 2 ? 113 : kBlocks == 3 ? 75 : 56) * 1024 - (kFarLoader ? (48 + 8 * RT) * kThreads : 0) - 512 - kQBytes - kOBytes - kStatBytes - 256;
+  static constexpr int kBlocks = RT == 1 ? 3 : 2;  // an SM
+  static constexpr bool kFar = RT >= 3 && D == 128;  // the accumulators leave no registers for the loader's state
+  static constexpr int kBudget = (kBlocks == 2 ? 113 : 75) * 1024 - (kFar ? (48 + 8 * RT) * kThreads : 0) - 512 - kQBytes - kOBytes - kStatBytes - 256;
   static constexpr int kFit = kBudget / (kWarps * kWarpStage);
-  static constexpr int kStages = kFit > V_MAXS ? V_MAXS : kFit;
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr int kSmem = kWarps * kStages * kWarpStage + kQBytes + kOBytes + kStatBytes + 256;
   static constexpr bool kQRegs = RT == 1;  // q fragments stay in registers, or are read for every step
   static_assert(kStages >= 3, "scales are stored one load after their codes, and a warp barrier passed, before they are read");
@@ -208,9 +198,9 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
   __shared__ int s_last;
   __shared__ int3 s_unit;
   __shared__ int2 s_row[C::kRows];  // a row's token (request, new token) of the call and its query head; token -1: no such row
-  __shared__ uint4 s_loader[C::kFarLoader ? 3 * kThreads : 1];
-  __shared__ float2 s_sums[C::kFarLoader ? RT * kThreads : 1];
-  __shared__ uint32_t s_odd[kWarps][C::kStages];  // tokens with a scale that fp16 does not hold
+  __shared__ uint4 s_loader[C::kFar ? 3 * kThreads : 1];
+  __shared__ float2 s_sums[C::kFar ? RT * kThreads : 1];
+  __shared__ uint32_t s_odd[kWarps][C::kStages];  // tokens whose V has a scale that fp16 does not hold
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int li = lane >> 2, lc = lane & 3;
@@ -312,36 +302,29 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
     bool odd = false;
     if (lane < kTok) {
       const uint32_t v_at = at + C::kVs + ((lane & ~7) + place_of<D>(lane & 7)) * 2;
-      uint32_t k_pair[kBlk];
+      const uint32_t k0 = e8m0_bf16x2(ks_bytes, false);
 #pragma unroll
       for (int b = 0; b < kBlk; b += 2) {
-        const uint32_t ks = e8m0_bf16x2(ks_bytes, b == 2), vs = e8m0_bf16x2(vs_bytes, b == 2);
-        uint32_t kh = pack_f16(__uint_as_float(ks << 16), __uint_as_float(ks & 0xFFFF0000u));
+        const uint32_t vs = e8m0_bf16x2(vs_bytes, b == 2), vb = __byte_perm(vs_bytes, 0, b == 2 ? 0x4342 : 0x4140);
         uint32_t vh = pack_f16(__uint_as_float(vs << 16) * (float)(1 << kVUp),
                                __uint_as_float(vs & 0xFFFF0000u) * (float)(1 << kVUp));
-        const uint32_t kb = __byte_perm(ks_bytes, 0, b == 2 ? 0x4342 : 0x4140), vb = __byte_perm(vs_bytes, 0, b == 2 ? 0x4342 : 0x4140);
-        if (kb != __vminu2(__vmaxu2(kb, kKLow * 0x10001u), kKHigh * 0x10001u)) {
-          odd = true;
-          kh &= __vcmpleu2(kKLow * 0x10001u, kb) & __vcmpleu2(kb, kKHigh * 0x10001u);
-        }
         if (vb != __vminu2(__vmaxu2(vb, kVLow * 0x10001u), kVHigh * 0x10001u)) {
           odd = true;
           vh &= __vcmpleu2(kVLow * 0x10001u, vb) & __vcmpleu2(vb, kVHigh * 0x10001u);
         }
-        k_pair[b] = __byte_perm(kh, 0, 0x1010), k_pair[b + 1] = __byte_perm(kh, 0, 0x3232);
         sts16(v_at + b * kTok * 2, vh);
         sts16(v_at + (b + 1) * kTok * 2, vh >> 16);
       }
       if constexpr (D == 128) {
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + C::kKs + lane * 16), "r"(k_pair[0]), "r"(k_pair[1]),
-                     "r"(k_pair[2]), "r"(k_pair[3])
+        const uint32_t k1 = e8m0_bf16x2(ks_bytes, true);
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at + C::kKs + lane * 16), "r"(k0 << 16),
+                     "r"(k0 & 0xFFFF0000u), "r"(k1 << 16), "r"(k1 & 0xFFFF0000u)
                      : "memory");
         sts32(at + C::kVb + lane * 4, vs_bytes);
-        sts32(at + C::kKb + lane * 4, ks_bytes);
       } else {
-        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + C::kKs + lane * 8), "r"(k_pair[0]), "r"(k_pair[1]) : "memory");
+        asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(at + C::kKs + lane * 8), "r"(k0 << 16), "r"(k0 & 0xFFFF0000u)
+                     : "memory");
         sts16(at + C::kVb + lane * 2, vs_bytes);
-        sts16(at + C::kKb + lane * 2, ks_bytes);
       }
     }
     const uint32_t any = __ballot_sync(0xFFFFFFFFu, odd);
@@ -350,11 +333,11 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
   // Fills a stage with the next tile.
   auto load_stage = [&](int stage) {
     Loader far;
-    if constexpr (C::kFarLoader) {
+    if constexpr (C::kFar) {
 #pragma unroll
       for (int i = 0; i < 3; ++i) far.w[i] = s_loader[i * kThreads + tid];
     }
-    Loader& x = C::kFarLoader ? far : keep;
+    Loader& x = C::kFar ? far : keep;
     store_scales(stage == 0 ? C::kStages - 1 : stage - 1, x.k_old, x.v_old);
     if (x.any) {
       const uint32_t dst0 = ring + stage * C::kWarpStage;
@@ -379,14 +362,14 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
     }
     cp_async_commit();
     look_ahead(x);
-    if constexpr (C::kFarLoader) {
+    if constexpr (C::kFar) {
 #pragma unroll
       for (int i = 0; i < 3; ++i) s_loader[i * kThreads + tid] = far.w[i];
     }
   };
   lookup(keep);
   look_ahead(keep);
-  if constexpr (C::kFarLoader) {
+  if constexpr (C::kFar) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) s_loader[i * kThreads + tid] = keep.w[i];
   }
@@ -398,10 +381,10 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
   float o[RT][kPairs][4];
   // This lane's sums of p, in registers or (many accumulators) in shared memory.
   struct Sums {
-    float2 in_reg[C::kFarLoader ? 1 : RT];
+    float2 in_reg[C::kFar ? 1 : RT];
     float2* far;
-    __device__ __forceinline__ float2 get(int a) const { return C::kFarLoader ? far[a * kThreads] : in_reg[a]; }
-    __device__ __forceinline__ void set(int a, float2 v) { (C::kFarLoader ? far[a * kThreads] : in_reg[a]) = v; }
+    __device__ __forceinline__ float2 get(int a) const { return C::kFar ? far[a * kThreads] : in_reg[a]; }
+    __device__ __forceinline__ void set(int a, float2 v) { (C::kFar ? far[a * kThreads] : in_reg[a]) = v; }
   } l;
   l.far = s_sums + tid;
   uint32_t unseen;           // rows (bit 2 a + e) that have not met a score yet: their reference is 0
@@ -498,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
       uint32_t kf[2][kBlk];
-      uint32_t sc[2][kBlk];
+      float sc[2][kBlk];
       if constexpr (D == 128) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) ldsm4(kb + (16 * k + 8 * j) * C::kRowBytes, kf[j]);
@@ -511,74 +494,38 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
       for (int j = 0; j < 2; ++j) {
         const uint32_t at = ksb + (16 * k + 8 * j) * kBlk * 4;
         if constexpr (D == 128) {
-          asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(sc[j][0]), "=r"(sc[j][1]), "=r"(sc[j][2]), "=r"(sc[j][3])
+          asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                       : "=f"(sc[j][0]), "=f"(sc[j][1]), "=f"(sc[j][2]), "=f"(sc[j][3])
                        : "r"(at)
                        : "memory");
         } else {
-          const uint2 w = lds64(at);
-          sc[j][0] = w.x, sc[j][1] = w.y;
+          asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(sc[j][0]), "=f"(sc[j][1]) : "r"(at) : "memory");
         }
       }
 #pragma unroll
       for (int b = 0; b < kBlk; ++b) {
-        auto key = [&](auto i, int j) { return mul_f16x2(e2m1_f16<decltype(i)::value>(kf[j][b]), sc[j][b]); };
-        const std::integral_constant<int, 0> i0;
-        const std::integral_constant<int, 1> i1;
-        const std::integral_constant<int, 2> i2;
-        const std::integral_constant<int, 3> i3;
-        const uint32_t a0[4] = {key(i0, 0), key(i0, 1), key(i1, 0), key(i1, 1)};
-        const uint32_t a1[4] = {key(i2, 0), key(i2, 1), key(i3, 0), key(i3, 1)};
-        uint32_t q[RT][4];
+        const uint32_t a0[4] = {e2m1_f16<0>(kf[0][b]), e2m1_f16<0>(kf[1][b]), e2m1_f16<1>(kf[0][b]), e2m1_f16<1>(kf[1][b])};
+        const uint32_t a1[4] = {e2m1_f16<2>(kf[0][b]), e2m1_f16<2>(kf[1][b]), e2m1_f16<3>(kf[0][b]), e2m1_f16<3>(kf[1][b])};
 #pragma unroll
         for (int a = 0; a < RT; ++a) {
+          uint32_t q[4];
           if constexpr (C::kQRegs) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) q[a][i] = qb[a][b][i];
+            for (int i = 0; i < 4; ++i) q[i] = qb[a][b][i];
           } else {
-            q_frag(a, b, q[a]);
+            q_frag(a, b, q);
           }
-          if (b == 0)
-            mma_f16_zero(s[a][k], a0, q[a][0], q[a][1]);
-          else
-            mma_f16(s[a][k], a0, q[a][0], q[a][1]);
+          float d[4];
+          mma_f16_zero(d, a0, q[0], q[1]);
+          mma_f16(d, a1, q[2], q[3]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (b == 0)
+              s[a][k][2 * j] = d[2 * j] * sc[j][b], s[a][k][2 * j + 1] = d[2 * j + 1] * sc[j][b];
+            else
+              fma2(s[a][k][2 * j], s[a][k][2 * j + 1], d[2 * j], d[2 * j + 1], sc[j][b], sc[j][b]);
+          }
         }
-#pragma unroll
-        for (int a = 0; a < RT; ++a) mma_f16(s[a][k], a1, q[a][2], q[a][3]);
-      }
-    }
-  };
-  // .. and what the blocks add whose scales fp16 does not hold (their multipliers are 0): tokens `odd` of the stage, in fp32
-  auto add_odd_keys = [&](uint32_t stage_at, int first, uint32_t odd) {
-    for (; odd; odd &= odd - 1u) {
-      const int t = __ffs(odd) - 1;
-      if ((t & 7) != token_at<D>(li)) continue;  // another lane's
-      for (int b = 0; b < kBlk; ++b) {
-        const uint32_t byte = lds8(stage_at + C::kKb + t * kBlk + b);
-        if (byte - kKLow <= kKHigh - kKLow) continue;
-        const float sc = e8m0_float(byte, 0);
-#pragma unroll
-        for (int a = 0; a < RT; ++a)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float sum = 0.f;
-            for (int i = 0; i < 4; ++i) {  // words of eight columns
-              const uint32_t w = lds32(stage_at + chunk_at<D>(t, b) + i * 4);
-#pragma unroll
-              for (int c = 0; c < 8; c += 2) {
-                const uint32_t q2 = lds32(smem_addr(s_q) + (8 * a + 2 * lc + e) * C::kQPitch + b * 64 + i * 4 + c * 8);
-                const __half2 q = *reinterpret_cast<const __half2*>(&q2);
-                sum = fmaf(__low2float(q), e2m1_value(w >> (4 * c)), sum);
-                sum = fmaf(__high2float(q), e2m1_value(w >> (4 * c + 4)), sum);
-              }
-            }
-            // (a block of zeros has the byte 0 and adds nothing)
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                if (first + 16 * k + 8 * j == (t & ~7)) s[a][k][2 * j + e] = fmaf(sum, sc, s[a][k][2 * j + e]);
-          }
       }
     }
   };
@@ -955,7 +902,6 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
         if (cur.t * kTile + tok_first + first >= seen_end) break;
         const uint32_t odd_here = odd >> first << first & (uint32_t)((2ull << (first + C::kStep - 1)) - 1ull);
         scores(at, first);
-        if (odd_here) add_odd_keys(at, first, odd_here);
         relate(first);
         float top = s[0][0][0];
 #pragma unroll
@@ -1015,10 +961,7 @@ cudaError_t launch_rows(const AttnParams& p, int num_sms, cudaStream_t s) {
 }  // namespace
 
 // Rows of a row tile: the smallest multiple of 8 that holds the rows of a kv head, 32 above that.
-#ifndef V_TR
-#define V_TR 32
-#endif
-int attention_fp4_tile_rows(int64_t rows) { if (rows > V_TR) return V_TR; return rows >= 25 ? 32 : rows > 8 ? (int)((rows + 7) / 8 * 8) : 8; }
+int attention_fp4_tile_rows(int64_t rows) { return rows >= 25 ? 32 : rows > 8 ? (int)((rows + 7) / 8 * 8) : 8; }
 
 int attention_fp4_blocks(int head_dim, int tile_rows) {
   auto of = [&](auto d) {
