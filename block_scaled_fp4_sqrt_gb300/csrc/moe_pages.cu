@@ -15,11 +15,11 @@ namespace moe {
 namespace {
 
 constexpr int kCluster = 8;
-constexpr int kPoolThreads = 512;
+constexpr int kPoolThreads = 1024;
 constexpr int kPoolWarps = kPoolThreads / 32;
 
+// Every block's writes before it are read by all blocks after it (global memory past the L1 cache).
 __device__ __forceinline__ void cluster_meet() {
-  __threadfence();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ int cluster_rank() {
@@ -59,19 +59,49 @@ __device__ __forceinline__ int block_scan(int v, int& total) {
   return before + incl - v;
 }
 
-// A cluster's sum of v over its blocks before this one, and over all; s is an int of each block.  All threads call it.
-__device__ __forceinline__ int cluster_scan(int v, int* s, int rank, int& total) {
+// A cluster's sums of v over its blocks before this one, and over all; s holds v of each block and is used for one scan only (no
+// block may still read it when it changes, or leave before the others have: a later cluster_meet sees to that).  All threads
+// call it.
+__device__ __forceinline__ int2 cluster_scan(int2 v, int2* s, int rank, int2& total) {
   if (threadIdx.x == 0) *s = v;
   cluster_meet();
-  int before = 0;
-  total = 0;
+  int2 before = make_int2(0, 0);
+  total = make_int2(0, 0);
+#pragma unroll
   for (int i = 0; i < kCluster; ++i) {
-    const int x = cluster_read(s, i);
-    if (i < rank) before += x;
-    total += x;
+    const int2 x = make_int2(cluster_read(&s->x, i), cluster_read(&s->y, i));
+    if (i < rank) before.x += x.x, before.y += x.y;
+    total.x += x.x, total.y += x.y;
   }
-  cluster_meet();  // read by all before it changes, or its block leaves
   return before;
+}
+
+// f(i, page_refs[i]) for this block's part [lo, hi) of the pages, eight loads of a thread under way together.
+template <typename F>
+__device__ __forceinline__ void each_page(const moe_page_pool_t& p, int lo, int hi, F&& f) {
+  constexpr int kAhead = 8;
+  for (int i0 = lo + (int)threadIdx.x; i0 < hi; i0 += kAhead * kPoolThreads) {
+    int r[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) r[u] = i0 + u * kPoolThreads < hi ? __ldcg(p.page_refs + i0 + u * kPoolThreads) : 0;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (i0 + u * kPoolThreads < hi) f(i0 + u * kPoolThreads, r[u]);
+  }
+}
+
+// f(j, row[j]) for a warp's lanes over the entries j0 .. j1 of a request's row of the table, four loads of a lane together.
+template <typename F>
+__device__ __forceinline__ void each_entry(const int32_t* row, int j0, int j1, F&& f) {
+  constexpr int kAhead = 4;
+  for (int j = j0 + (int)(threadIdx.x & 31); j < j1; j += kAhead * 32) {
+    int e[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) e[u] = j + 32 * u < j1 ? __ldcg(row + j + 32 * u) : -1;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (j + 32 * u < j1) f(j + 32 * u, e[u]);
+  }
 }
 
 __device__ __forceinline__ int pages_of(int len, int page_size) { return len / page_size + (len % page_size != 0); }
@@ -103,10 +133,10 @@ __global__ void __launch_bounds__(kPoolThreads) pages_fork_kernel(const moe_page
     if ((unsigned)d < (unsigned)p.n_seqs) atomicMin(&s_claim[d], i);
   }
   __syncthreads();
-  // a warp of the cluster takes the pairs of its number; n <= MOE_POOL_MAX_SEQS = 64 a warp: lengths in two registers
+  // a warp of the cluster takes the pairs of its number; n <= MOE_POOL_MAX_SEQS, 32 a warp: lane k keeps the k-th's length
   constexpr int kWarpsAll = kCluster * kPoolWarps;
-  static_assert(MOE_POOL_MAX_SEQS <= 64 * kWarpsAll, "a warp remembers 64 pairs");
-  int kept[2] = {-1, -1};
+  static_assert(MOE_POOL_MAX_SEQS <= 32 * kWarpsAll, "a warp remembers 32 pairs");
+  int kept = -1;
   int k = 0;
   for (int i = rank * kPoolWarps + warp; i < n; i += kWarpsAll, ++k) {
     const int a = __ldg(src + i), d = __ldg(dst + i);
@@ -117,24 +147,24 @@ __global__ void __launch_bounds__(kPoolThreads) pages_fork_kernel(const moe_page
     }
     const int len = pool_len(p, a), np = pages_of(len, p.page_size);
     // (a source with pages is no branch of another pair: its row does not change here)
-    for (int j = lane; j < np; j += 32) {
-      const int page = __ldcg(p.block_table + (int64_t)a * p.max_pages + j);
-      p.block_table[(int64_t)d * p.max_pages + j] = page;
+    int32_t* to = p.block_table + (int64_t)d * p.max_pages;
+    each_entry(p.block_table + (int64_t)a * p.max_pages, 0, np, [&](int j, int page) {
+      to[j] = page;
       if (page_ok(p, page)) atomicAdd(p.page_refs + page, 1);
-    }
-    if ((k & 31) == lane) kept[k >> 5] = len;
+    });
+    if (k == lane) kept = len;
   }
   cluster_meet();  // every length has been read
   k = 0;
   for (int i = rank * kPoolWarps + warp; i < n; i += kWarpsAll, ++k)
-    if ((k & 31) == lane && kept[k >> 5] >= 0) p.seq_lens[__ldg(dst + i)] = kept[k >> 5];
+    if (k == lane && kept >= 0) p.seq_lens[__ldg(dst + i)] = kept;
 }
 
 // ---------------------------------------------------------------------------------------------- resize
 __global__ void __launch_bounds__(kPoolThreads) pages_resize_kernel(const moe_page_pool_t p, const int32_t* new_lens,
                                                                     int2* copies) {
   __shared__ int s_end[MOE_POOL_MAX_SEQS];  // pages wanted by the requests up to and with this one; sign bit: with a copy
-  __shared__ int s_sum;
+  __shared__ int2 s_sum;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = cluster_rank();
@@ -151,10 +181,10 @@ __global__ void __launch_bounds__(kPoolThreads) pages_resize_kernel(const moe_pa
     const int old = pool_len(p, b), now = target(b, old);
     if (lane == 0 && now != __ldg(new_lens + b)) set_status(p.status, MOE_KV_BAD_LENGTH);
     int32_t* row = p.block_table + (int64_t)b * p.max_pages;
-    for (int j = pages_of(now, P) + lane; j < pages_of(old, P); j += 32) {
-      if (page_ok(p, row[j])) atomicSub(p.page_refs + row[j], 1);
+    each_entry(row, pages_of(now, P), pages_of(old, P), [&](int j, int page) {
+      if (page_ok(p, page)) atomicSub(p.page_refs + page, 1);
       row[j] = -1;
-    }
+    });
   }
   cluster_meet();
 
@@ -182,13 +212,14 @@ __global__ void __launch_bounds__(kPoolThreads) pages_resize_kernel(const moe_pa
   __syncthreads();
 
   // the free pages of this block's part of the pool
-  const int per = ((p.n_pages + kCluster - 1) / kCluster + 3) / 4 * 4;
+  const int per = (p.n_pages + kCluster - 1) / kCluster;
   const int lo = min(p.n_pages, rank * per), hi = min(p.n_pages, lo + per);
-  int mine = 0;
-  for (int i = lo + tid; i < hi; i += kPoolThreads) mine += __ldcg(p.page_refs + i) == 0;
-  int in_block, n_free;
+  int mine = 0, in_block;
+  each_page(p, lo, hi, [&](int, int refs) { mine += refs == 0; });
   block_scan(mine, in_block);
-  int first = cluster_scan(in_block, &s_sum, rank, n_free);
+  int2 all;
+  int first = cluster_scan(make_int2(in_block, 0), &s_sum, rank, all).x;
+  const int n_free = all.x;
   // requests are served in order while the free pages last, and those that want none
   auto end_of = [&](int b) { return s_end[b] & 0x7FFFFFFF; };
   auto start_of = [&](int b) { return b ? end_of(b - 1) : 0; };
@@ -232,31 +263,33 @@ __global__ void __launch_bounds__(kPoolThreads) pages_resize_kernel(const moe_pa
 
 // ---------------------------------------------------------------------------------------------- compact
 __global__ void __launch_bounds__(kPoolThreads) pages_compact_kernel(const moe_page_pool_t p, int2* copies, int capacity) {
-  __shared__ int s_sum;
+  __shared__ int2 s_live, s_moves;
   pdl_trigger();
   pdl_wait();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, rank = cluster_rank();
+  const int tid = threadIdx.x, warp = tid >> 5, rank = cluster_rank();
   const int per = (p.n_pages + kCluster - 1) / kCluster;
   const int lo = min(p.n_pages, rank * per), hi = min(p.n_pages, lo + per);
-  int mine = 0, total, n_live, n_moves;
-  for (int i = lo + tid; i < hi; i += kPoolThreads) mine += __ldcg(p.page_refs + i) != 0;
-  block_scan(mine, total);
-  const int live_before = cluster_scan(total, &s_sum, rank, n_live);
-  (void)live_before;
+  int live = 0, total;
+  int2 all;
+  each_page(p, lo, hi, [&](int, int refs) { live += refs != 0; });
+  block_scan(live, total);
+  cluster_scan(make_int2(total, 0), &s_live, rank, all);
+  const int n_live = all.x;
   // live pages from n_live on move into the free ones below: there are as many of the one as of the other
-  auto is_hole = [&](int i) { return i < n_live && __ldcg(p.page_refs + i) == 0; };
-  auto is_mover = [&](int i) { return i >= n_live && __ldcg(p.page_refs + i) != 0; };
-  int holes = 0, movers = 0;
-  for (int i = lo + tid; i < hi; i += kPoolThreads) holes += is_hole(i), movers += is_mover(i);
+  auto is_hole = [&](int i, int refs) { return i < n_live && refs == 0; };
+  auto is_mover = [&](int i, int refs) { return i >= n_live && refs != 0; };
+  int holes = 0, movers = 0, total_movers;
+  each_page(p, lo, hi, [&](int i, int refs) { holes += is_hole(i, refs), movers += is_mover(i, refs); });
   block_scan(holes, total);
-  int hole = cluster_scan(total, &s_sum, rank, n_moves);
-  block_scan(movers, total);
-  int mover = cluster_scan(total, &s_sum, rank, n_moves);
+  block_scan(movers, total_movers);
+  const int2 before = cluster_scan(make_int2(total, total_movers), &s_moves, rank, all);
+  const int n_moves = all.x;
+  int hole = before.x, mover = before.y;
   const int moves = min(n_moves, capacity);
   int32_t* flat = reinterpret_cast<int32_t*>(copies);
   for (int i0 = lo; i0 < hi; i0 += kPoolThreads) {
-    const int i = i0 + tid;
-    const bool h = i < hi && is_hole(i), m = i < hi && is_mover(i);
+    const int i = i0 + tid, refs = i < hi ? __ldcg(p.page_refs + i) : 0;
+    const bool h = i < hi && is_hole(i, refs), m = i < hi && is_mover(i, refs);
     const int rh = hole + block_scan(h, total);
     hole += total;
     const int rm = n_moves - 1 - (mover + block_scan(m, total));  // the highest mover is the first
@@ -277,12 +310,11 @@ __global__ void __launch_bounds__(kPoolThreads) pages_compact_kernel(const moe_p
   for (int b = rank * kPoolWarps + warp; b < p.n_seqs; b += kCluster * kPoolWarps) {
     int32_t* row = p.block_table + (int64_t)b * p.max_pages;
     const int np = pages_of(pool_len(p, b), p.page_size);
-    for (int j = lane; j < np; j += 32) {
-      const int page = row[j];
-      if (!page_ok(p, page)) continue;
+    each_entry(row, 0, np, [&](int j, int page) {
+      if (!page_ok(p, page)) return;
       const int to = -1 - __ldcg(p.page_refs + page);
       if (to >= 0 && to < n_live && page >= n_live) row[j] = to;
-    }
+    });
   }
   cluster_meet();
   for (int i = rank * kPoolThreads + tid; i < moves; i += kCluster * kPoolThreads) p.page_refs[__ldcg(copies + i).x] = 0;
@@ -321,7 +353,7 @@ struct CopyParams {
   int32_t n, n_tensors;
 };
 constexpr int kCopyThreads = 256;
-constexpr int kCopyUnroll = 4;
+constexpr int kCopyUnroll = 8;
 constexpr int kCopyItem = kCopyThreads * kCopyUnroll;  // words of an item
 
 template <typename W>
@@ -351,8 +383,10 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
     if (mine.x >= 0) s_pair[at] = mine;
     __syncthreads();
     const uint64_t all = (uint64_t)n * p.n_tensors * items;
+    const uint32_t per_pair = p.n_tensors * items;  // below 2^31
     for (; turn < all; turn += gridDim.x) {
-      const uint32_t pair = (uint32_t)(turn / (p.n_tensors * items)), rest = (uint32_t)(turn % (p.n_tensors * items));
+      const uint32_t pair = turn >> 32 ? (uint32_t)(turn / per_pair) : (uint32_t)turn / per_pair;
+      const uint32_t rest = (uint32_t)(turn - (uint64_t)pair * per_pair);
       const uint32_t ti = rest / items;
       const CopyTensor& t = p.t[ti];
       const int2 c = s_pair[pair];
@@ -369,8 +403,11 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
         const uint32_t w = (rest % items) * kCopyItem + k * kCopyThreads + tid;
         off[k] = -1;
         if (w < t.words) {
-          const uint32_t run = w / t.units, i2 = run % t.n2, i1 = run / t.n2;
-          off[k] = i1 * t.s1 + i2 * t.s2 + (w - run * t.units);
+          off[k] = w;
+          if (t.units != t.words) {  // a page in several runs
+            const uint32_t run = w / t.units, i2 = run % t.n2, i1 = run / t.n2;
+            off[k] = i1 * t.s1 + i2 * t.s2 + (w - run * t.units);
+          }
           v[k] = src[off[k]];
         }
       }

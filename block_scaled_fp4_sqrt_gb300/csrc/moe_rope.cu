@@ -2,12 +2,18 @@
 //
 //   x' = x w rsqrt(mean x^2 + eps);  y_i = x'_i cos a - x'_j sin a,  y_j = x'_i sin a + x'_j cos a,  a = position * frequency
 //
-// One pass: a row's heads are read once, each by D / 8 lanes with eight neighbouring columns a lane, and written once.
-// The angles are shared by all heads of a token, so a block takes a token and computes its rot_dim / 2 of them first.
-// A phase is position * turns modulo 2^64, an integer product: exact for every position, where an fp32 angle at position
-// 100,000 would be off by 2^-8 of a radian.
+// One pass: a head of a row is read once, by D / 8 lanes, and written once; memory-bound for prompts, latency-bound for a
+// step's few rows.
+//  * A lane keeps its columns for all heads of a chunk, so that a token's sines and cosines are computed once and stay in
+//    registers: no shared memory and no barrier.  Pairs (i, i + rot / 2) are held by one lane, as two groups of four columns
+//    half of rot_dim apart (8-byte loads, whole lines a head); only where rot_dim / 2 is no multiple of four (or, for a
+//    quantised cache, of an MX block) is the partner fetched through shared memory.
+//  * Few rows: a chunk is one head, and every group of lanes computes its own angles; a prompt: up to 16 heads.
+//  * A phase is position * turns modulo 2^64, an integer product: exact for every position, where an fp32 angle at position
+//    100,000 would be off by 2^-8 of a radian.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "moe_decode_device.cuh"
 
@@ -15,7 +21,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kMaxThreads = 512;
+constexpr int kBlock = 256;
+constexpr int kBatch = 4;     // heads whose loads are under way together
+constexpr int kMaxChunk = 16; // heads a group of lanes takes
 
 struct RopeParams {
   moe_kv_cache_t c;
@@ -26,27 +34,82 @@ struct RopeParams {
   const uint8_t* axis;
   const int32_t* pos;
   int64_t qs, ks, vs, qos, kos, ps;
-  int L, hq, hkv, rot, adjacent, w_f32, heads;  // heads: of q, k and (with a cache) v together
+  int rows, L, hq, hkv, rot, w_f32, heads, chunk;  // heads: of q, k and (with a cache) v together
   float eps;
-  PageDiv page;
+  PageDiv page, len;
 };
 
 constexpr int kNoCache = -1;
+// How a lane holds its eight columns: two groups of four half of rot_dim apart (the columns behind rot_dim: eight in a row);
+// eight in a row, pairs being neighbours; eight in a row, the partners with other lanes.
+enum Layout { kHalves, kNeighbours, kExchange };
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(kMaxThreads) head_norm_rope_kernel(const RopeParams p) {
+__device__ __forceinline__ uint2 ld8(const __nv_bfloat16* p) { return *reinterpret_cast<const uint2*>(p); }
+__device__ __forceinline__ void st8(__nv_bfloat16* p, uint2 v) { *reinterpret_cast<uint2*>(p) = v; }
+
+// Four columns of a weight.
+__device__ __forceinline__ void weight4(const void* w, int f32, int col, float* to) {
+  if (f32) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + col));
+    to[0] = a.x, to[1] = a.y, to[2] = a.z, to[3] = a.w;
+  } else {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + col));
+    to[0] = __uint_as_float(u.x << 16), to[1] = __uint_as_float(u.x & 0xFFFF0000u);
+    to[2] = __uint_as_float(u.y << 16), to[3] = __uint_as_float(u.y & 0xFFFF0000u);
+  }
+}
+
+template <int D, int FMT, Layout LAY>
+__global__ void __launch_bounds__(kBlock, 3) head_norm_rope_kernel(const RopeParams p) {
   constexpr int kLanes = D / 8;  // lanes of a head
-  __shared__ float2 s_cs[D / 2];
-  __shared__ float s_x[kMaxThreads / kLanes][D];
+  constexpr int kAngles = LAY == kExchange ? 8 : 4;
+  __shared__ float s_x[LAY == kExchange ? kBlock / kLanes : 1][D];
   pdl_trigger();
   pdl_wait();
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, i = tid & (kLanes - 1);
+  const int row = blockIdx.x * (kBlock / kLanes) + tid / kLanes;
+  if (row >= p.rows) return;
   const uint32_t group = (kLanes == 16 ? 0xFFFFu : 0xFFu) << (lane & ~(kLanes - 1));  // the head's lanes
-  const int col = (tid & (kLanes - 1)) * 8;
-  const int64_t row = blockIdx.x;
+  const int half = p.rot >> 1;
+  const bool turned = LAY != kHalves || i < p.rot / 8;  // (kHalves) this lane's columns are pairs
+  const int col0 = LAY != kHalves ? 8 * i : turned ? 4 * i : p.rot + 8 * (i - p.rot / 8);
+  const int col1 = LAY == kHalves && turned ? half + 4 * i : col0 + 4;
+
+  const int first = blockIdx.y * p.chunk, last = min(first + p.chunk, p.heads);
+  // The heads of a kind (0 q, 1 k, 2 v) are heads kind_at .. of the call's.
+  uint2 raw[kBatch][2];
+  auto load = [&](auto kind, int h0, int end, uint2 (&to)[kBatch][2]) {
+    constexpr int K = decltype(kind)::value;
+    const int kind_at = K == 0 ? 0 : K == 1 ? p.hq : p.hq + p.hkv;
+    const __nv_bfloat16* src = K == 0 ? p.q + row * p.qs : K == 1 ? p.k + row * p.ks : p.v + row * p.vs;
+    src += (int64_t)(h0 - kind_at) * D;
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n) {
+      if (h0 + n >= end) break;
+      if (LAY == kHalves && K < 2) {
+        to[n][0] = ld8(src + n * D + col0);
+        to[n][1] = ld8(src + n * D + col1);
+      } else {
+        const uint4 u = *reinterpret_cast<const uint4*>(src + n * D + 8 * i);
+        to[n][0] = make_uint2(u.x, u.y), to[n][1] = make_uint2(u.z, u.w);
+      }
+    }
+  };
+  const std::integral_constant<int, 0> q_heads;
+  const std::integral_constant<int, 1> k_heads;
+  const std::integral_constant<int, 2> v_heads;
+  // what follows does not wait for the first heads
+  if (first < p.hq)
+    load(q_heads, first, min(last, p.hq), raw);
+  else if (first < p.hq + p.hkv)
+    load(k_heads, first, min(last, p.hq + p.hkv), raw);
+  else
+    load(v_heads, first, last, raw);
+
   int pos = 0, page = -1, prow = 0;
   if (FMT != kNoCache) {
-    const int b = (int)(row / p.L), l = (int)(row - (int64_t)b * p.L);
+    int l;
+    const int b = page_of(row, p.len, p.L, &l);
     pos = seq_len_of(p.c, b) - p.L + l;
     if (pos >= 0) {
       const int j = page_of(pos, p.page, p.c.page_size, &prow);
@@ -57,114 +120,194 @@ __global__ void __launch_bounds__(kMaxThreads) head_norm_rope_kernel(const RopeP
       }
     }
   }
-  for (int i = tid; i < p.rot / 2; i += blockDim.x) {
-    const int at = p.pos ? __ldg(p.pos + (p.axis ? p.axis[i] : 0) * p.ps + row) : pos;
-    const uint64_t phase = (uint64_t)(int64_t)at * __ldg(p.turns + i);
-    // the upper 32 bits as a signed fraction of half a turn
-    float2 cs;
-    sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &cs.y, &cs.x);
-    s_cs[i] = cs;
-  }
-  __syncthreads();
-  float* x_row = s_x[tid / kLanes];
-  for (int u = tid / kLanes; u < p.heads; u += blockDim.x / kLanes) {
-    const bool is_q = u < p.hq, is_k = !is_q && u < p.hq + p.hkv;
-    const int head = is_q ? u : is_k ? u - p.hq : u - p.hq - p.hkv;
-    const __nv_bfloat16* src = is_q ? p.q + row * p.qs : is_k ? p.k + row * p.ks : p.v + row * p.vs;
-    const uint4 raw = *reinterpret_cast<const uint4*>(src + head * D + col);
-    float x[8];
-    bf16x8_to_f32(raw, x);
-    uint4 out = raw;
-    const void* w = is_q ? p.q_w : is_k ? p.k_w : nullptr;
-    if (is_q || is_k) {
-      if (w) {
-        float sq = 0.f;
+  // the lane's angles: of the pairs of its first group, of its four neighbouring pairs, or of every column
+  float cs[kAngles], sn[kAngles];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sq = fmaf(x[i], x[i], sq);
-#pragma unroll
-        for (int off = 1; off < kLanes; off <<= 1) sq += __shfl_xor_sync(group, sq, off);
-        const float inv = rsqrtf(fmaf(sq, 1.f / D, p.eps));
-        float wv[8];
-        if (p.w_f32) {
-          const float4* wp = reinterpret_cast<const float4*>(static_cast<const float*>(w) + col);
-          const float4 a = __ldg(wp), b = __ldg(wp + 1);
-          wv[0] = a.x, wv[1] = a.y, wv[2] = a.z, wv[3] = a.w, wv[4] = b.x, wv[5] = b.y, wv[6] = b.z, wv[7] = b.w;
-        } else {
-          bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + col)), wv);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * wv[i];
-      }
-      if (p.adjacent) {
-#pragma unroll
-        for (int i = 0; i < 8; i += 2)
-          if (col + i < p.rot) {
-            const float2 cs = s_cs[(col + i) >> 1];
-            const float a = x[i], b = x[i + 1];
-            x[i] = a * cs.x - b * cs.y;
-            x[i + 1] = a * cs.y + b * cs.x;
-          }
-      } else {
-        __syncwarp(group);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x_row[col + i] = x[i];
-        __syncwarp(group);
-        const int half = p.rot >> 1;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = col + i;
-          if (c < half) {
-            const float2 cs = s_cs[c];
-            x[i] = x[i] * cs.x - x_row[c + half] * cs.y;
-          } else if (c < p.rot) {
-            const float2 cs = s_cs[c - half];
-            x[i] = x_row[c - half] * cs.y + x[i] * cs.x;
-          }
-        }
-      }
-      if (w || p.rot) out = f32_to_bf16x8(x);  // what is not computed keeps its bits, those of a NaN too
-      if (is_q) *reinterpret_cast<uint4*>(p.q_out + row * p.qos + head * D + col) = out;
-      if (is_k && p.k_out) *reinterpret_cast<uint4*>(p.k_out + row * p.kos + head * D + col) = out;
+  for (int e = 0; e < kAngles; ++e) {
+    const int pair = LAY == kHalves ? 4 * i + e : LAY == kNeighbours ? 4 * i + e : (8 * i + e < half ? 8 * i + e : 8 * i + e - half);
+    cs[e] = 1.f, sn[e] = 0.f;
+    if (LAY == kExchange ? 8 * i + e < p.rot : pair < half) {
+      const int at = p.pos ? __ldg(p.pos + (p.axis ? __ldg(p.axis + pair) : 0) * p.ps + row) : pos;
+      const uint64_t phase = (uint64_t)(int64_t)at * __ldg(p.turns + pair);
+      // the upper 32 bits as a signed fraction of half a turn
+      sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &sn[e], &cs[e]);
     }
-    if (FMT != kNoCache && !is_q) {
-      const int64_t at = page * p.c.page_stride + prow * p.c.row_stride + head * p.c.head_stride + col;
-      void* codes = is_k ? p.c.k : p.c.v;
-      uint8_t* scales = is_k ? p.c.k_s : p.c.v_s;
+  }
+
+  // The heads h0 .. end of a kind, the first batch of which has been asked for where `loaded`: while one batch is worked on,
+  // the next is on its way.
+  auto heads = [&](auto kind, int h0, int end, bool loaded) {
+    constexpr int K = decltype(kind)::value;
+    const int kind_at = K == 0 ? 0 : K == 1 ? p.hq : p.hq + p.hkv;
+    const void* w = K == 0 ? p.q_w : K == 1 ? p.k_w : nullptr;
+    float wv[8];
+    if (w) {
+      weight4(w, p.w_f32, col0, wv);
+      weight4(w, p.w_f32, col1, wv + 4);
+    }
+    auto one = [&](int head, const uint2 (&r)[2]) {
+      float x[8];
+      bf16x8_to_f32(make_uint4(r[0].x, r[0].y, r[1].x, r[1].y), x);
+      uint4 out = make_uint4(r[0].x, r[0].y, r[1].x, r[1].y);
+      if constexpr (K < 2) {
+        if (w) {
+          float sq = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
+#pragma unroll
+          for (int off = 1; off < kLanes; off <<= 1) sq += __shfl_xor_sync(group, sq, off);
+          const float inv = rsqrtf(fmaf(sq, 1.f / D, p.eps));
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * wv[e];
+        }
+        if constexpr (LAY == kHalves) {
+          if (turned) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float a = x[e], b = x[4 + e];
+              x[e] = a * cs[e] - b * sn[e];
+              x[4 + e] = a * sn[e] + b * cs[e];
+            }
+          }
+        } else if constexpr (LAY == kNeighbours) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (8 * i + 2 * e < p.rot) {
+              const float a = x[2 * e], b = x[2 * e + 1];
+              x[2 * e] = a * cs[e] - b * sn[e];
+              x[2 * e + 1] = a * sn[e] + b * cs[e];
+            }
+        } else {
+          float* x_row = s_x[tid / kLanes];
+          __syncwarp(group);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x_row[8 * i + e] = x[e];
+          __syncwarp(group);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int c = 8 * i + e;
+            if (c < half)
+              x[e] = x[e] * cs[e] - x_row[c + half] * sn[e];
+            else if (c < p.rot)
+              x[e] = x_row[c - half] * sn[e] + x[e] * cs[e];
+          }
+        }
+        if (w || p.rot) out = f32_to_bf16x8(x);  // what is not computed keeps its bits, those of a NaN too
+        __nv_bfloat16* dst = K == 0 ? p.q_out + row * p.qos : p.k_out ? p.k_out + row * p.kos : nullptr;
+        if (dst) {
+          dst += (int64_t)head * D;
+          if (LAY == kHalves) {
+            st8(dst + col0, make_uint2(out.x, out.y));
+            st8(dst + col1, make_uint2(out.z, out.w));
+          } else {
+            *reinterpret_cast<uint4*>(dst + col0) = out;
+          }
+        }
+      }
+      if constexpr (FMT == kNoCache || K == 0) return;
+      const bool split = LAY == kHalves && K == 1;  // the columns lie in two groups
+      const int64_t at = page * p.c.page_stride + prow * p.c.row_stride + head * p.c.head_stride;
+      void* codes = K == 1 ? p.c.k : p.c.v;
+      [[maybe_unused]] uint8_t* scales = K == 1 ? p.c.k_s : p.c.v_s;
+      const int c0 = split ? col0 : 8 * i, c1 = split ? col1 : 8 * i + 4;
       if constexpr (FMT == MOE_KV_BF16) {
-        if (page >= 0) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(codes) + at) = out;
-      } else {
-        uint8_t scale;  // four neighbouring lanes hold a block
-        if constexpr (FMT == MOE_KV_MXFP8) {
-          float amax = 0.f;  // of the numbers: a NaN keeps its own code
-#pragma unroll
-          for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
-          amax = fmaxf(amax, __shfl_xor_sync(group, amax, 1));
-          amax = fmaxf(amax, __shfl_xor_sync(group, amax, 2));
-          const int e = mxfp8_block_exp(amax);
-          scale = (uint8_t)(e + 127);
-          if (page >= 0) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(codes) + at) = e4m3_8(x, exp2_neg_int(e));
-        } else {
-          uint32_t top = abs_max_bits(x);
-          top = max(top, __shfl_xor_sync(group, top, 1));
-          top = max(top, __shfl_xor_sync(group, top, 2));
-          uint32_t word;
-          scale = mxfp4_quad(x, top, word);
-          if (page >= 0) *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(codes) + (at >> 1)) = word;
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(codes) + at;
+        if (page >= 0) {
+          if (split) {
+            st8(dst + c0, make_uint2(out.x, out.y));
+            st8(dst + c1, make_uint2(out.z, out.w));
+          } else {
+            *reinterpret_cast<uint4*>(dst + c0) = out;
+          }
         }
-        if (page >= 0 && (lane & 3) == 0) scales[at >> 5] = scale;
+      } else {
+        // the largest magnitudes of the blocks of the two groups: pairs half of rot_dim apart lie in two blocks, each held by
+        // eight lanes; eight columns in a row in one, held by four
+        const bool two = split && turned;
+        uint32_t top[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (FMT == MOE_KV_MXFP8) {  // of the numbers: a NaN keeps its own code
+            float m = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(x[4 * g + e]));
+            top[g] = __float_as_uint(m);
+          } else {
+            top[g] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top[g] = max(top[g], __float_as_uint(x[4 * g + e]) & 0x7FFFFFFFu);
+          }
+        }
+        if (!two) top[0] = top[1] = max(top[0], top[1]);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          top[g] = max(top[g], __shfl_xor_sync(group, top[g], 1));
+          top[g] = max(top[g], __shfl_xor_sync(group, top[g], 2));
+          const uint32_t other = __shfl_xor_sync(group, top[g], 4);
+          if (two) top[g] = max(top[g], other);
+        }
+        const bool writes_scale = (i & (two ? 7 : 3)) == 0;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int64_t to = at + (g ? c1 : c0);
+          uint8_t scale;
+          if constexpr (FMT == MOE_KV_MXFP8) {
+            const int e = mxfp8_block_exp(__uint_as_float(top[g]));
+            const float mul = exp2_neg_int(e);
+            scale = (uint8_t)(e + 127);
+            const uint32_t w = (uint32_t)e4m3x2(x[4 * g] * mul, x[4 * g + 1] * mul) |
+                               ((uint32_t)e4m3x2(x[4 * g + 2] * mul, x[4 * g + 3] * mul) << 16);
+            if (page >= 0) *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(codes) + to) = w;
+          } else {
+            uint32_t w;
+            scale = mxfp4_quad({x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3], 0.f, 0.f, 0.f, 0.f}, top[g], w);
+            if (page >= 0) *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(codes) + (to >> 1)) = (uint16_t)w;
+          }
+          if (page >= 0 && writes_scale && (two || g == 0)) scales[to >> 5] = scale;
+        }
       }
+    };
+    if (!loaded) load(kind, h0, end, raw);
+    for (; h0 < end; h0 += kBatch) {
+      uint2 next[kBatch][2];
+      load(kind, h0 + kBatch, end, next);
+#pragma unroll
+      for (int n = 0; n < kBatch; ++n) {
+        if (h0 + n >= end) break;
+        one(h0 + n - kind_at, raw[n]);
+      }
+#pragma unroll
+      for (int n = 0; n < kBatch; ++n) raw[n][0] = next[n][0], raw[n][1] = next[n][1];
     }
-  }
+  };
+  if (first < p.hq) heads(q_heads, first, min(last, p.hq), true);
+  if (first < p.hq + p.hkv && last > p.hq) heads(k_heads, max(first, p.hq), min(last, p.hq + p.hkv), first >= p.hq);
+  if (FMT != kNoCache && last > p.hq + p.hkv) heads(v_heads, max(first, p.hq + p.hkv), last, first >= p.hq + p.hkv);
 }
 
 template <int D>
-cudaError_t launch(const RopeParams& p, int fmt, int64_t rows, cudaStream_t s) {
-  const int threads = std::min(kMaxThreads, (p.heads * (D / 8) + 31) / 32 * 32);
-  auto* kernel = fmt == MOE_KV_BF16    ? head_norm_rope_kernel<D, MOE_KV_BF16>
-                 : fmt == MOE_KV_MXFP8 ? head_norm_rope_kernel<D, MOE_KV_MXFP8>
-                 : fmt == MOE_KV_MXFP4 ? head_norm_rope_kernel<D, MOE_KV_MXFP4>
-                                       : head_norm_rope_kernel<D, kNoCache>;
-  return launch_pdl(kernel, dim3((unsigned)rows), dim3(threads), 0, s, p);
+cudaError_t launch(RopeParams p, int fmt, bool adjacent, int sms, cudaStream_t s) {
+  constexpr int kLanes = D / 8;
+  // Equal chunks of heads, the largest that leave 16 warps an SM: fewer and longer ones compute fewer angles (512 rows of 48
+  // heads: 8.2 us; with one head a chunk 11.3, with 8 warps an SM 11.3).
+  const int64_t warps = (int64_t)p.rows * p.heads * kLanes / 32;
+  const int chunk = (int)std::max<int64_t>(1, std::min<int64_t>({warps / ((int64_t)sms * 16), kMaxChunk, p.heads}));
+  const int chunks = (p.heads + chunk - 1) / chunk;
+  p.chunk = (p.heads + chunks - 1) / chunks;
+  const bool quantised = fmt == MOE_KV_MXFP8 || fmt == MOE_KV_MXFP4;
+  const Layout lay = adjacent ? kNeighbours : p.rot % (quantised ? 64 : 8) == 0 ? kHalves : kExchange;
+  const dim3 grid((p.rows + kBlock / kLanes - 1) / (kBlock / kLanes), (p.heads + p.chunk - 1) / p.chunk);
+  auto pick = [&](auto f) {
+    constexpr int FMT = decltype(f)::value;
+    return lay == kHalves       ? head_norm_rope_kernel<D, FMT, kHalves>
+           : lay == kNeighbours ? head_norm_rope_kernel<D, FMT, kNeighbours>
+                                : head_norm_rope_kernel<D, FMT, kExchange>;
+  };
+  auto* kernel = fmt == MOE_KV_BF16    ? pick(std::integral_constant<int, MOE_KV_BF16>{})
+                 : fmt == MOE_KV_MXFP8 ? pick(std::integral_constant<int, MOE_KV_MXFP8>{})
+                 : fmt == MOE_KV_MXFP4 ? pick(std::integral_constant<int, MOE_KV_MXFP4>{})
+                                       : pick(std::integral_constant<int, kNoCache>{});
+  return launch_pdl(kernel, grid, dim3(kBlock), 0, s, p);
 }
 
 }  // namespace
@@ -194,7 +337,8 @@ extern "C" moe_status_t moe_head_norm_rope(const moe_kv_cache_t* cache, const mo
   if (a->n_q_heads < 0 || a->n_kv_heads < 0 || a->n_q_heads > 65535 || a->n_kv_heads > 65535)
     return decode_fail(MOE_ERR_INVALID_ARG, "%s: heads (%d, %d) outside [0, 65535]", call, a->n_q_heads, a->n_kv_heads);
   const int64_t rows = cache ? (int64_t)cache->n_seqs * a->L : a->T;
-  if (rows > 0x7FFFFFFFll) return decode_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^31 - 1 rows", call);
+  if (rows > 0x7FFFFF00ll || (int64_t)a->n_q_heads + 2 * (int64_t)a->n_kv_heads > 65535)
+    return decode_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^31 - 256 rows or 65535 heads", call);
   const bool with_q = a->q || a->q_out, with_k = cache || a->k || a->k_out;
   RopeParams p{};
   const struct {
@@ -228,7 +372,8 @@ extern "C" moe_status_t moe_head_norm_rope(const moe_kv_cache_t* cache, const mo
   if (cache && !cache->seq_lens) return decode_fail(MOE_ERR_INVALID_ARG, "%s: seq_lens is NULL", call);
   if (a->rot_dim && (!a->turns || (!cache && !a->positions)))
     return decode_fail(MOE_ERR_INVALID_ARG, "%s: turns or positions is NULL", call);
-  st = check_device(nullptr);
+  int sms = 0;
+  st = check_device(&sms);
   if (st != MOE_OK) return st;
   if (cache) p.c = *cache;
   p.q = static_cast<const __nv_bfloat16*>(a->q);
@@ -241,19 +386,21 @@ extern "C" moe_status_t moe_head_norm_rope(const moe_kv_cache_t* cache, const mo
   p.turns = a->turns;
   p.axis = a->axis;
   p.pos = a->positions;
+  p.rows = (int)rows;
   p.L = cache ? a->L : 1;
   p.hq = with_q ? a->n_q_heads : 0;
   p.hkv = with_k ? a->n_kv_heads : 0;
   p.heads = p.hq + p.hkv * (cache ? 2 : 1);
   p.rot = a->rot_dim;
-  p.adjacent = a->pairs == MOE_ROPE_ADJACENT;
   p.w_f32 = a->weight_f32;
   p.eps = a->eps;
   p.page = cache ? page_div((uint32_t)cache->page_size) : PageDiv{0, 0};
+  p.len = page_div((uint32_t)p.L);
   if (p.heads == 0) return MOE_OK;
   const int fmt = cache ? cache->format : kNoCache;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = a->head_dim == 128 ? launch<128>(p, fmt, rows, s) : launch<64>(p, fmt, rows, s);
+  const bool adjacent = a->pairs == MOE_ROPE_ADJACENT;
+  const cudaError_t e = a->head_dim == 128 ? launch<128>(p, fmt, adjacent, sms, s) : launch<64>(p, fmt, adjacent, sms, s);
   if (e != cudaSuccess) return decode_fail(MOE_ERR_CUDA, "%s: %s", call, cudaGetErrorString(e));
   return MOE_OK;
 }
