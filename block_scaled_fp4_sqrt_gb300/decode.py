@@ -12,7 +12,7 @@ from fractions import Fraction
 
 import torch
 
-from . import (MOE_ATTENTION_COUNTER_BYTES, MOE_OK, MoEError, _dense, _empty, _ok, _on_current_gpu, _on_stream, _raw_stream,
+from . import (MOE_ATTENTION_COUNTER_BYTES, MOE_OK, MoEError, _empty, _ok, _on_current_gpu, _on_stream, _raw_stream,
                _refuse, lib, moe_attention_t, moe_head_rope_t, moe_kv_cache_t, moe_norm_t, moe_page_pool_t)
 
 MOE_KV_BF16, MOE_KV_MXFP8, MOE_KV_MXFP4 = 0, 1, 4
@@ -24,6 +24,7 @@ KV_STATUS = {16: "a wait inside a kernel ran out", 1: "a sequence length outside
              4: "a request wanted more pages than are free", 8: "a fork between requests that do not allow it"}
 MOE_POOL_MAX_SEQS = 8192
 PAIRS = {"half": 0, "adjacent": 1}
+_CacheAt = ctypes.POINTER(moe_kv_cache_t)
 
 
 def _rows(t: torch.Tensor, name: str, shape, gpu: int, dtype=torch.bfloat16) -> tuple[int, int]:
@@ -105,65 +106,57 @@ class RotaryPlan:
         self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
         self.axis = None if axis is None else torch.tensor(axis, dtype=torch.uint8, device=device)
         self.pairs = PAIRS[pairs]
+        self.at, self.axis_at = self.turns.data_ptr() if freq else None, None if axis is None or not axis else self.axis.data_ptr()
 
 
 def _head_rows(t: torch.Tensor, name: str, gpu: int) -> tuple:
     """(rows, heads, head_dim, row stride) of a bf16 tensor [..., heads, head_dim] whose rows lie at one stride."""
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
     if len(shape) < 3 or t.dtype is not torch.bfloat16 or t.get_device() != gpu:
         raise ValueError(f"{name} must be bf16 [..., heads, head_dim] on cuda:{gpu}, got {t.dtype} {tuple(shape)} on {t.device}")
-    h, d = shape[-2:]
+    *lead, h, d = shape
+    *steps, sh, sd = t.stride()
     rows, row = 1, 0
-    for n, s in zip(reversed(shape[:-2]), reversed(stride[:-2])):
-        if n > 1:
-            if rows > 1 and s != rows * row:
-                raise ValueError(f"{name}: the rows must lie at one stride")
+    for n, s in zip(reversed(lead), reversed(steps)):
+        if n != 1:
             if rows == 1:
                 row = s
                 if row == 0:  # the library reads stride 0 as contiguous rows
                     raise ValueError(f"{name} is broadcast: its rows must lie in memory of their own")
-        rows *= n
-    if (d > 1 and stride[-1] != 1) or (h > 1 and stride[-2] != d):
+            elif s != rows * row:
+                raise ValueError(f"{name}: the rows must lie at one stride")
+            rows *= n
+    if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"{name}: heads must be contiguous")
     return rows, h, d, row
 
 
-def _rope_args(gpu: int, q, k, v, rope: RotaryPlan, positions, q_weight, k_weight, eps, q_out, k_out) -> moe_head_rope_t:
-    a, rows, dim, shapes = moe_head_rope_t(), None, None, {}
-    for name, t in (("q", q), ("k", k), ("v", v), ("q_out", q_out), ("k_out", k_out)):
-        if t is None:
-            continue
-        n, h, d, row = _head_rows(t, name, gpu)
-        if (rows is not None and rows != n) or (dim is not None and dim != d):
-            raise ValueError(f"{name} holds {n} rows of heads of {d} columns, others {rows} of {dim}")
-        rows, dim, shapes[name] = n, d, h
-        setattr(a, name, t.data_ptr())
-        setattr(a, name + "_stride", row)
-    for x, y in (("q", "q_out"), ("k", "k_out"), ("k", "v")):
-        if x in shapes and y in shapes and shapes[x] != shapes[y]:
-            raise ValueError(f"{x} has {shapes[x]} heads, {y} {shapes[y]}")
-    if rope.turns.get_device() != gpu:
-        raise ValueError(f"the rotation's plan lies on {rope.turns.device}, the tensors on cuda:{gpu}")
-    if positions is not None:
-        if positions.dtype is not torch.int32 or positions.get_device() != gpu or not positions.is_contiguous() or \
-                positions.numel() != rope.n_axes * rows:
-            _refuse(positions, "positions", f"int32 [{rope.n_axes}, {rows}]")
-        a.positions = positions.data_ptr()
-    kinds = {w.dtype for w in (q_weight, k_weight) if w is not None}
+def _head_weights(q_weight, k_weight, dim: int, gpu: int) -> tuple:
+    """Addresses of the two weights (None: no norm) and whether they are fp32."""
+    at, kind = [], None
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
         if w is None:
+            at.append(None)
             continue
-        if len(kinds) != 1 or w.dtype not in (torch.bfloat16, torch.float32) or w.shape != (dim,) or not w.is_contiguous() or \
-                w.get_device() != gpu:
+        dtype = w.dtype
+        if (dtype is not torch.bfloat16 and dtype is not torch.float32) or (kind is not None and dtype is not kind) or \
+                w.shape != (dim,) or not w.is_contiguous() or w.get_device() != gpu:
             raise ValueError(f"{name} must be a contiguous bf16 or fp32 tensor of {dim} columns on cuda:{gpu}, of the other "
                              "weight's type")
-        setattr(a, name, w.data_ptr())
-    a.turns = rope.turns.data_ptr() if rope.rot_dim else None
-    a.axis = None if rope.axis is None else rope.axis.data_ptr()
-    a.T, a.n_q_heads, a.n_kv_heads = rows, shapes.get("q", 0), shapes.get("k", 0)
-    a.head_dim, a.rot_dim, a.pairs, a.n_axes = dim, rope.rot_dim, rope.pairs, rope.n_axes
-    a.weight_f32, a.eps = int(kinds == {torch.float32}), eps
-    return a
+        kind = dtype
+        at.append(w.data_ptr())
+    return at[0], at[1], kind is torch.float32
+
+
+def _head_positions(positions, rope: "RotaryPlan", rows: int, gpu: int):
+    if rope.turns.get_device() != gpu:
+        raise ValueError(f"the rotation's plan lies on {rope.turns.device}, the tensors on cuda:{gpu}")
+    if positions is None:
+        return None
+    if positions.dtype is not torch.int32 or positions.numel() != rope.n_axes * rows or not positions.is_contiguous() or \
+            positions.get_device() != gpu:
+        _refuse(positions, "positions", f"int32 [{rope.n_axes}, {rows}]")
+    return positions.data_ptr()
 
 
 def moe_head_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, rope: RotaryPlan, positions: torch.Tensor,
@@ -181,14 +174,34 @@ def moe_head_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, rope: Rot
     if gpu < 0:
         raise ValueError(f"q and k must be CUDA tensors, got one on {lead.device}")
     _on_current_gpu("q" if q is not None else "k", gpu)
-    if (q is None and q_out is not None) or (k is None and k_out is not None):
-        raise ValueError("an output without its input")
-    q_out = _empty(q.shape, q.dtype, q.device, stream) if q is not None and q_out is None else q_out
-    k_out = _empty(k.shape, k.dtype, k.device, stream) if k is not None and k_out is None else k_out
-    a = _rope_args(gpu, q, k, None, rope, positions, q_weight, k_weight, eps, q_out, k_out)
-    if positions is None and a.T and rope.rot_dim:
+    rows, heads, dim, at = -1, [0, 0], -1, []
+    for i, (name, t, out) in enumerate((("q", q, q_out), ("k", k, k_out))):
+        if t is None:
+            if out is not None:
+                raise ValueError(f"{name}_out is given without {name}")
+            at.append((None, None, 0, 0))
+            continue
+        n, h, d, step = _head_rows(t, name, gpu)
+        if out is None:
+            out = _empty(t.shape, t.dtype, t.device, stream)
+        no, ho, do, step_out = _head_rows(out, name + "_out", gpu)
+        if (no, ho, do) != (n, h, d) or (rows >= 0 and (rows, dim) != (n, d)):
+            raise ValueError(f"{name} holds {n} rows of {h} heads of {d} columns, {name}_out {no} of {ho} of {do}, and q {rows} of "
+                             f"heads of {dim}")
+        rows, dim, heads[i] = n, d, h
+        at.append((t.data_ptr(), out.data_ptr(), step, step_out))
+        if i == 0:
+            q_out = out
+        else:
+            k_out = out
+    pos = _head_positions(positions, rope, rows, gpu)
+    if pos is None and rows and rope.rot_dim:
         raise ValueError("positions must be given")
-    status = lib().moe_head_norm_rope(None, ctypes.byref(a), _raw_stream(stream))
+    qw, kw, w32 = _head_weights(q_weight, k_weight, dim, gpu)
+    (qp, qop, qs, qos), (kp, kop, ks, kos) = at
+    status = lib().moe_head_norm_rope(None, moe_head_rope_t(
+        qp, kp, None, qop, kop, qw, kw, rope.at, rope.axis_at, pos, qs, ks, 0, qos, kos, 0, rows, 0, heads[0], heads[1], dim,
+        rope.rot_dim, rope.pairs, rope.n_axes, w32, eps), _raw_stream(stream))
     if status:
         _ok("moe_head_norm_rope", status)
     return q_out, k_out
@@ -241,7 +254,7 @@ class PagedKVCache:
                                  v_scales.data_ptr() if mx else None, block_table.data_ptr(), seq_lens.data_ptr(),
                                  self.status.data_ptr(), *st, self.format, n_pages, page,
                                  heads, d, self.n_seqs, block_table.shape[1])
-        self._ref = ctypes.byref(self._c)
+        self._ref, self._at = ctypes.byref(self._c), ctypes.pointer(self._c)
         self._workspace_bytes = {}
         self._index = k.get_device()
 
@@ -296,21 +309,32 @@ class PagedKVCache:
         the tokens' places in their sequences.  Returns q_out (allocated on `stream` if not given; may be q); k_out, if given,
         receives the rotated keys as well."""
         _on_current_gpu("the cache", self._index)
-        if q is None and q_out is not None:
-            raise ValueError("an output without its input")
-        q_out = _empty(q.shape, q.dtype, self.device, stream) if q is not None and q_out is None else q_out
-        L = None
-        for name, t, heads in (("q", q, None), ("q_out", q_out, None), ("k_new", k_new, self.n_kv_heads),
-                               ("v_new", v_new, self.n_kv_heads), ("k_out", k_out, self.n_kv_heads)):
-            if t is None:
-                continue
-            n = self._step_rows(t, name, heads)[0]
-            if L is not None and n != L:
-                raise ValueError(f"{name} holds another number of tokens")
-            L = n
-        a = _rope_args(self._index, q, k_new, v_new, rope, positions, q_weight, k_weight, eps, q_out, k_out)
-        a.L = L
-        status = lib().moe_head_norm_rope(self._ref, ctypes.byref(a), _raw_stream(stream))
+        L, _, ks = self._step_rows(k_new, "k_new", self.n_kv_heads)
+        Lv, _, vs = self._step_rows(v_new, "v_new", self.n_kv_heads)
+        if L != Lv:
+            raise ValueError("k_new and v_new hold different numbers of tokens")
+        qp = qop = kop = None
+        heads = qs = qos = kos = 0
+        if q is not None:
+            Lq, heads, qs = self._step_rows(q, "q")
+            if q_out is None:
+                q_out = _empty(q.shape, q.dtype, self.device, stream)
+            Lo, _, qos = self._step_rows(q_out, "q_out", heads)
+            if Lq != L or Lo != L:
+                raise ValueError("q, q_out and k_new hold different numbers of tokens")
+            qp, qop = q.data_ptr(), q_out.data_ptr()
+        elif q_out is not None:
+            raise ValueError("q_out is given without q")
+        if k_out is not None:
+            Lo, _, kos = self._step_rows(k_out, "k_out", self.n_kv_heads)
+            if Lo != L:
+                raise ValueError("k_out and k_new hold different numbers of tokens")
+            kop = k_out.data_ptr()
+        pos = _head_positions(positions, rope, self.n_seqs * L, self._index)
+        qw, kw, w32 = _head_weights(q_weight, k_weight, self.head_dim, self._index)
+        status = lib().moe_head_norm_rope(self._ref, moe_head_rope_t(
+            qp, k_new.data_ptr(), v_new.data_ptr(), qop, kop, qw, kw, rope.at, rope.axis_at, pos, qs, ks, vs, qos, kos, 0, 0, L,
+            heads, self.n_kv_heads, self.head_dim, rope.rot_dim, rope.pairs, rope.n_axes, w32, eps), _raw_stream(stream))
         if status:
             _ok("moe_head_norm_rope", status)
         return q_out
@@ -423,8 +447,8 @@ class PagePool:
         i32 = dict(dtype=torch.int32, device=device)
         return cls(torch.full((n_seqs, max_pages), -1, **i32), torch.zeros(n_seqs, **i32), torch.zeros(n_pages, **i32), page_size)
 
-    def _ints(self, t: torch.Tensor, name: str, *shape) -> int:
-        if t.shape != shape or not _dense(t, torch.int32, t.numel()) or t.get_device() != self._index:
+    def _ints(self, t: torch.Tensor, name: str, shape: tuple) -> int:
+        if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous() or t.get_device() != self._index:
             _refuse(t, name, f"int32 {list(shape)} on {self.device}")
         return t.data_ptr()
 
@@ -432,7 +456,7 @@ class PagePool:
         """Request dst[i], of length 0, becomes a branch of request src[i]: the same pages and length.  int32 [n]."""
         _on_current_gpu("the pool", self._index)
         n = src.shape[0] if src.dim() == 1 else -1
-        status = lib().moe_pages_fork(self._ref, self._ints(src, "src", n), self._ints(dst, "dst", n), n, _raw_stream(stream))
+        status = lib().moe_pages_fork(self._ref, self._ints(src, "src", (n,)), self._ints(dst, "dst", (n,)), n, _raw_stream(stream))
         if status:
             _ok("moe_pages_fork", status)
 
@@ -444,8 +468,8 @@ class PagePool:
         _on_current_gpu("the pool", self._index)
         if copies is None:
             copies = _empty((self.n_seqs, 2), torch.int32, self.device, stream)
-        status = lib().moe_pages_resize(self._ref, self._ints(new_lens, "new_lens", self.n_seqs),
-                                        self._ints(copies, "copies", self.n_seqs, 2), _raw_stream(stream))
+        status = lib().moe_pages_resize(self._ref, self._ints(new_lens, "new_lens", (self.n_seqs,)),
+                                        self._ints(copies, "copies", (self.n_seqs, 2)), _raw_stream(stream))
         if status:
             _ok("moe_pages_resize", status)
         return copies
@@ -455,7 +479,7 @@ class PagePool:
         [capacity, 2], receives (from, to) of the moves for ``moe_copy_pages``, and (-1, -1)."""
         _on_current_gpu("the pool", self._index)
         n = copies.shape[0]
-        status = lib().moe_pages_compact(self._ref, self._ints(copies, "copies", n, 2), n, _raw_stream(stream))
+        status = lib().moe_pages_compact(self._ref, self._ints(copies, "copies", (n, 2)), n, _raw_stream(stream))
         if status:
             _ok("moe_pages_compact", status)
         return copies
@@ -472,16 +496,17 @@ class PagePool:
 def moe_copy_pages(caches, copies: torch.Tensor, stream=None) -> None:
     """In every cache of the list, page copies[i, 1] receives the contents of page copies[i, 0]; pairs whose first page is
     negative are skipped.  copies: int32 [n, 2].  No page may be the second of two pairs, or of one and the first of another."""
-    caches = list(caches)
-    if len(copies.shape) != 2 or copies.shape[1] != 2 or not _dense(copies, torch.int32, copies.numel()):
+    shape, gpu = copies.shape, copies.get_device()
+    if len(shape) != 2 or shape[1] != 2 or copies.dtype is not torch.int32 or gpu < 0 or not copies.is_contiguous():
         _refuse(copies, "copies", "int32 [n, 2]")
-    _on_current_gpu("copies", copies.get_device())
+    _on_current_gpu("copies", gpu)
+    at = []
     for c in caches:
-        if c._index != copies.get_device():
+        if c._index != gpu:
             raise ValueError(f"a cache lies on {c.device}, copies on {copies.device}")
-    if not caches:
+        at.append(c._at)
+    if not at:
         return
-    refs = (ctypes.POINTER(moe_kv_cache_t) * len(caches))(*[ctypes.pointer(c._c) for c in caches])
-    status = lib().moe_copy_pages(refs, len(caches), copies.data_ptr(), copies.shape[0], _raw_stream(stream))
+    status = lib().moe_copy_pages((_CacheAt * len(at))(*at), len(at), copies.data_ptr(), shape[0], _raw_stream(stream))
     if status:
         _ok("moe_copy_pages", status)
