@@ -69,13 +69,12 @@ MOE_API moe_status_t moe_add_rms_norm(const moe_norm_t* args, moe_stream_t strea
  *   seq_lens     int32 [n_seqs]: tokens of every request, the step's L new ones included; may be 0.
  *   status       device int32 or NULL: sticky error bits (MOE_KV_BAD_LENGTH: a length below 0 or above
  *                max_pages * page_size, used as 0 or as that bound; MOE_KV_BAD_PAGE: a page outside
- *                [0, n_pages), which is not accessed: its request's result is not meaningful; MOE_KV_TIMEOUT: a wait
- *                inside a kernel ran out of its two seconds, and the call's results are not meaningful).
+ *                [0, n_pages), which is not accessed: its request's result is not meaningful).
  *   head_dim     64 or 128; page_size >= 1; n_kv_heads >= 1.
  * Pages may be shared by requests as long as no call writes to them.
  */
 enum { MOE_KV_BF16 = 0, MOE_KV_MXFP8 = 1, MOE_KV_MXFP4 = 4 };
-enum { MOE_KV_BAD_LENGTH = 1, MOE_KV_BAD_PAGE = 2, MOE_KV_TIMEOUT = 16 };
+enum { MOE_KV_BAD_LENGTH = 1, MOE_KV_BAD_PAGE = 2 };
 typedef struct {
   void* k;
   void* v;
@@ -112,8 +111,8 @@ MOE_API moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const void* k_ne
  *            0 = contiguous), 16-byte aligned.
  *   lse      fp32 [n_seqs, L, n_q_heads] or NULL.
  *   n_q_heads a multiple of n_kv_heads; L >= 0; scale finite; k and v span less than 64 GB each; the keys of an MXFP8
- *            or MXFP4 cache lie below 2^100 (their block sums are held in fp32 before q's own scale), and so do the values of
- *            an MXFP4 cache (their sums are held times 2^19).
+ *            or MXFP4 cache lie below 2^100 (their block sums are held in fp32 before q's own scale), the values of an
+ *            MXFP4 cache below 2^77 (a weight in their sums is up to 2^19, and 2^31 of them may add up).
  *   workspace  at least moe_paged_attention_workspace(cache, n_q_heads, L) bytes, 256-byte aligned.  Its first
  *            MOE_ATTENTION_COUNTER_BYTES bytes must be ZERO before its first use; every call leaves them zero, and what
  *            else it holds does not matter.  So one buffer serves any calls, of any caches and shapes, that run one
@@ -147,10 +146,11 @@ MOE_API moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_
  * are x'.  Every output is the fp32 value rounded once.
  *   rope       turns [rot_dim / 2], device, 8-byte aligned: the angle per position as a fraction of a turn, in units of 2^-64
  *              turns (modulo 2^64): the phase of any position is exact integer arithmetic, so that far positions lose nothing.
- *              axis [rot_dim / 2] or NULL (all 0): which row of `positions` a pair turns with, below n_axes.
+ *              axis [rot_dim / 2] or NULL (all 0): which row of `positions` a pair turns with, below n_axes (any other
+ *              counts as n_axes - 1).
  *              rot_dim even, 0 to head_dim.
  *   positions  int32 [n_axes][T] with rows position_stride apart (0 = T), or NULL with a cache: seq_lens[b] - L + l on
- *              every axis.
+ *              every axis.  Of any sign.
  *   q, k, v    bf16 rows at q_stride / k_stride / v_stride (multiples of 8; 0 = contiguous), 16-byte aligned, heads
  *              contiguous: views of a fused projection's output serve.  q_out, k_out likewise; they may be q or k themselves
  *              (same stride); other overlaps are not allowed.  q and q_out go together; k_out may be NULL with a cache.
@@ -198,8 +198,9 @@ MOE_API moe_status_t moe_head_norm_rope(const moe_kv_cache_t* cache, const moe_h
  *   others hold too takes a page of its own for it: copies[b] (device int32 [n_seqs][2]) is then (old page, new page), and
  *   (-1, -1) otherwise.  First all requests give pages back; then the pages that are wanted, in the order of the requests
  *   (the copy's page first), are the free ones in the order of their indexes.  A request that wants pages beyond the last
- *   free one keeps its length; a new length outside [0, max_pages * page_size] is reported and not taken.  Pages that only
- *   become free because their last holders took copies are not handed out in the same call.
+ *   free one keeps its length (the pages that it would have had a part of stay free); a new length outside
+ *   [0, max_pages * page_size] is reported and not taken.  Pages that only become free because their last holders took
+ *   copies are not handed out in the same call.
  * moe_pages_compact: the live page of the highest index moves to the free page of the lowest, the next highest to the next
  *   lowest, and so on while that is lower, at most `capacity` pages; copies[i] (device int32 [capacity][2]) is (from, to) of
  *   move i, (-1, -1) behind the last.
