@@ -2,7 +2,12 @@
 //
 //   s_t = scale * sum_blk 2^ks[t,blk] (q . e2m1(k[t]))_blk,  p_t = exp(s_t - m),  out = sum p_t 2^vs[t] e2m1(v[t]) / sum p_t
 //
-// A token of a head is 136 bytes (D = 128), so unpacking and the products weigh more than memory.  What follows from it:
+// A token of a head is 136 bytes (D = 128), so instructions and their latencies at eight to twelve warps an SM bound it, not
+// memory.  64 requests of 100 to 8000 tokens, 8 x 4 heads of 128: one row 41 us (floor 19; 3.2 TB/s), eight rows 90 us (floor
+// 20; the products alone 26 on mma.sync); three requests of up to 131,071 tokens 65 us (floor 36, 3.8 TB/s); one request of
+// 333 tokens 9 us; two prompts of 500 tokens over up to 3001, 4 x 4 heads of 64, 65 us (127 TFLOP/s).  Of the 90 us about 20
+// are units' beginnings and ends (three to a block), 6 dealing and the first loads, the rest 2,500 cycles a tile, of which the
+// softmax's chain of dependent instructions is 900.  What follows from it:
 //  * The products are transposed, S^T = K q^T and O^T = V^T P^T: the 16-row side of a product holds tokens or columns, the
 //    8-column side the rows of q, so that one to eight rows cost half of what they would the other way round.
 //  * A tile's tokens belong to the block's four warps, WT each, from the copy into shared memory to the accumulators: no
@@ -17,11 +22,12 @@
 //  * Scores: q in fp16, its row scaled by a power of two to a maximum in [2^14, 2^15); a block's scale multiplies the fp32
 //    product of its 32 columns, so keys have fp32's range.
 //  * Values: a code times its scale is exact in fp16 while the scale lies in [2^-28, 2^8] (2^5 times it is at least 2^-23, of
-//    which half is fp16's smallest number).  Tiles with another scale, among them 255 (a block that held a NaN or an
-//    infinity), are summed token by token in fp32, leaving out for each row the tokens that it does not see.
-//  * p is at most 2^14 (the running maximum of a row stands 2^6 lower than its largest score, and moves when a score exceeds
-//    it by 2^14): fp16 keeps eleven bits of it down to 2^-20 of the row's largest weight and some down to 2^-30.  Its sum
-//    is taken in fp32, before that rounding.
+//    which half is fp16's smallest number).  A block of 32 columns with another scale, among them 255 (it held a NaN or an
+//    infinity), takes part in the products with the multiplier 0 and is added in fp32, for each row that sees its token.
+//  * p is at most 2^14: a row's reference stands 6 below its largest score, in log2 units, and moves when a score exceeds it
+//    by 14, for the row's own scores alone, so that neither other rows nor tokens that it does not see change its bits.  fp16
+//    keeps eleven bits of p down to 2^-20 of the row's largest weight and some down to 2^-30.  Its sum is taken in fp32,
+//    before that rounding.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -32,9 +38,9 @@ namespace moe {
 
 namespace {
 
-constexpr float kTop = 6.f;    // the largest p, in log2 units, right after the running maximum has moved
-constexpr float kGrow4 = 14.f; // and the one at which it moves
-constexpr int kVUp = 5;        // values are held times 2^kVUp
+constexpr float kTop = 6.f;     // the largest p, in log2 units, right after a row's reference has moved
+constexpr float kGrow4 = 14.f;  // and the one at which it moves
+constexpr int kVUp = 5;         // values are held times 2^kVUp
 // scale bytes at which fp16 holds every code times its scale exactly: half of 2^-23 is its smallest number, 6 2^13 below its
 // largest
 constexpr uint32_t kVLow = 127 - 23 - kVUp, kVHigh = 127 + 13 - kVUp;
@@ -43,7 +49,7 @@ constexpr uint32_t kVLow = 127 - 23 - kVUp, kVHigh = 127 + 13 - kVUp;
 template <int D, int RT>
 struct Cfg4 {
   static constexpr int kRows = 8 * RT;
-    // Tokens of a tile that a warp fetches, and works on at once.  Us for 64 requests, one and eight rows a head: 32 and 32
+  // Tokens of a tile that a warp fetches, and works on at once.  Us for 64 requests, one and eight rows a head: 32 and 32
   // tokens 44 (16 and 16: 54, with a fourth block 52), 32 and 16 tokens 91 (16 and 16: 104).
   static constexpr int kTok = 32;
   static constexpr int kStep = RT <= 2 ? 32 : 16;
@@ -66,8 +72,12 @@ struct Cfg4 {
   static constexpr int kOBytes = kOBuffers * kOPart;
   static constexpr int kStatBytes = (3 * kWarps + 1) * kRows * 4;
   static constexpr int kBlocks = RT == 1 ? 3 : 2;  // an SM
-  static constexpr bool kFar = RT >= 3 && D == 128;  // the accumulators leave no registers for the loader's state
-  static constexpr int kBudget = (kBlocks == 2 ? 113 : 75) * 1024 - (kFar ? (48 + 8 * RT) * kThreads : 0) - 512 - kQBytes - kOBytes - kStatBytes - 256;
+  // The accumulators leave no registers for the loader's state and the sums of p: they stay in shared memory between the
+  // steps.  (Spilled by the compiler they wait for the L2, as shared memory leaves the L1 28 KB.  64 x 8 rows: 102 -> 93 us.)
+  static constexpr bool kFar = RT >= 3 && D == 128;
+  static constexpr int kFarBytes = kFar ? (48 + 8 * RT) * kThreads : 0;
+  static constexpr int kBudget =
+      (kBlocks == 2 ? 113 : 75) * 1024 - kFarBytes - 512 - kQBytes - kOBytes - kStatBytes - 256;
   static constexpr int kFit = kBudget / (kWarps * kWarpStage);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static constexpr int kSmem = kWarps * kStages * kWarpStage + kQBytes + kOBytes + kStatBytes + 256;
@@ -252,7 +262,8 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
 
   // ---- loading: lane t < kTok looks up where the warp's token t lies; kChunks lanes fetch a row of codes.  The scales take
   // the way through lane t's registers.  Nothing waits for memory here: a tile's pages are looked up two steps before its
-  // codes are asked for, its scales are asked for one step before them and stored, converted, one step after them.
+  // codes are asked for, its scales are asked for one step before them and stored, converted, one step after them.  (A page
+  // checked right after its lookup held every step up for the lookup: 1,200 of 3,700 cycles.)
   const uint32_t ring = smem_addr(smem) + warp * C::kStages * C::kWarpStage;
   const int tok_first = warp * kTok;
   constexpr int kPerIter = 32 / kChunks;  // tokens a warp instruction covers
@@ -409,7 +420,8 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
       place[it] = make_int2(-1, 0);
       if (in) {
         place[it] = make_int2(cur.b * p.L + ql, (cur.head * lanes + lane_head) * p.group + j);
-        raw[it] = __ldg(reinterpret_cast<const uint4*>(p.q + place[it].x * p.q_stride + (int64_t)place[it].y * D + (i % kVec) * 8));
+        raw[it] = __ldg(reinterpret_cast<const uint4*>(p.q + place[it].x * p.q_stride + (int64_t)place[it].y * D +
+                                                       (i % kVec) * 8));
         lim[it] = cur.len - p.L + 1 + ql;
       } else {
         lim[it] = cur.len;  // rows that the tile does not have: their scores are 0 and their results nobody's
@@ -534,7 +546,10 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
 #pragma unroll
     for (int a = 0; a < RT; ++a) {
       float2 f, r;
-      asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(f.x), "=f"(r.x), "=f"(f.y), "=f"(r.y) : "r"(at_fr + a * 64) : "memory");
+      asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                   : "=f"(f.x), "=f"(r.x), "=f"(f.y), "=f"(r.y)
+                   : "r"(at_fr + a * 64)
+                   : "memory");
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
 #pragma unroll

@@ -20,7 +20,7 @@ MOE_KV_BF16, MOE_KV_MXFP8, MOE_KV_MXFP4 = 0, 1, 4
 # calls of a stream run one after another, whatever their caches and shapes.
 _WORKSPACES: dict[tuple[int, int], torch.Tensor] = {}
 
-KV_STATUS = {16: "a wait inside a kernel ran out", 1: "a sequence length outside the block table", 2: "a page index outside the cache",
+KV_STATUS = {1: "a sequence length outside the block table", 2: "a page index outside the cache",
              4: "a request wanted more pages than are free", 8: "a fork between requests that do not allow it"}
 MOE_POOL_MAX_SEQS = 8192
 PAIRS = {"half": 0, "adjacent": 1}
