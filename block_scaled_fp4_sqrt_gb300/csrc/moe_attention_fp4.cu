@@ -3,11 +3,11 @@
 //   s_t = scale * sum_blk 2^ks[t,blk] (q . e2m1(k[t]))_blk,  p_t = exp(s_t - m),  out = sum p_t 2^vs[t] e2m1(v[t]) / sum p_t
 //
 // A token of a head is 136 bytes (D = 128), so instructions and their latencies at eight to twelve warps an SM bound it, not
-// memory.  64 requests of 100 to 8000 tokens, 8 x 4 heads of 128: one row 41 us (floor 19; 3.2 TB/s), eight rows 90 us (floor
+// memory.  64 requests of 100 to 8000 tokens, 8 x 4 heads of 128: one row 41 us (floor 19; 3.1 TB/s), eight rows 90 us (floor
 // 20; the products alone 26 on mma.sync); three requests of up to 131,071 tokens 65 us (floor 36, 3.8 TB/s); one request of
-// 333 tokens 9 us; two prompts of 500 tokens over up to 3001, 4 x 4 heads of 64, 65 us (127 TFLOP/s).  Of the 90 us about 20
-// are units' beginnings and ends (three to a block), 6 dealing and the first loads, the rest 2,500 cycles a tile, of which the
-// softmax's chain of dependent instructions is 900.  What follows from it:
+// 333 tokens 9 us; two prompts of 500 tokens over up to 3001, 4 x 4 heads of 64, 61 us (135 TFLOP/s).  Of the 90 us about 15
+// are units' beginnings and ends (two or three to a block), 6 dealing and the first loads, the rest 2,500 cycles a tile, of
+// which the softmax's chain of dependent instructions is 900 and a fifth of the instructions the loader's.  What follows:
 //  * The products are transposed, S^T = K q^T and O^T = V^T P^T: the 16-row side of a product holds tokens or columns, the
 //    8-column side the rows of q, so that one to eight rows cost half of what they would the other way round.
 //  * A tile's tokens belong to the block's four warps, WT each, from the copy into shared memory to the accumulators: no
@@ -55,7 +55,7 @@ struct Cfg4 {
   static constexpr int kStep = RT <= 2 ? 32 : 16;
   static constexpr int kTile = kWarps * kTok;
   // what beginning and ending a unit costs when the work is dealt, in tiles
-  static constexpr int kCost = RT == 1 ? 2 : 3;
+  static constexpr int kCost = RT == 1 || D == 64 ? 2 : 3;
   static constexpr int kRowBytes = D / 2;  // one token of one head
   static constexpr int kBlk = D / 32;      // MX blocks of a row
   static constexpr int kPart = kTok * kRowBytes;  // K (or V) of a warp's tokens
@@ -71,7 +71,8 @@ struct Cfg4 {
   static constexpr int kOBuffers = RT > 1 ? 2 : 1;
   static constexpr int kOBytes = kOBuffers * kOPart;
   static constexpr int kStatBytes = (3 * kWarps + 1) * kRows * 4;
-  static constexpr int kBlocks = RT == 1 ? 3 : 2;  // an SM
+  // an SM.  (D = 64, 16 rows and more, with two blocks: 64 x 8 rows 64 us for 57, two prompts 65 for 61.)
+  static constexpr int kBlocks = RT == 1 || D == 64 ? 3 : 2;
   // The accumulators leave no registers for the loader's state and the sums of p: they stay in shared memory between the
   // steps.  (Spilled by the compiler they wait for the L2, as shared memory leaves the L1 28 KB.  64 x 8 rows: 102 -> 93 us.)
   static constexpr bool kFar = RT >= 3 && D == 128;
@@ -341,15 +342,21 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
     const uint32_t any = __ballot_sync(0xFFFFFFFFu, odd);
     if (lane == 0) s_odd[warp][stage] = any;
   };
-  // Fills a stage with the next tile.
-  auto load_stage = [&](int stage) {
-    Loader far;
-    if constexpr (C::kFar) {
+  // Fills a stage with the next tile, and puts the scales of the one before it in their place: they have arrived, but for the
+  // run's first tiles, whose codes are asked for before the wait.
+  auto put_loader = [&](const Loader& x) {
 #pragma unroll
-      for (int i = 0; i < 3; ++i) far.w[i] = s_loader[i * kThreads + tid];
-    }
-    Loader& x = C::kFar ? far : keep;
-    store_scales(stage == 0 ? C::kStages - 1 : stage - 1, x.k_old, x.v_old);
+    for (int i = 0; i < 3; ++i) s_loader[i * kThreads + tid] = x.w[i];
+  };
+  auto get_loader = [&](Loader& x) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) x.w[i] = s_loader[i * kThreads + tid];
+  };
+  auto load_stage = [&](int stage, Loader& x, auto at_start) {
+    constexpr bool kAtStart = decltype(at_start)::value;
+    const int before = stage == 0 ? C::kStages - 1 : stage - 1;
+    const uint32_t k_old = x.k_old, v_old = x.v_old;
+    if (!kAtStart) store_scales(before, k_old, v_old);
     if (x.any) {
       const uint32_t dst0 = ring + stage * C::kWarpStage;
       auto rows = [&](auto all) {
@@ -373,19 +380,18 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
     }
     cp_async_commit();
     look_ahead(x);
-    if constexpr (C::kFar) {
+    if (kAtStart && stage > 0) store_scales(before, k_old, v_old);
+  };
+  int stage = -1;  // of the tile that is worked on; below 0 before the run's first tiles have been asked for
+  auto load_first = [&]() {
+    look_ahead(keep);
 #pragma unroll
-      for (int i = 0; i < 3; ++i) s_loader[i * kThreads + tid] = far.w[i];
-    }
+    for (int s = 0; s < C::kStages - 1; ++s) load_stage(s, keep, std::true_type{});
+    if constexpr (C::kFar) put_loader(keep);
+    stage = 0;
   };
   lookup(keep);
-  look_ahead(keep);
-  if constexpr (C::kFar) {
-#pragma unroll
-    for (int i = 0; i < 3; ++i) s_loader[i * kThreads + tid] = keep.w[i];
-  }
-#pragma unroll
-  for (int s = 0; s < C::kStages - 1; ++s) load_stage(s);
+  if constexpr (C::kFar) load_first();  // (at the place below it costs registers)
 
   // ---- per-unit state.  This lane's rows: 8 a + 2 lc + e; o[a][i][2 c + e] is column (D / 8) li + 2 i + c of such a row.
   uint32_t qb[C::kQRegs ? RT : 1][C::kQRegs ? kBlk : 1][4];
@@ -428,6 +434,9 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
       }
     }
     seen_end = cur.len - p.L + 1 + (min(row0 + C::kRows, p.rows) - 1) / p.group;
+    if constexpr (!C::kFar) {
+      if (stage < 0) load_first();  // behind the run's first rows of q: one wait serves both
+    }
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
       const int i = it * kThreads + tid, rr = i / kVec, c8 = i % kVec;
@@ -903,13 +912,17 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
   };
 
   // ---- the run
-  int stage = 0;
   while (left > 0) {
     begin_unit();
     for (;;) {
       cp_async_wait<C::kStages - 2>();
       __syncwarp();  // the warp's tokens have landed for all its lanes, and all are done with the previous ones
-      load_stage(stage == 0 ? C::kStages - 1 : stage - 1);
+      {
+        Loader far;
+        if constexpr (C::kFar) get_loader(far);
+        load_stage(stage == 0 ? C::kStages - 1 : stage - 1, C::kFar ? far : keep, std::false_type{});
+        if constexpr (C::kFar) put_loader(far);
+      }
       const uint32_t at = ring + stage * C::kWarpStage;
       const uint32_t odd = s_odd[warp][stage];
 #pragma unroll 1

@@ -10,8 +10,8 @@
 //    quantised cache, of an MX block) is the partner fetched through shared memory.
 //  * Few rows: a chunk is one head, and every group of lanes computes its own angles; a prompt: up to 16 heads.  (Angles of a
 //    token computed by one warp and handed out through shared memory, behind a barrier: 8191 tokens of 40 heads on three
-//    axes 175 us; held by lanes that go over the heads: 36, 70 % of the copy rate.  512 rows into an MXFP8 cache: 15 -> 8 us,
-//    4099 tokens into an MXFP4 cache 29 us, 46 % of it; one row 4 us.)
+//    axes 175 us; held by lanes that go over the heads: 36, 70 % of the copy rate.  512 rows into an MXFP8 cache: 15 -> 7 us,
+//    4099 tokens into an MXFP4 cache 24 us, 54 % of it; one row 4 us.)
 //  * A phase is position * turns modulo 2^64, an integer product: exact for every position, where an fp32 angle at position
 //    100,000 would be off by 2^-8 of a radian.
 #include <algorithm>
@@ -24,7 +24,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kBlock = 256;
+constexpr int kBlock = 128;
 constexpr int kBatch = 4;     // heads whose loads are under way together
 constexpr int kMaxChunk = 16; // heads a group of lanes takes
 
@@ -63,7 +63,7 @@ __device__ __forceinline__ void weight4(const void* w, int f32, int col, float* 
 }
 
 template <int D, int FMT, Layout LAY>
-__global__ void __launch_bounds__(kBlock, 3) head_norm_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kBlock, 6) head_norm_rope_kernel(const RopeParams p) {
   constexpr int kLanes = D / 8;  // lanes of a head
   constexpr int kAngles = LAY == kExchange ? 8 : 4;
   __shared__ float s_x[LAY == kExchange ? kBlock / kLanes : 1][D];
@@ -78,7 +78,9 @@ __global__ void __launch_bounds__(kBlock, 3) head_norm_rope_kernel(const RopePar
   const int col0 = LAY != kHalves ? 8 * i : turned ? 4 * i : p.rot + 8 * (i - p.rot / 8);
   const int col1 = LAY == kHalves && turned ? half + 4 * i : col0 + 4;
 
-  const int first = blockIdx.y * p.chunk, last = min(first + p.chunk, p.heads);
+  // The last heads first: those of the cache take longer, and what begins late should be short (4099 tokens into an MXFP4
+  // cache 28.0 -> 24.2 us; with blocks of 256 threads 25.2).
+  const int first = (gridDim.y - 1 - blockIdx.y) * p.chunk, last = min(first + p.chunk, p.heads);
   // The heads of a kind (0 q, 1 k, 2 v) are heads kind_at .. of the call's.
   uint2 raw[kBatch][2];
   auto load = [&](auto kind, int h0, int end, uint2 (&to)[kBatch][2]) {
@@ -292,7 +294,7 @@ template <int D>
 cudaError_t launch(RopeParams p, int fmt, bool adjacent, int sms, cudaStream_t s) {
   constexpr int kLanes = D / 8;
   // Equal chunks of heads, the largest that leave 16 warps an SM: fewer and longer ones compute fewer angles (512 rows of 48
-  // heads: 8.2 us; with one head a chunk 11.3, with 8 warps an SM 11.3).
+  // heads: 7.2 us; with one head a chunk 11.3, with 12 warps an SM 8.1, with 20 to 32 the same).
   const int64_t warps = (int64_t)p.rows * p.heads * kLanes / 32;
   const int chunk = (int)std::max<int64_t>(1, std::min<int64_t>({warps / ((int64_t)sms * 16), kMaxChunk, p.heads}));
   const int chunks = (p.heads + chunk - 1) / chunk;
