@@ -4,7 +4,7 @@
 // The tables are small (a pool of 200,000 pages: 0.8 MB of counts), so their calls are bound by latency: one kernel each, one
 // cluster of eight blocks that meet at cluster barriers, no workspace.  What a call decides follows from prefix sums over
 // the requests and over the pages: the i-th wanted page is the i-th free one, whatever the order in which blocks run.
-// Measured: a step's growth of 256 requests in 200,000 pages 14.5 us, a fork of 256 requests 8, of two 4; compaction 12.
+// Measured: a step's growth of 256 requests in 200,000 pages 14 us, a fork of 256 requests 8, of two 4; compaction 12.
 // The copies are bound by memory: every byte of a page is read and written once, 16 at a time, by blocks that take a window
 // of 256 pairs each and deal its pages evenly.  4096 pages of 128 KB 168 us, 92 % of the copy rate.
 #include <algorithm>
@@ -77,10 +77,10 @@ __device__ __forceinline__ int2 cluster_scan(int2 v, int2* s, int rank, int2& to
   return before;
 }
 
-// f(i, page_refs[i]) for this block's part [lo, hi) of the pages, eight loads of a thread under way together.
+// f(i, page_refs[i]) for this block's part [lo, hi) of the pages, sixteen loads of a thread under way together.
 template <typename F>
 __device__ __forceinline__ void each_page(const moe_page_pool_t& p, int lo, int hi, F&& f) {
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 16;
   for (int i0 = lo + (int)threadIdx.x; i0 < hi; i0 += kAhead * kPoolThreads) {
     int r[kAhead];
 #pragma unroll
@@ -121,7 +121,7 @@ __device__ __forceinline__ bool page_ok(const moe_page_pool_t& p, int page) {
 }
 
 // ---------------------------------------------------------------------------------------------- fork
-__global__ void __launch_bounds__(kPoolThreads) pages_fork_kernel(const moe_page_pool_t p, const int32_t* src,
+__global__ void __launch_bounds__(kPoolThreads, 1) pages_fork_kernel(const moe_page_pool_t p, const int32_t* src,
                                                                   const int32_t* dst, int n) {
   __shared__ int s_claim[MOE_POOL_MAX_SEQS];  // the first pair that names a request as its branch
   pdl_trigger();
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kPoolThreads) pages_fork_kernel(const moe_page
 }
 
 // ---------------------------------------------------------------------------------------------- resize
-__global__ void __launch_bounds__(kPoolThreads) pages_resize_kernel(const moe_page_pool_t p, const int32_t* new_lens,
+__global__ void __launch_bounds__(kPoolThreads, 1) pages_resize_kernel(const moe_page_pool_t p, const int32_t* new_lens,
                                                                     int2* copies) {
   __shared__ int s_end[MOE_POOL_MAX_SEQS];  // pages wanted by the requests up to and with this one; sign bit: with a copy
   __shared__ int2 s_sum;
@@ -177,6 +177,12 @@ __global__ void __launch_bounds__(kPoolThreads) pages_resize_kernel(const moe_pa
     return n >= 0 && n <= cap ? n : old;
   };
 
+  // What the calls of the first requests look up below, asked for now: nothing before the first meeting changes it.
+  int first_old = 0, first_now = 0, first_last = -1;
+  if (tid < p.n_seqs) {
+    first_old = pool_len(p, tid), first_now = target(tid, first_old);
+    if (first_now > first_old && first_old % P) first_last = __ldcg(p.block_table + (int64_t)tid * p.max_pages + first_old / P);
+  }
   // pages go back, a warp a request
   for (int b = rank * kPoolWarps + warp; b < p.n_seqs; b += kCluster * kPoolWarps) {
     const int old = pool_len(p, b), now = target(b, old);
@@ -196,10 +202,10 @@ __global__ void __launch_bounds__(kPoolThreads) pages_resize_kernel(const moe_pa
     int want = 0;
     bool copy = false;
     if (b < p.n_seqs) {
-      const int old = pool_len(p, b), now = target(b, old);
+      const int old = b0 ? pool_len(p, b) : first_old, now = b0 ? target(b, old) : first_now;
       if (now > old) {
         if (old % P) {
-          const int last = __ldcg(p.block_table + (int64_t)b * p.max_pages + old / P);
+          const int last = b0 ? __ldcg(p.block_table + (int64_t)b * p.max_pages + old / P) : first_last;
           copy = page_ok(p, last) && __ldcg(p.page_refs + last) > 1;
         }
         want = pages_of(now, P) - pages_of(old, P) + copy;
@@ -263,7 +269,7 @@ __global__ void __launch_bounds__(kPoolThreads) pages_resize_kernel(const moe_pa
 }
 
 // ---------------------------------------------------------------------------------------------- compact
-__global__ void __launch_bounds__(kPoolThreads) pages_compact_kernel(const moe_page_pool_t p, int2* copies, int capacity) {
+__global__ void __launch_bounds__(kPoolThreads, 1) pages_compact_kernel(const moe_page_pool_t p, int2* copies, int capacity) {
   __shared__ int2 s_live, s_moves;
   pdl_trigger();
   pdl_wait();
