@@ -945,7 +945,7 @@ moe_status_t plan(const moe_kv_cache_t& c, int n_q_heads, int L, int num_sms, co
   z->rows = (int64_t)(n_q_heads / c.n_kv_heads) * L;
   if (z->rows > (1 << 20) || (int64_t)n_q_heads * c.head_dim > (1ll << 31))
     return decode_fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^20 rows a kv head", call);
-  const int tr = c.format == MOE_KV_MXFP4 ? attention_fp4_tile_rows(z->rows) : tile_rows(z->rows);
+  const int tr = c.format == MOE_KV_MXFP4 ? attention_fp4_tile_rows(c.head_dim, z->rows) : tile_rows(z->rows);
   z->row_tiles = (int)((z->rows + tr - 1) / tr);
   const int64_t units = (int64_t)c.n_seqs * c.n_kv_heads * z->row_tiles;
   if (units > (1ll << 30)) return decode_fail(MOE_ERR_UNSUPPORTED, "%s: too many row tiles", call);

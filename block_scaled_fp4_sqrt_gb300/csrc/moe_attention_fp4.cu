@@ -72,10 +72,10 @@ struct Cfg4 {
   static constexpr int kOBytes = kOBuffers * kOPart;
   static constexpr int kStatBytes = (3 * kWarps + 1) * kRows * 4;
   // an SM.  (D = 64, 16 rows and more, with two blocks: 64 x 8 rows 64 us for 57, two prompts 65 for 61.)
-  static constexpr int kBlocks = RT == 1 || D == 64 ? 3 : 2;
+  static constexpr int kBlocks = RT == 1 || (D == 64 && RT <= 4) ? 3 : 2;
   // The accumulators leave no registers for the loader's state and the sums of p: they stay in shared memory between the
   // steps.  (Spilled by the compiler they wait for the L2, as shared memory leaves the L1 28 KB.  64 x 8 rows: 102 -> 93 us.)
-  static constexpr bool kFar = RT >= 3 && D == 128;
+  static constexpr bool kFar = RT * D >= 384;
   static constexpr int kFarBytes = kFar ? (48 + 8 * RT) * kThreads : 0;
   static constexpr int kBudget =
       (kBlocks == 2 ? 113 : 75) * 1024 - kFarBytes - 512 - kQBytes - kOBytes - kStatBytes - 256;
@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
         for (int n = 0; n < kJoinPairs; ++n) jo[a][n] = make_float4(0.f, 0.f, 0.f, 0.f);
       }
       // (the accumulators are free by now) kIn parts are under way at once, the last ones repeated where fewer are left
-      constexpr int kIn = 4;
+      constexpr int kIn = RT > 4 ? 2 : 4;
       for (int i0 = 0; i0 < n_parts; i0 += kIn) {
         float2 pm[kIn][RT], pl[kIn][RT];
         float4 po[kIn][RT][kJoinPairs];
@@ -978,18 +978,25 @@ cudaError_t launch_one(const AttnParams& p, int num_sms, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_rows(const AttnParams& p, int num_sms, cudaStream_t s) {
-  switch (attention_fp4_tile_rows(p.rows)) {
+  switch (attention_fp4_tile_rows(D, p.rows)) {
     case 8: return launch_one<D, 1>(p, num_sms, s);
     case 16: return launch_one<D, 2>(p, num_sms, s);
     case 24: return launch_one<D, 3>(p, num_sms, s);
-    default: return launch_one<D, 4>(p, num_sms, s);
+    case 32: return launch_one<D, 4>(p, num_sms, s);
   }
+  if constexpr (D == 64) return launch_one<D, 6>(p, num_sms, s);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-// Rows of a row tile: the smallest multiple of 8 that holds the rows of a kv head, 32 above that.
-int attention_fp4_tile_rows(int64_t rows) { return rows >= 25 ? 32 : rows > 8 ? (int)((rows + 7) / 8 * 8) : 8; }
+// Rows of a row tile: the smallest multiple of 8 that holds the rows of a kv head, up to 32, and 32 above that; but 33 to 48
+// rows of heads of 64, whose accumulators take half of the registers, are one tile of 48 (64 requests: 84 us, two tiles of 32
+// 96).  One tile of 64 at two blocks an SM is slower than two of 32 at three (107 us for 96, two prompts 64 for 61).
+int attention_fp4_tile_rows(int head_dim, int64_t rows) {
+  if (rows <= 32) return rows > 8 ? (int)((rows + 7) / 8 * 8) : 8;
+  return head_dim == 64 && rows <= 48 ? 48 : 32;
+}
 
 int attention_fp4_blocks(int head_dim, int tile_rows) {
   auto of = [&](auto d) {
@@ -997,7 +1004,8 @@ int attention_fp4_blocks(int head_dim, int tile_rows) {
     return tile_rows == 8    ? Cfg4<D, 1>::kBlocks
            : tile_rows == 16 ? Cfg4<D, 2>::kBlocks
            : tile_rows == 24 ? Cfg4<D, 3>::kBlocks
-                             : Cfg4<D, 4>::kBlocks;
+           : tile_rows == 32 ? Cfg4<D, 4>::kBlocks
+                             : Cfg4<64, 6>::kBlocks;
   };
   return head_dim == 128 ? of(std::integral_constant<int, 128>{}) : of(std::integral_constant<int, 64>{});
 }

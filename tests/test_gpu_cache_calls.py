@@ -122,3 +122,21 @@ def test_the_same_request_and_tensor_twice(moe):  # noqa: F811
     moe.moe_copy_pages([cache, cache], i32([(2, 7), (-1, -1), (2, 9)]))  # one source twice, one cache twice
     cache.check()
     assert torch.equal(cache.k, want_k) and torch.equal(cache.v, want_v)
+
+
+@pytest.mark.parametrize("group,L", [(11, 3), (4, 10), (16, 3), (7, 7), (8, 8), (13, 5), (3, 65)])
+def test_attention_of_many_rows_a_head(moe, group, L):  # noqa: F811
+    """33 to 195 rows a key-value head: what a row tile of any size has to get right."""
+    lens, kv, D = [5000, 70, 0, 130], 2, 64
+    cache, g = fp4.make_cache(moe, lens, kv, D, 48, seed=group)
+    fp4.fill(cache, g, lens)
+    fp4.check_attend(cache, (1.5 * randn(g, len(lens), L, kv * group, D)).to(BF), lens)
+    for lo, hi in ((99, 135), (98, 127), (0, 3)):
+        fp4.test_attend_values_of_any_scale(moe, D, group, L, lo, hi)
+    for order in ("growing", "falling"):
+        fp4.test_attend_large_scores_move_the_maximum(moe, D, group, L, order)
+
+
+@pytest.mark.parametrize("L", [10, 16, 31])
+def test_nan_blocks_and_many_rows(moe, L):  # noqa: F811
+    fp4.test_attend_nan_blocks_reach_only_the_rows_that_see_them(moe, 64, L)
