@@ -627,6 +627,13 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
   auto add_odd_values = [&](uint32_t stage_at, int first, uint32_t odd) {
     for (; odd; odd &= odd - 1u) {
       const int t = __ffs(odd) - 1;
+      // Zeros add nothing, whatever their scale: cleared pages and heads that a model does not use hold nothing else (added one
+      // by one they took 20 times as long).
+      const uint32_t byte = lds8(stage_at + C::kVb + t * kBlk + (D / 8) * li / 32);
+      const bool outside = byte - kVLow > kVHigh - kVLow;
+      uint32_t codes = lds32(stage_at + C::kPart + v_at<D>(t, li));
+      if constexpr (D == 128) codes |= lds32(stage_at + C::kPart + v_at<D>(t, li) + 4);
+      if (!__any_sync(0xFFFFFFFFu, outside && (byte == 255u || (codes & 0x77777777u)))) continue;
       float pr[RT][2];
 #pragma unroll
       for (int a = 0; a < RT; ++a)
@@ -638,12 +645,10 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
 #pragma unroll
             for (int j = 0; j < 2; ++j)
               if (first + 16 * k + 8 * j == (t & ~7)) x = s[a][k][2 * j + e];
-          pr[a][e] = __shfl_sync(0xFFFFFFFFu, x, 4 * place_of<D>(t & 7) + lc);
+          pr[a][e] = __shfl_sync(0xFFFFFFFFu, x, 4 * place_of<D>(t & 7) + lc) * (float)(1 << kVUp);
         }
-      const int col = (D / 8) * li;
-      const uint32_t byte = lds8(stage_at + C::kVb + t * kBlk + col / 32);
-      if (byte - kVLow <= kVHigh - kVLow) continue;
-      const float sc = e8m0_float(byte, 0) * (float)(1 << kVUp);
+      if (!outside) continue;
+      const float sc = e8m0_float(byte, 0);  // finite but for 255, and multiplied last: a zero stays one
 #pragma unroll
       for (int a = 0; a < RT; ++a)
 #pragma unroll
@@ -651,9 +656,9 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
           if (cur.t * kTile + tok_first + t >= s_lim[a * 8 + 2 * lc + e]) continue;
 #pragma unroll
           for (int n = 0; n < kPairs; ++n) {
-            const uint32_t codes = lds8(stage_at + C::kPart + v_at<D>(t, li) + n);
-            o[a][n][e] = fmaf(pr[a][e], e2m1_value(codes) * sc, o[a][n][e]);
-            o[a][n][2 + e] = fmaf(pr[a][e], e2m1_value(codes >> 4) * sc, o[a][n][2 + e]);
+            const uint32_t pair = lds8(stage_at + C::kPart + v_at<D>(t, li) + n);
+            o[a][n][e] = fmaf(pr[a][e] * e2m1_value(pair), sc, o[a][n][e]);
+            o[a][n][2 + e] = fmaf(pr[a][e] * e2m1_value(pair >> 4), sc, o[a][n][2 + e]);
           }
         }
     }

@@ -140,3 +140,29 @@ def test_attention_of_many_rows_a_head(moe, group, L):  # noqa: F811
 @pytest.mark.parametrize("L", [10, 16, 31])
 def test_nan_blocks_and_many_rows(moe, L):  # noqa: F811
     fp4.test_attend_nan_blocks_reach_only_the_rows_that_see_them(moe, 64, L)
+
+
+@pytest.mark.parametrize("D,group,L", [(64, 4, 1), (128, 4, 1), (128, 4, 8), (64, 4, 8)])
+def test_blocks_of_zeros_among_the_values(moe, D, group, L):  # noqa: F811
+    """Zeros of either sign under any scale byte but 255 add nothing; tiny and large blocks of the same tokens still do."""
+    lens, kv = [400, 33], 2
+    cache, g = fp4.make_cache(moe, lens, kv, D, 16, seed=D + L)
+    fp4.fill(cache, g, lens)
+    for b, n in enumerate(lens):
+        at = fp4.at_of(cache, b, n)
+        codes, scales = cache.v[at].unflatten(-1, (-1, 16)), cache.v_scales[at]
+        kind = torch.randint(0, 5, scales.shape, generator=g, device=DEV)
+        kind[n // 2:][kind[n // 2:] > 2] = 1  # half of the tokens hold nothing but zeros and ordinary blocks
+        for i, (code, scale) in {1: (0x00, 0), 2: (0x80, 254), 3: (None, 60), 4: (None, 150)}.items():
+            scales[kind == i] = scale
+            if code is not None:
+                codes[kind == i] = code
+        cache.v[at], cache.v_scales[at] = codes.flatten(-2), scales
+    q = randn(g, 2, L, kv * group, D).to(BF)
+    want, _ = fp4.check_attend(cache, q, lens)
+    at = fp4.at_of(cache, 0, lens[0])
+    cache.v_scales[at[0][-1], at[1][-1], 0, 0], cache.v[at[0][-1], at[1][-1], 0, :16] = 255, 0  # the newest token of one head
+    out = cache.attend(q)
+    hit = torch.zeros_like(q, dtype=torch.bool)
+    hit[0, -1, :group, :32] = True
+    assert torch.isnan(out[hit]).all() and torch.equal(out[0, :-1], want[0, :-1]) and torch.equal(out[1], want[1])
