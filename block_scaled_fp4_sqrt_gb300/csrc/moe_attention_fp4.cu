@@ -162,10 +162,10 @@ __device__ __forceinline__ void sts16(uint32_t at, uint32_t v) {
 __device__ __forceinline__ void sts32(uint32_t at, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
 }
-__device__ __forceinline__ float e2m1_value(uint32_t nibble) {
-  const float mag = nibble & 4u ? (nibble & 2u ? 4.f : 2.f) * (nibble & 1u ? 1.5f : 1.f)
-                                : (nibble & 2u ? 1.f : 0.f) + (nibble & 1u ? 0.5f : 0.f);
-  return nibble & 8u ? -mag : mag;
+__device__ __forceinline__ float2 f16x2_float(uint32_t w) {
+  float2 r;
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}" : "=f"(r.x), "=f"(r.y) : "r"(w));
+  return r;
 }
 // E8M0 bytes 0, 1 (or 2, 3) of w as a bf16 pair, exact.
 __device__ __forceinline__ uint32_t e8m0_bf16x2(uint32_t w, bool high) {
@@ -635,6 +635,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
       if constexpr (D == 128) codes |= lds32(stage_at + C::kPart + v_at<D>(t, li) + 4);
       if (!__any_sync(0xFFFFFFFFu, outside && (byte == 255u || (codes & 0x77777777u)))) continue;
       float pr[RT][2];
+      uint32_t sees = 0;  // of this lane's rows (bit 2 a + e)
 #pragma unroll
       for (int a = 0; a < RT; ++a)
 #pragma unroll
@@ -646,21 +647,29 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
             for (int j = 0; j < 2; ++j)
               if (first + 16 * k + 8 * j == (t & ~7)) x = s[a][k][2 * j + e];
           pr[a][e] = __shfl_sync(0xFFFFFFFFu, x, 4 * place_of<D>(t & 7) + lc) * (float)(1 << kVUp);
+          if (cur.t * kTile + tok_first + t < s_lim[a * 8 + 2 * lc + e]) sees |= 1u << (2 * a + e);
         }
       if (!outside) continue;
       const float sc = e8m0_float(byte, 0);  // finite but for 255, and multiplied last: a zero stays one
+      auto column_pair = [&](uint32_t word, auto y, int n) {
+        const float2 v = f16x2_float(e2m1_f16<decltype(y)::value>(word));
 #pragma unroll
-      for (int a = 0; a < RT; ++a)
+        for (int a = 0; a < RT; ++a)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (cur.t * kTile + tok_first + t >= s_lim[a * 8 + 2 * lc + e]) continue;
+          for (int e = 0; e < 2; ++e)
+            if (sees >> (2 * a + e) & 1u) {
+              o[a][n][e] = fmaf(pr[a][e] * v.x, sc, o[a][n][e]);
+              o[a][n][2 + e] = fmaf(pr[a][e] * v.y, sc, o[a][n][2 + e]);
+            }
+      };
 #pragma unroll
-          for (int n = 0; n < kPairs; ++n) {
-            const uint32_t pair = lds8(stage_at + C::kPart + v_at<D>(t, li) + n);
-            o[a][n][e] = fmaf(pr[a][e] * e2m1_value(pair), sc, o[a][n][e]);
-            o[a][n][2 + e] = fmaf(pr[a][e] * e2m1_value(pair >> 4), sc, o[a][n][2 + e]);
-          }
-        }
+      for (int w = 0; w < kW; ++w) {
+        const uint32_t word = lds32(stage_at + C::kPart + v_at<D>(t, li) + 4 * w);
+        column_pair(word, std::integral_constant<int, 0>{}, 4 * w);
+        column_pair(word, std::integral_constant<int, 1>{}, 4 * w + 1);
+        column_pair(word, std::integral_constant<int, 2>{}, 4 * w + 2);
+        column_pair(word, std::integral_constant<int, 3>{}, 4 * w + 3);
+      }
     }
   };
 
