@@ -1,0 +1,43 @@
+"""The attention over a 4-bit cache where a block works through many units one after another: whole ones, and parts of shared
+ones that it joins right before it begins the next."""
+import pytest
+import torch
+
+import test_gpu_cache_fp4 as fp4
+from test_gpu_decode import BF, DEV, gen, moe, randn  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+MIXED = [3000, 1, 40, 900, 0, 2, 2500, 130, 7, 64] * 6
+SHORT = [1, 33, 0, 128, 5, 129, 64] * 40
+
+
+@pytest.mark.parametrize("lens,kv,group,L,D,page", [
+    (MIXED, 4, 4, 1, 128, 64),     # 8 rows a head (and so on below: every row tile that there is)
+    (SHORT, 4, 4, 1, 128, 16),
+    (MIXED, 4, 2, 8, 128, 16),     # 16
+    (SHORT, 4, 4, 6, 128, 16),     # 24
+    (MIXED, 4, 4, 8, 128, 64),     # 32
+    (SHORT, 4, 4, 8, 128, 16),
+    (SHORT[:140], 2, 8, 9, 128, 16),  # 72: three row tiles a head
+    (MIXED, 4, 8, 1, 64, 64),
+    (SHORT, 4, 8, 2, 64, 16),
+    (MIXED, 4, 8, 3, 64, 48),
+    (SHORT, 4, 8, 4, 64, 16),
+    (MIXED, 4, 8, 6, 64, 64),      # 48
+    (SHORT, 4, 8, 5, 64, 16),
+])
+def test_rows_go_to_their_own_unit(moe, lens, kv, group, L, D, page):  # noqa: F811
+    """A warp that begins the next unit while another still writes the last one's rows must not hand it that unit's places: every
+    row has values of its own, outputs are poisoned before every run, and all runs give the first one's bits."""
+    cache, g = fp4.make_cache(moe, lens, kv, D, page, seed=len(lens) + L)
+    fp4.fill(cache, g, lens)
+    q = (1.5 * randn(g, len(lens), L, kv * group, D)).to(BF)
+    out, lse = fp4.check_attend(cache, q, lens)
+    again, lse2 = torch.empty_like(out), torch.empty_like(lse)
+    for _ in range(40):
+        again.fill_(float("nan"))
+        lse2.fill_(float("nan"))
+        cache.attend(q, again, lse2)
+        assert torch.equal(again, out) and torch.equal(lse2, lse)
+    cache.check()
