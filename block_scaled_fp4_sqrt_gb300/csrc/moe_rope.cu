@@ -10,8 +10,8 @@
 //    quantised cache, of an MX block) is the partner fetched through shared memory.
 //  * Few rows: a chunk is one head, and every group of lanes computes its own angles; a prompt: up to 16 heads.  (Angles of a
 //    token computed by one warp and handed out through shared memory, behind a barrier: 8191 tokens of 40 heads on three
-//    axes 175 us; held by lanes that go over the heads: 36, 70 % of the copy rate.  512 rows into an MXFP8 cache: 15 -> 7 us,
-//    4099 tokens into an MXFP4 cache 24 us, 54 % of it; one row 4 us.)
+//    axes 175 us; held by lanes that go over the heads: 36, 70 % of the copy rate.  512 rows into an MXFP8 cache: 15 -> 8 us,
+//    4099 tokens into an MXFP4 cache 25 us, 53 % of it; one row 4 us.)
 //  * A phase is position * turns modulo 2^64, an integer product: exact for every position, where an fp32 angle at position
 //    100,000 would be off by 2^-8 of a radian.
 #include <algorithm>
@@ -26,6 +26,8 @@ namespace {
 
 constexpr int kBlock = 128;
 constexpr int kBatch = 4;     // heads whose loads are under way together
+// fp32 bits of the mean squares that have fp32's precision: 2^-90 to the largest number
+constexpr uint32_t kLeastSquare = 0x12800000u, kLargestSquare = 0x7F7FFFFFu;
 constexpr int kMaxChunk = 16; // heads a group of lanes takes
 
 struct RopeParams {
@@ -156,12 +158,26 @@ __global__ void __launch_bounds__(kBlock, 6) head_norm_rope_kernel(const RopePar
       uint4 out = make_uint4(r[0].x, r[0].y, r[1].x, r[1].y);
       if constexpr (K < 2) {
         if (w) {
-          float sq = 0.f;
+          auto mean_square = [&](float eps) {
+            float sq = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
+            for (int e = 0; e < 8; ++e) sq = fmaf(x[e], x[e], sq);
 #pragma unroll
-          for (int off = 1; off < kLanes; off <<= 1) sq += __shfl_xor_sync(group, sq, off);
-          const float inv = rsqrtf(fmaf(sq, 1.f / D, p.eps));
+            for (int off = 1; off < kLanes; off <<= 1) sq += __shfl_xor_sync(group, sq, off);
+            return fmaf(sq, 1.f / D, eps);
+          };
+          const float total = mean_square(p.eps);
+          float inv = rsqrtf(total);
+          // Squares that leave fp32's range are summed again in units of 2^80 or 2^-100, which bring every head into it (bf16's
+          // numbers lie in 2^-133 .. 2^128).  The lanes of a head go the same way: their sums are the same.  The branch costs
+          // 2 % (8191 tokens 34.9 -> 35.6 us, 4099 into MXFP4 24.0 -> 24.6, 512 rows 7.2 -> 8.2); a second look at a batch of
+          // heads with one test for all of them spills (38.0, 25.5).
+          if (__float_as_uint(total) - kLeastSquare > kLargestSquare - kLeastSquare) {
+            const float unit = total < 1.f ? 0x1p100f : 0x1p-80f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= unit;
+            inv = rsqrtf(mean_square(p.eps * unit * unit));
+          }
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * wv[e];
         }
@@ -294,7 +310,8 @@ template <int D>
 cudaError_t launch(RopeParams p, int fmt, bool adjacent, int sms, cudaStream_t s) {
   constexpr int kLanes = D / 8;
   // Equal chunks of heads, the largest that leave 16 warps an SM: fewer and longer ones compute fewer angles (512 rows of 48
-  // heads: 7.2 us; with one head a chunk 11.3, with 12 warps an SM 8.1, with 20 to 32 the same).
+  // heads, before the norms looked at their range: 7.2 us; with one head a chunk 11.3, with 12 warps an SM 8.1, with 20 to 32
+  // the same).
   const int64_t warps = (int64_t)p.rows * p.heads * kLanes / 32;
   const int chunk = (int)std::max<int64_t>(1, std::min<int64_t>({warps / ((int64_t)sms * 16), kMaxChunk, p.heads}));
   const int chunks = (p.heads + chunk - 1) / chunk;

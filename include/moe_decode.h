@@ -140,7 +140,8 @@ MOE_API moe_status_t moe_paged_attention(const moe_kv_cache_t* cache, const moe_
 /*
  * Norms of the heads with the position rotation, for the rows of a step: between the fused projection and the attention.
  * For every head of q and k (and row r, or (b, l) with a cache):
- *   x' = x * w / sqrt(mean(x^2) + eps)         over the head's D columns, fp32; x' = x where the weight is NULL
+ *   x' = x * w / sqrt(mean(x^2) + eps)         over the head's D columns, fp32; x' = x where the weight is NULL.  Any finite
+ *         head: where its squares leave fp32's range, the mean is taken in units of a power of two
  *   pair (i, j):  y_i = x'_i cos a - x'_j sin a,  y_j = x'_i sin a + x'_j cos a,   a = 2 pi position[axis_i] turns_i / 2^64
  * for the rot_dim / 2 pairs: MOE_ROPE_HALF (i, i + rot_dim / 2), MOE_ROPE_ADJACENT (2 i, 2 i + 1); columns from rot_dim on
  * are x'.  Every output is the fp32 value rounded once.
