@@ -116,6 +116,10 @@ def _head_rows(t: torch.Tensor, name: str, gpu: int) -> tuple:
         raise ValueError(f"{name} must be bf16 [..., heads, head_dim] on cuda:{gpu}, got {t.dtype} {tuple(shape)} on {t.device}")
     *lead, h, d = shape
     *steps, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and h > 1):
+        raise ValueError(f"{name}: heads must be contiguous")
+    if 0 in lead:  # no rows: their strides mean nothing
+        return 0, h, d, 0
     rows, row = 1, 0
     for n, s in zip(reversed(lead), reversed(steps)):
         if n != 1:
@@ -126,8 +130,6 @@ def _head_rows(t: torch.Tensor, name: str, gpu: int) -> tuple:
             elif s != rows * row:
                 raise ValueError(f"{name}: the rows must lie at one stride")
             rows *= n
-    if (sd != 1 and d > 1) or (sh != d and h > 1):
-        raise ValueError(f"{name}: heads must be contiguous")
     return rows, h, d, row
 
 
