@@ -41,3 +41,25 @@ def test_rows_go_to_their_own_unit(moe, lens, kv, group, L, D, page):  # noqa: F
         cache.attend(q, again, lse2)
         assert torch.equal(again, out) and torch.equal(lse2, lse)
     cache.check()
+
+
+@pytest.mark.parametrize("lens,kv,group,L,D,page", [
+    ([15000], 3, 2, 1, 64, 16),          # three heads side by side, one unit over 152 blocks of each
+    ([9000, 5, 0, 700], 17, 1, 2, 64, 16),   # 17 has no divisor up to 16: heads one after another, joins in two steps
+    ([12000], 18, 2, 1, 128, 64),        # two groups of nine heads: 304 or 456 blocks leave some without work
+    ([12000, 77], 18, 2, 3, 64, 48),
+    ([6000, 1, 300], 32, 2, 1, 128, 16),     # two groups of 16
+    (SHORT[:35], 32, 1, 5, 64, 16),
+    ([40] * 60 + [4000], 24, 2, 4, 64, 16),  # two of twelve, several short units a block
+    ([3000, 0, 129], 33, 3, 8, 128, 64),     # three of eleven, 24 rows a head
+    ([500, 64], 65, 1, 20, 64, 16),          # five of thirteen
+    ([2000], 48, 1, 70, 64, 16),             # three of 16, three row tiles
+])
+def test_heads_in_groups(moe, lens, kv, group, L, D, page):  # noqa: F811
+    """Blocks read up to 16 key-value heads side by side, the largest number that divides them; the other heads follow."""
+    cache, g = fp4.make_cache(moe, lens, kv, D, page, seed=kv + L)
+    fp4.fill(cache, g, lens)
+    q = (1.5 * randn(g, len(lens), L, kv * group, D)).to(BF)
+    out, lse = fp4.check_attend(cache, q, lens)
+    again = fp4.check_attend(cache, q, lens)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
