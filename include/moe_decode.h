@@ -119,6 +119,10 @@ MOE_API moe_status_t moe_kv_append(const moe_kv_cache_t* cache, const void* k_ne
  *            after another; calls that may overlap need one each.
  * The result does not depend on timing: the work is split over the length by a rule on the lengths alone and
  * joined in a fixed order.
+ * Scores, exponentials and sums are fp32, and lse holds every weight as it is.  For the product with v a weight is rounded
+ * once: to bf16 (eight bits at any size) over a bf16 or MXFP8 cache; over an MXFP4 cache to fp16 in units of the row's
+ * largest weight, to eleven bits down to 2^-20 of it and by up to 2^-31 of it below: weights under 2^-31 add nothing to out.
+ * (It shows where nearly all weight lies on tokens whose values are close to zero.)
  */
 #define MOE_ATTENTION_COUNTER_BYTES 4096
 typedef struct {

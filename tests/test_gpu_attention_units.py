@@ -63,3 +63,26 @@ def test_heads_in_groups(moe, lens, kv, group, L, D, page):  # noqa: F811
     out, lse = fp4.check_attend(cache, q, lens)
     again = fp4.check_attend(cache, q, lens)
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("D,group,L", [(128, 4, 1), (64, 8, 4)])
+@pytest.mark.parametrize("gap", [8, 15, 19, 22, 27, 33])
+def test_weights_far_below_the_largest(moe, D, group, L, gap):  # noqa: F811
+    """One token, whose values are zeros, takes nearly all weight; the others hold 2^-gap of it each.  fp16 keeps eleven bits of
+    them down to a gap of 20 and an error of 2^-31 of the largest below; lse keeps them all."""
+    n, kv = 3000, 2
+    cache, g = fp4.make_cache(moe, [n], kv, D, 64, seed=gap)
+    k, v = 0.25 * randn(g, 1, n, kv, D), randn(g, 1, n, kv, D).abs()
+    k[..., 0], v[:, 100] = 0, 0
+    k[:, 100] = 0
+    k[:, 100, :, 0] = 4.0
+    cache.append(k.to(BF), v.to(BF))
+    q = 0.25 * randn(g, 1, L, kv * group, D)
+    q[..., 0] = gap * 0.6931 / (4.0 * D ** -0.5)
+    q = q.to(BF)
+    out, _ = fp4.check_attend(cache, q, [n])
+    if gap <= 19:  # of sums of positive values nothing but roundings is lost: 2^-8 of out, 2^-11 of a weight, 2^-9 for scores
+        ref = fp4.reference(cache, q, [n], D ** -0.5)[0]
+        assert torch.all((out.double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -9) * ref)
+    if gap == 33:
+        assert torch.all(out.abs() <= 3000 * 2.0 ** -31 * 4)
