@@ -52,3 +52,23 @@ def test_heads_that_are_not_finite_keep_to_themselves(moe):  # noqa: F811
     want[0, 1], want[1, 2], want[1, 3] = float("nan"), 0, 0
     want[1, 2, 9] = want[1, 3, 0] = float("nan")
     assert torch.equal(torch.isnan(y), torch.isnan(want)) and torch.equal(y.nan_to_num(), want.nan_to_num())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8", "mxfp4"])
+def test_on_another_stream(moe, fmt):  # noqa: F811
+    """Outputs of a call on a stream of its own, read after that stream: what the call gives on the current one, bit for bit."""
+    lens, L, kv, D = [200, 3, 50], 2, 2, 128
+    cache, g = make(moe, fmt, lens, kv, D, 16, seed=4)
+    other = make(moe, fmt, lens, kv, D, 16, seed=4)[0]
+    q, k, v = randn(g, len(lens), L, 8, D).to(BF).split((4, 2, 2), dim=2)
+    plan, w = moe.RotaryPlan(freqs(D), device=DEV), torch.ones(D, device=DEV)
+    want = cache.append_rotated(q, k, v, plan, None, w, w)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = [other.append_rotated(q, k, v, plan, None, w, w, stream=side)]
+    got += moe.moe_head_norm_rope(q, k, plan, (other.seq_lens[:, None] - L + torch.arange(L, device=DEV)).int(), w, w)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want) and torch.equal(got[1], want)
+    for n in ("k", "v") + (("k_scales", "v_scales") if fmt != "bf16" else ()):
+        assert torch.equal(getattr(other, n).view(torch.uint8), getattr(cache, n).view(torch.uint8))
