@@ -207,15 +207,13 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
   float* s_l = reinterpret_cast<float*>(s_fr + kWarps * C::kRows);           // [warp][row]
   int* s_lim = reinterpret_cast<int*>(s_l + kWarps * C::kRows);              // [row] first position the row does not see
   __shared__ int s_last;
-  // What a unit keeps in shared memory, and what stands between its last read and the next unit's write (every unit passes a
-  // barrier in begin_unit and at least one in end_unit):
-  //   s_q, s_lim, s_fr.x  read with the scores, before end_unit's barriers; written before begin_unit's
-  //   s_fr.y, s_l, s_o    read behind end_unit's last barrier; written behind begin_unit's
-  //   s_unit              read until write_rows; written behind begin_unit's barrier
-  //   s_row               read in write_rows, behind end_unit's last barrier, and written before begin_unit's: it has two
-  //                       buffers that take turns, so that a warp still writing rows keeps its unit's places
-  __shared__ int4 s_unit;  // request, head, row tile, and which buffer of s_row
-  __shared__ int2 s_row[2][C::kRows];  // a row's token (request, new token) of the call and its query head; token -1: no such row
+  // What a unit keeps in shared memory is ordered by barriers:
+  //   s_q, s_lim, s_fr.x, s_row  written between begin_unit's two barriers; read until the next unit's first one (s_row last, by
+  //                              write_rows, behind end_unit's barriers)
+  //   s_fr.y, s_unit             written behind begin_unit's second barrier; read until the next unit's first one
+  //   s_l, s_o                   written and read in end_unit, with a barrier between
+  __shared__ int3 s_unit;           // request, head, row tile
+  __shared__ int2 s_row[C::kRows];  // a row's token (request, new token) of the call and its query head; token -1: no such row
   __shared__ uint4 s_loader[C::kFar ? 3 * kThreads : 1];
   __shared__ float2 s_sums[C::kFar ? RT * kThreads : 1];
   __shared__ uint32_t s_odd[kWarps][C::kStages];  // tokens whose V has a scale that fp16 does not hold
@@ -239,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
   {
     Run run;
     if (!deal_run<kTile, kCost>(p, head_groups, groups, g, tid, run)) return;
-    if (tid == 0) s_t0 = run.t0, s_t1 = run.t1, s_per = run.per, s_unit.w = 0;
+    if (tid == 0) s_t0 = run.t0, s_t1 = run.t1, s_per = run.per;
     __syncthreads();
     cur = run.cur;
     left = (int)(run.t1 - run.pos);
@@ -440,11 +438,13 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
         lim[it] = cur.len;  // rows that the tile does not have: their scores are 0 and their results nobody's
       }
     }
-    const int buffer = s_unit.w ^ 1;
     seen_end = cur.len - p.L + 1 + (min(row0 + C::kRows, p.rows) - 1) / p.group;
     if constexpr (!C::kFar) {
       if (stage < 0) load_first();  // behind the run's first rows of q: one wait serves both
     }
+    // The last unit's rows have been written: their places in s_row may go.  (Two buffers of s_row that take turns, without this
+    // barrier, cost more: 64 x 8 rows 92.1 us for 90.6.)
+    __syncthreads();
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
       const int i = it * kThreads + tid, rr = i / kVec, c8 = i % kVec;
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
         *reinterpret_cast<uint32_t*>(dst + 32) = h[2];
         *reinterpret_cast<uint32_t*>(dst + 48) = h[3];
         if (c8 == 0) {
-          s_row[buffer][rr] = place[it];
+          s_row[rr] = place[it];
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) s_fr[w * C::kRows + rr].x = factor;
           s_lim[rr] = lim[it];
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
     }
     for (int i = lane; i < C::kRows; i += 32) s_fr[warp * C::kRows + i].y = 0.f;
     __syncwarp();
-    if (tid == 0) s_unit = make_int4(cur.b, cur.head, cur.rt, buffer);  // read again at the unit's end
+    if (tid == 0) s_unit = make_int3(cur.b, cur.head, cur.rt);  // read again at the unit's end
     unseen = (1u << (2 * RT)) - 1u;
     open = true;
   };
@@ -797,12 +797,11 @@ __global__ void __launch_bounds__(kThreads, Cfg4<D, RT>::kBlocks) paged_attentio
     const int64_t first_tile = unit_first + kCost, unit_end = first_tile + tiles_of<kTile>(cur.len);
     const int64_t t0 = s_t0, t1 = s_t1, per = s_per;
     auto write_rows = [&]() {
-      const int2* rows = s_row[s_unit.w];
 #pragma unroll
       for (int a = 0; a < RT; ++a)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int2 row = rows[a * 8 + 2 * lc + e];
+          const int2 row = s_row[a * 8 + 2 * lc + e];
           if (row.x < 0) continue;
           const float z = jl[a][e];
           const float inv = z == 0.f ? 0.f : __fdividef(1.f / (float)(1 << kVUp), z);  // a row that sees nothing is 0
