@@ -5,7 +5,7 @@
 // A token of a head is 136 bytes (D = 128), so instructions and their latencies at eight to twelve warps an SM bound it, not
 // memory.  64 requests of 100 to 8000 tokens, 8 x 4 heads of 128: one row 41 us (floor 19; 3.1 TB/s), eight rows 90 us (floor
 // 20; the products alone 26 on mma.sync); three requests of up to 131,071 tokens 65 us (floor 36, 3.8 TB/s); one request of
-// 333 tokens 9 us; two prompts of 500 tokens over up to 3001, 4 x 4 heads of 64, 61 us (135 TFLOP/s).  Of the 90 us about 15
+// 333 tokens 9 us; two prompts of 500 tokens over up to 3001, 4 x 4 heads of 64, 60.5 us (136 TFLOP/s).  Of the 90 us about 15
 // are units' beginnings and ends (two or three to a block), 6 dealing and the first loads, the rest 2,500 cycles a tile, of
 // which the softmax's chain of dependent instructions is 900 and a fifth of the instructions the loader's.  What follows:
 //  * The products are transposed, S^T = K q^T and O^T = V^T P^T: the 16-row side of a product holds tokens or columns, the
