@@ -193,7 +193,8 @@ MOE_API moe_status_t moe_head_norm_rope(const moe_kv_cache_t* cache, const moe_h
  *   status       device int32 or NULL: sticky bits as in moe_kv_cache_t, and MOE_POOL_EXHAUSTED (a growth that the free
  *                pages do not cover, which is not made) and MOE_POOL_BAD_REQUEST (a fork that is not allowed, not made).
  * n_seqs up to MOE_POOL_MAX_SEQS.  The calls change the tables in place, asynchronously, by rules on their contents alone:
- * the same tables give the same pages.  A page index outside [0, n_pages) in a used entry is reported and left alone.
+ * the same tables give the same pages.  A page index outside [0, n_pages) in a used entry is reported and no count of it is
+ * touched (a request that gives the entry back has -1 there, as for any page).
  *
  * moe_pages_fork: request dst[i] becomes a branch of request src[i]: it holds the same pages (their counts grow) and has the
  *   same length, as it stood before the call.  dst[i] must have length 0, and only the first of several pairs with the
